@@ -8,6 +8,10 @@ hold device memory and to name the current HIP stream.
 import ctypes
 import os
 
+from . import mx4 as _mx4
+from .mx4 import Mx4, mx4_dequantize, mx4_gemm, mx4_quantize, mx4_quantize_both  # noqa: F401
+from .mx4 import mx4_train_backward, mx4_train_forward  # noqa: F401
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # The in-tree build; SGEMM_F32_LIBRARY may name another build of the same sources.
 LIB_PATH = os.environ.get("SGEMM_F32_LIBRARY") or os.path.join(_HERE, "libsgemm_f32.so")
@@ -161,6 +165,7 @@ def library():
     lib.sgemm_f32_gemm_plan.argtypes = [i, i, i, i, i, i, i, i, ctypes.POINTER(i), i, ctypes.POINTER(_Plan)]
     lib.sgemm_f32_release.restype = i
     lib.sgemm_f32_release.argtypes = []
+    _mx4._bind(lib)
     _lib = lib
     return lib
 

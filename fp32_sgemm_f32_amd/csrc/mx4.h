@@ -1,0 +1,117 @@
+// The microscaled 4-bit format (MXFP4) and what its kernels share.
+//
+// A matrix of R rows and K columns is held in blocks of 32 values along a
+// row: 4-bit codes (sign, then the index into 0, 0.5, 1, 1.5, 2, 3, 4, 6) and
+// one scale byte s per block, standing for 2^(s - 127); s = 255 makes the
+// block NaN.  Kp = K rounded up to 128 (a slab: four blocks).
+//   codes   R rows of Kp / 2 bytes, the even column in the low four bits
+//   scales  Kp / 128 planes (one per slab) of Rp = R rounded up to 32 words;
+//           byte b of a row's word is the scale of block b of the slab
+// Codes beyond K and scales beyond K and R are zeros.  So every row of codes
+// starts on a 64-byte boundary, a tile needs no mask along K, and the scales
+// of neighbouring rows lie side by side, as the tiles read them.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sgemm_f32.h"
+
+namespace sgemm {
+
+constexpr int kMxSlab = 128;      // columns of a slab
+constexpr int kMxSlabBytes = 64;  // bytes of its codes in a row
+
+inline __host__ __device__ int mx_slabs(int cols) { return (int)(((int64_t)cols + kMxSlab - 1) / kMxSlab); }
+inline __host__ __device__ int64_t mx_plane_rows(int64_t rows) { return (rows + 31) / 32 * 32; }
+
+typedef float f32v4 __attribute__((ext_vector_type(4)));
+typedef float f32v16 __attribute__((ext_vector_type(16)));
+typedef int i32v4 __attribute__((ext_vector_type(4)));
+typedef int i32v8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16v2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16v8 __attribute__((ext_vector_type(8)));
+
+template <int TYPE>
+struct MxType;
+template <>
+struct MxType<SGEMM_TYPE_F32> {
+    typedef float T;
+    static __device__ __forceinline__ float load(const T *p) { return *p; }
+    static __device__ __forceinline__ T from(float v) { return v; }
+};
+template <>
+struct MxType<SGEMM_TYPE_BF16> {
+    typedef uint16_t T;
+    static __device__ __forceinline__ float load(const T *p) { return __uint_as_float((uint32_t)*p << 16); }
+    // Round to nearest, ties to even (NaN stays NaN).
+    static __device__ __forceinline__ T from(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+};
+template <>
+struct MxType<SGEMM_TYPE_F16> {
+    typedef uint16_t T;
+    static __device__ __forceinline__ float load(const T *p) { return (float)__builtin_bit_cast(_Float16, *p); }
+    static __device__ __forceinline__ T from(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+};
+
+// Eight adjacent values as floats, from a 16-byte aligned pointer.
+template <int TYPE>
+__device__ __forceinline__ void mx_load8(const typename MxType<TYPE>::T *p, float (&v)[8]) {
+    if constexpr (TYPE == SGEMM_TYPE_F32) {
+        const f32v4 a = ((const f32v4 *)p)[0], b = ((const f32v4 *)p)[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+    } else {
+        const uint4 u = *(const uint4 *)p;
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint16_t lo = (uint16_t)w[i], hi = (uint16_t)(w[i] >> 16);
+            v[2 * i] = MxType<TYPE>::load(&lo);
+            v[2 * i + 1] = MxType<TYPE>::load(&hi);
+        }
+    }
+}
+
+template <int TYPE>
+__device__ __forceinline__ void mx_store8(typename MxType<TYPE>::T *p, const float (&v)[8]) {
+    if constexpr (TYPE == SGEMM_TYPE_F32) {
+        ((f32v4 *)p)[0] = f32v4{v[0], v[1], v[2], v[3]};
+        ((f32v4 *)p)[1] = f32v4{v[4], v[5], v[6], v[7]};
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (uint32_t)MxType<TYPE>::from(v[2 * i]) | (uint32_t)MxType<TYPE>::from(v[2 * i + 1]) << 16;
+        *(uint4 *)p = uint4{w[0], w[1], w[2], w[3]};
+    }
+}
+
+// ---- host: one job per launcher ----
+
+struct MxQuantJob {
+    const void *x;
+    int64_t ldx;
+    int rows, cols, type, noclip;
+    uint8_t *codes, *scales;        // along the rows; NULL: not wanted
+    uint8_t *codes_t, *scales_t;    // of the transposed matrix; NULL: not wanted
+};
+struct MxDequantJob {
+    const uint8_t *codes, *scales;
+    int rows, cols, type;
+    void *y;
+    int64_t ldy;
+};
+struct MxGemmJob {
+    const uint8_t *a, *sa, *b, *sb;
+    int M, N, K, type;
+    float alpha, beta;
+    void *c;
+    int64_t ldc;
+};
+
+hipError_t launch_mx4_quantize(const MxQuantJob &j, hipStream_t s);
+hipError_t launch_mx4_dequantize(const MxDequantJob &j, hipStream_t s);
+hipError_t launch_mx4_gemm(const MxGemmJob &j, int num_cus, hipStream_t s);
+
+}  // namespace sgemm

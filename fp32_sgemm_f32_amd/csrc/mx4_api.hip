@@ -1,0 +1,130 @@
+// C entry points of the 4-bit operators (declared in include/sgemm_f32.h):
+// argument checks, then one launcher each.
+#include <hip/hip_runtime_api.h>
+
+#include <atomic>
+
+#include "abi.h"
+#include "mx4.h"
+
+#define SGEMM_API extern "C" __attribute__((visibility("default")))
+
+namespace sgemm {
+namespace {
+
+int type_bytes(int type) { return type == SGEMM_TYPE_F32 ? 4 : 2; }
+bool known_type(int type) { return type >= SGEMM_TYPE_F32 && type <= SGEMM_TYPE_F16; }
+bool dim_ok(int n) { return n >= 0 && n <= SGEMM_MX4_MAX_DIM; }
+
+int64_t codes_bytes(int rows, int cols) { return (int64_t)rows * mx_slabs(cols) * kMxSlabBytes; }
+int64_t scales_bytes(int rows, int cols) { return mx_plane_rows(rows) * 4 * mx_slabs(cols); }
+
+// One array of a call, in the order of the checks.
+struct Span {
+    const void *p;
+    int64_t bytes;
+    int align;
+    bool out;
+};
+
+Span floats(const void *p, int64_t rows, int64_t cols, int64_t ld, int type, bool out) {
+    return Span{p, rows > 0 && cols > 0 ? ((rows - 1) * ld + cols) * type_bytes(type) : 0, type_bytes(type), out};
+}
+Span codes(const void *p, int rows, int cols, bool out) { return Span{p, codes_bytes(rows, cols), 16, out}; }
+Span scales(const void *p, int rows, int cols, bool out) { return Span{p, scales_bytes(rows, cols), 4, out}; }
+
+// Null, alignment, overlap with an output, and device memory, of all arrays
+// that hold anything.
+template <int N>
+int check_spans(const Span (&s)[N], int *dev) {
+    for (const Span &x : s)
+        if (x.bytes > 0 && !x.p) return SGEMM_ERR_NULL;
+    for (const Span &x : s)
+        if (x.bytes > 0 && ((uintptr_t)x.p & (x.align - 1))) return SGEMM_ERR_ALIGN;
+    for (int i = 0; i < N; ++i)
+        for (int k = 0; k < N; ++k) {
+            if (i == k || !s[i].out || s[i].bytes <= 0 || s[k].bytes <= 0) continue;
+            const uintptr_t a = (uintptr_t)s[i].p, b = (uintptr_t)s[k].p;
+            if (a < b + (uint64_t)s[k].bytes && b < a + (uint64_t)s[i].bytes) return SGEMM_ERR_ALIAS;
+        }
+    const hipError_t e = hipGetDevice(dev);
+    if (e != hipSuccess) return hip_fail(e);
+    for (const Span &x : s) {
+        const int st = check_device_range(x.p, x.bytes, *dev);
+        if (st != SGEMM_OK) return st;
+    }
+    return SGEMM_OK;
+}
+
+int done(hipError_t e) { return e == hipSuccess ? SGEMM_OK : hip_fail(e); }
+
+// Compute units of a device, asked for once.
+int compute_units(int dev, int *out) {
+    static std::atomic<int> known[64];
+    if (dev >= 0 && dev < 64 && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return SGEMM_OK;
+    const hipError_t e = hipDeviceGetAttribute(out, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess) return hip_fail(e);
+    if (dev >= 0 && dev < 64) known[dev].store(*out, std::memory_order_relaxed);
+    return SGEMM_OK;
+}
+
+}  // namespace
+}  // namespace sgemm
+
+using namespace sgemm;
+
+SGEMM_API int sgemm_f32_mx4_bytes(int rows, int cols, long long *codes_out, long long *scales_out) {
+    if (!dim_ok(rows) || !dim_ok(cols)) return SGEMM_ERR_SHAPE;
+    if (codes_out) *codes_out = codes_bytes(rows, cols);
+    if (scales_out) *scales_out = scales_bytes(rows, cols);
+    return SGEMM_OK;
+}
+
+SGEMM_API int sgemm_f32_mx4_quantize(int rows, int cols, int type, const void *X, int ldx, int rule, void *c, void *s,
+                                     void *ct, void *st, hipStream_t stream) {
+    if (!dim_ok(rows) || !dim_ok(cols)) return SGEMM_ERR_SHAPE;
+    if (!known_type(type) || (rule != SGEMM_MX4_SCALE_FLOOR && rule != SGEMM_MX4_SCALE_NOCLIP)) return SGEMM_ERR_CONFIG;
+    if (rows == 0 || cols == 0) return SGEMM_OK;
+    if (ldx < cols) return SGEMM_ERR_LD;
+    const bool along = c || s, down = ct || st;
+    if (!along && !down) return SGEMM_ERR_NULL;
+    const Span spans[] = {floats(X, rows, cols, ldx, type, false),
+                          codes(c, along ? rows : 0, cols, true), scales(s, along ? rows : 0, cols, true),
+                          codes(ct, down ? cols : 0, rows, true), scales(st, down ? cols : 0, rows, true)};
+    int dev = 0;
+    const int status = check_spans(spans, &dev);
+    if (status != SGEMM_OK) return status;
+    return done(launch_mx4_quantize({X, ldx, rows, cols, type, rule == SGEMM_MX4_SCALE_NOCLIP, (uint8_t *)c, (uint8_t *)s,
+                                     (uint8_t *)ct, (uint8_t *)st}, stream));
+}
+
+SGEMM_API int sgemm_f32_mx4_dequantize(int rows, int cols, const void *c, const void *s, int type, void *Y, int ldy,
+                                       hipStream_t stream) {
+    if (!dim_ok(rows) || !dim_ok(cols)) return SGEMM_ERR_SHAPE;
+    if (!known_type(type)) return SGEMM_ERR_CONFIG;
+    if (rows == 0 || cols == 0) return SGEMM_OK;
+    if (ldy < cols) return SGEMM_ERR_LD;
+    const Span spans[] = {codes(c, rows, cols, false), scales(s, rows, cols, false),
+                          floats(Y, rows, cols, ldy, type, true)};
+    int dev = 0;
+    const int status = check_spans(spans, &dev);
+    if (status != SGEMM_OK) return status;
+    return done(launch_mx4_dequantize({(const uint8_t *)c, (const uint8_t *)s, rows, cols, type, Y, ldy}, stream));
+}
+
+SGEMM_API int sgemm_f32_mx4_gemm(int M, int N, int K, float alpha, const void *a, const void *sa, const void *b,
+                                 const void *sb, float beta, int type, void *C, int ldc, hipStream_t stream) {
+    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return SGEMM_ERR_SHAPE;
+    if (!known_type(type)) return SGEMM_ERR_CONFIG;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    if (ldc < N) return SGEMM_ERR_LD;
+    const int k = alpha == 0.0f ? 0 : K;   // nothing of A and B is read then
+    const Span spans[] = {codes(a, M, k, false), scales(sa, M, k, false), codes(b, N, k, false),
+                          scales(sb, N, k, false), floats(C, M, N, ldc, type, true)};
+    int dev = 0, cus = 0;
+    int status = check_spans(spans, &dev);
+    if (status == SGEMM_OK) status = compute_units(dev, &cus);
+    if (status != SGEMM_OK) return status;
+    return done(launch_mx4_gemm({(const uint8_t *)a, (const uint8_t *)sa, (const uint8_t *)b, (const uint8_t *)sb, M, N, k,
+                                 type, alpha, beta, C, ldc}, cus, stream));
+}

@@ -1,0 +1,353 @@
+// C = alpha A B^T + beta C for two matrices in the microscaled 4-bit format
+// (A: M x K, B: N x K), sums in fp32, on the scaled matrix instruction
+// v_mfma_scale_f32_32x32x64_f8f6f4: one lane's operand is 32 codes of a row,
+// one block of the format, and its scale is one byte of a register, so a
+// block's scale costs no arithmetic.
+//
+// A workgroup computes a BM x BN tile.  The codes and the scale words of a
+// K chunk (BK columns) go from global memory straight into LDS, through a
+// ring of S stages; the buffer resources end where the matrix does, so rows
+// beyond it read as zeros and no mask is needed (K is padded with zeros in
+// the format itself).
+//
+// LDS of a stage: A's rows (BK / 2 bytes each), B's rows, A's scale words,
+// B's scale words (slab by slab).  A row's 16-byte quad q (one block) is kept
+// at quad q ^ swz(row), so that the 32 rows of an operand read fall on
+// different banks.  B's rows are kept in the order that gives a lane FN
+// adjacent columns of C (fragment f holds columns FN l + f), which makes the
+// stores FN values wide.
+//
+// K order: matrix step j of a chunk multiplies the blocks 2j (lanes 0-31) and
+// 2j + 1 (lanes 32-63).  The scale word of a slab is shifted by one byte for
+// the upper lanes, after which byte 0 serves the slab's first step and byte 2
+// its second.
+//
+// Ring: during the last step of chunk c, whose operands are in registers by
+// then, the waves meet once (loads of chunk c + 1 landed, LDS reads of chunk
+// c done), read the first operands of chunk c + 1, and load chunk c + S into
+// the stage of chunk c.
+#include <type_traits>
+
+#include "mx4.h"
+
+namespace sgemm {
+namespace {
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// 16 (4) bytes per lane from the resource's base + voff into LDS at
+// m0 + 16 (4) * lane; lanes out of the resource's range leave zeros.
+__device__ __forceinline__ void dma16(i32v4 rsrc, uint32_t voff, uint32_t m0v) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "s"(m0v)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(i32v4 rsrc, uint32_t voff, uint32_t m0v) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "s"(m0v)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// At most VM of this wave's loads still in flight, its LDS reads done, and
+// every wave of the workgroup here.
+template <int VM>
+__device__ __forceinline__ void meet() {
+    static_assert(VM >= 0 && VM < 64, "vmcnt range");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
+}
+
+__device__ __forceinline__ i32v4 resource(const void *p, int64_t bytes) {
+    const uint64_t a = (uint64_t)p;
+    return i32v4{(int)(uint32_t)a, (int)(uint32_t)(a >> 32), (int)(uint32_t)(bytes > 0 ? bytes : 0), 0x00020000};
+}
+__device__ __forceinline__ void advance(i32v4 &r, int64_t bytes) {
+    const uint64_t a = (((uint64_t)(uint32_t)r[1] << 32) | (uint32_t)r[0]) + (uint64_t)bytes;
+    r[0] = (int)(uint32_t)a;
+    r[1] = (int)(uint32_t)(a >> 32);
+}
+
+struct Args {
+    const uint8_t *a, *sa, *b, *sb;
+    void *c;
+    int64_t ldc;
+    int M, N, slabs;
+    int tiles_m, tiles_n;
+    float alpha, beta;
+};
+
+template <int F, class T>
+struct __attribute__((packed, aligned(sizeof(T) * F))) Vec {
+    T v[F];
+};
+
+template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, S = S_;
+    static constexpr int NW = WM * WN, NT = 64 * NW;
+    static constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
+    static constexpr int ROWB = BK / 2, QPR = ROWB / 16;     // bytes and quads of a row in a stage
+    static constexpr int STEPS = BK / 64, SLABS = BK / kMxSlab;
+    static constexpr int A_BYTES = BM * ROWB, B_BYTES = BN * ROWB;
+    static constexpr int W_BYTES = (BM + BN) * 4 * SLABS;    // scale words
+    static constexpr int STAGE = A_BYTES + B_BYTES + W_BYTES;
+    static constexpr int A_PW = A_BYTES / 1024 / NW, B_PW = B_BYTES / 1024 / NW, W_PW = W_BYTES / 256 / NW;
+    static constexpr int L = A_PW + B_PW + W_PW;             // loads of a wave per chunk
+    static_assert(A_PW * NW * 1024 == A_BYTES && B_PW * NW * 1024 == B_BYTES && W_PW * NW * 256 == W_BYTES,
+                  "a chunk's loads split evenly over the waves");
+    static_assert(S * STAGE <= 160 * 1024 && (S - 2) * L < 64 && S >= 3, "LDS and vmcnt budget");
+    static_assert(BM % 64 == 0 && BN % 64 == 0, "a scale load covers 64 rows of one operand");
+
+    __device__ __forceinline__ static int swz(int r) { return QPR == 4 ? (r >> 2) & 3 : (r ^ (r >> 3)) & 7; }
+    // Column of the tile that B's LDS row r holds.
+    __device__ __forceinline__ static int b_col(int r) { return r / WTN * WTN + FN * (r % 32) + r % WTN / 32; }
+};
+
+template <class TL, int TYPE>
+__global__ __launch_bounds__(TL::NT, 1) void mx4_gemm_kernel(Args g) {
+    typedef typename MxType<TYPE>::T T;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / TL::WN, wn = wave % TL::WN;
+
+    // Workgroup -> tile: each XCD (workgroups w, w + 8, ...) takes a
+    // contiguous run of tiles, which go down columns of 8-row groups.
+    int tm, tn;
+    {
+        const int tiles = g.tiles_m * g.tiles_n, per = tiles >> 3, rest = tiles & 7;
+        const int x = blockIdx.x & 7, y = blockIdx.x >> 3;
+        const int t = x * per + (x < rest ? x : rest) + y;
+        const int group = 8 * g.tiles_n, gi = t / group, first = gi * 8;
+        const int rows = g.tiles_m - first < 8 ? g.tiles_m - first : 8;
+        tm = first + (t - gi * group) % rows;
+        tn = (t - gi * group) / rows;
+    }
+    const int m0 = tm * TL::BM, n0 = tn * TL::BN;
+    const int64_t rowb = (int64_t)g.slabs * kMxSlabBytes;
+    const int64_t plane_a = mx_plane_rows(g.M) * 4, plane_b = mx_plane_rows(g.N) * 4;
+    const int chunks = (g.slabs + TL::SLABS - 1) / TL::SLABS;
+
+    // Sources of this wave's loads.  The resources end with the tile's last
+    // real row.  For BK = 256 a chunk may reach one slab past its rows' end
+    // (odd slab counts): load_chunk masks those lanes.
+    const int am = g.M - m0 < TL::BM ? g.M - m0 : TL::BM, bn = g.N - n0 < TL::BN ? g.N - n0 : TL::BN;
+    i32v4 ra = resource(g.a + m0 * rowb, am * rowb), rb = resource(g.b + n0 * rowb, bn * rowb);
+    i32v4 rsa = resource(g.sa + m0 * 4, 0), rsb = resource(g.sb + n0 * 4, 0);
+    uint32_t va[TL::A_PW], vb[TL::B_PW];
+    bool ua[TL::A_PW], ub[TL::B_PW];   // BK = 256: the lane's block lies in the chunk's second slab
+#pragma unroll
+    for (int i = 0; i < TL::A_PW; ++i) {
+        const int r = (wave * TL::A_PW + i) * (1024 / TL::ROWB) + lane / TL::QPR;
+        const int q = (lane % TL::QPR) ^ TL::swz(r);
+        va[i] = (uint32_t)(r * rowb) + 16 * q;
+        ua[i] = q >= 4;
+    }
+#pragma unroll
+    for (int i = 0; i < TL::B_PW; ++i) {
+        const int r = (wave * TL::B_PW + i) * (1024 / TL::ROWB) + lane / TL::QPR;
+        const int q = (lane % TL::QPR) ^ TL::swz(r);
+        vb[i] = (uint32_t)(TL::b_col(r) * rowb) + 16 * q;
+        ub[i] = q >= 4;
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
+
+    auto load_chunk = [&](int c, int stage) {
+        const uint32_t base = lds0 + stage * TL::STAGE;
+        // A slab past the row's end (BK = 256, odd slab counts): no lane loads it.
+        const bool half = TL::SLABS == 2 && 2 * c + 1 >= g.slabs;
+        const int64_t off = (int64_t)c * TL::ROWB;
+        i32v4 r = ra;
+        advance(r, off);
+        r[2] = am * rowb > off ? (int)(am * rowb - off) : 0;
+#pragma unroll
+        for (int i = 0; i < TL::A_PW; ++i) {
+            uint32_t v = va[i];
+            if constexpr (TL::SLABS == 2) v = half && ua[i] ? 0x80000000u : v;
+            dma16(r, v, base + (wave * TL::A_PW + i) * 1024);
+        }
+        r = rb;
+        advance(r, off);
+        r[2] = bn * rowb > off ? (int)(bn * rowb - off) : 0;
+#pragma unroll
+        for (int i = 0; i < TL::B_PW; ++i) {
+            uint32_t v = vb[i];
+            if constexpr (TL::SLABS == 2) v = half && ub[i] ? 0x80000000u : v;
+            dma16(r, v, base + TL::A_BYTES + (wave * TL::B_PW + i) * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < TL::W_PW; ++i) {
+            // Load w of the scale words: 64 rows of one operand in one slab.
+            const int w = wave * TL::W_PW + i;
+            constexpr int PER = (TL::BM + TL::BN) / 64;
+            const int slab = c * TL::SLABS + w / PER, u = w % PER;
+            const bool is_a = u < TL::BM / 64;
+            const int row = is_a ? u * 64 + lane : TL::b_col(u * 64 - TL::BM + lane);
+            i32v4 q = is_a ? rsa : rsb;
+            const int64_t plane = is_a ? plane_a : plane_b;
+            advance(q, slab * plane);
+            // (past the last slab: nothing)
+            q[2] = slab < g.slabs ? (int)(plane - (is_a ? m0 : n0) * 4) : 0;
+            dma4(q, row * 4, base + TL::A_BYTES + TL::B_BYTES + w * 256);
+        }
+    };
+
+    f32v16 acc[TL::FM][TL::FN];
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+        for (int k = 0; k < TL::FN; ++k)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][k][r] = 0.0f;
+
+    // Operand reads: lane l takes row l % 32 of a fragment, block 2 j + l / 32.
+    const int fr = lane & 31, h = lane >> 5;
+    struct Ops {
+        i32v4 a[TL::FM], b[TL::FN];
+    };
+    struct Words {
+        uint32_t a[TL::SLABS][TL::FM], b[TL::SLABS][TL::FN];
+    };
+    auto read_ops = [&](Ops &o, int stage, int j) {
+        const uint8_t *st = lds + stage * TL::STAGE;
+#pragma unroll
+        for (int i = 0; i < TL::FM; ++i) {
+            const int r = wm * TL::WTM + 32 * i + fr;
+            o.a[i] = *(const i32v4 *)(st + r * TL::ROWB + 16 * ((2 * j + h) ^ TL::swz(r)));
+        }
+#pragma unroll
+        for (int i = 0; i < TL::FN; ++i) {
+            const int r = wn * TL::WTN + 32 * i + fr;
+            o.b[i] = *(const i32v4 *)(st + TL::A_BYTES + r * TL::ROWB + 16 * ((2 * j + h) ^ TL::swz(r)));
+        }
+    };
+    auto read_words = [&](Words &w, int stage) {
+        const uint32_t *st = (const uint32_t *)(lds + stage * TL::STAGE + TL::A_BYTES + TL::B_BYTES);
+#pragma unroll
+        for (int s = 0; s < TL::SLABS; ++s) {
+#pragma unroll
+            for (int i = 0; i < TL::FM; ++i)
+                w.a[s][i] = st[s * (TL::BM + TL::BN) + wm * TL::WTM + 32 * i + fr] >> (8 * h);
+#pragma unroll
+            for (int i = 0; i < TL::FN; ++i)
+                w.b[s][i] = st[s * (TL::BM + TL::BN) + TL::BM + wn * TL::WTN + 32 * i + fr] >> (8 * h);
+        }
+    };
+    auto multiply = [&](const Ops &o, const Words &w, auto jc) {
+        constexpr int j = decltype(jc)::value;
+#pragma unroll
+        for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+            for (int k = 0; k < TL::FN; ++k) {
+                const i32v8 x = __builtin_shufflevector(o.a[i], o.a[i], 0, 1, 2, 3, -1, -1, -1, -1);
+                const i32v8 y = __builtin_shufflevector(o.b[k], o.b[k], 0, 1, 2, 3, -1, -1, -1, -1);
+                acc[i][k] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    x, y, acc[i][k], 4, 4, (j & 1) * 2, (int)w.a[j / 2][i], (j & 1) * 2, (int)w.b[j / 2][k]);
+            }
+    };
+
+    // Chunks 0 .. S-1 go out; from then on every iteration adds one.  Past
+    // the last chunk nothing is in range, but the loads are issued all the
+    // same (they leave zeros): the waits count them.
+#pragma unroll
+    for (int c = 0; c < TL::S; ++c) load_chunk(c, c);
+    meet<(TL::S - 1) * TL::L>();
+    Ops o0, o1;
+    Words w0, w1;
+    read_ops(o0, 0, 0);
+    read_words(w0, 0);
+    int stage = 0;
+    for (int c = 0; c < chunks; ++c) {
+        if constexpr (TL::STEPS == 4) {
+            read_ops(o1, stage, 1);
+            multiply(o0, w0, std::integral_constant<int, 0>{});
+            read_ops(o0, stage, 2);
+            multiply(o1, w0, std::integral_constant<int, 1>{});
+            read_ops(o1, stage, 3);
+            multiply(o0, w0, std::integral_constant<int, 2>{});
+        } else {
+            read_ops(o1, stage, 1);
+            multiply(o0, w0, std::integral_constant<int, 0>{});
+        }
+        meet<(TL::S - 2) * TL::L>();
+        const int next = stage + 1 == TL::S ? 0 : stage + 1;
+        read_ops(o0, next, 0);
+        read_words(w1, next);
+        load_chunk(c + TL::S, stage);
+        if constexpr (TL::STEPS == 4) multiply(o1, w0, std::integral_constant<int, 3>{});
+        else multiply(o1, w0, std::integral_constant<int, 1>{});
+        w0 = w1;
+        stage = next;
+    }
+    // Loads still in flight write this workgroup's LDS: let them land.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+
+    // Lane l holds columns FN (l % 32) + 0 .. FN-1 of its wave's tile, rows
+    // 8 (r / 4) + 4 (l / 32) + r % 4 of each fragment.
+    const int col = n0 + wn * TL::WTN + TL::FN * fr;
+    const bool wide = col + TL::FN <= g.N && (g.ldc % TL::FN) == 0 && ((uintptr_t)g.c % (TL::FN * sizeof(T))) == 0;
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = m0 + wm * TL::WTM + 32 * i + 8 * (r / 4) + 4 * h + r % 4;
+            if (row >= g.M) continue;
+            T *p = (T *)g.c + row * g.ldc + col;
+            if (wide) {
+                Vec<TL::FN, T> out;
+                if (g.beta != 0.0f) {
+                    const Vec<TL::FN, T> old = *(const Vec<TL::FN, T> *)p;
+#pragma unroll
+                    for (int k = 0; k < TL::FN; ++k)
+                        out.v[k] = MxType<TYPE>::from(g.alpha * acc[i][k][r] + g.beta * MxType<TYPE>::load(&old.v[k]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < TL::FN; ++k) out.v[k] = MxType<TYPE>::from(g.alpha * acc[i][k][r]);
+                }
+                *(Vec<TL::FN, T> *)p = out;
+            } else {
+#pragma unroll
+                for (int k = 0; k < TL::FN; ++k)
+                    if (col + k < g.N) {
+                        float v = g.alpha * acc[i][k][r];
+                        if (g.beta != 0.0f) v += g.beta * MxType<TYPE>::load(p + k);
+                        p[k] = MxType<TYPE>::from(v);
+                    }
+            }
+        }
+}
+
+typedef Tile<256, 256, 128, 2, 4, 4> T256;   // 8 waves of 128 x 64, 136 KiB
+typedef Tile<128, 128, 128, 2, 2, 4> T128;   // 4 waves of 64 x 64, 68 KiB
+typedef Tile<64, 64, 256, 2, 2, 4> T64;      // 4 waves of 32 x 32, 68 KiB
+
+template <class TL, int TYPE>
+hipError_t launch_tile(const MxGemmJob &j, hipStream_t s) {
+    Args g{j.a, j.sa, j.b, j.sb, j.c, j.ldc, j.M, j.N, mx_slabs(j.K), (int)(((int64_t)j.M + TL::BM - 1) / TL::BM),
+           (int)(((int64_t)j.N + TL::BN - 1) / TL::BN), j.alpha, j.beta};
+    const void *k = (const void *)mx4_gemm_kernel<TL, TYPE>;
+    const int bytes = TL::S * TL::STAGE;
+    hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    void *params[] = {&g};
+    return hipLaunchKernel(k, dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(TL::NT), params, bytes, s);
+}
+
+template <int TYPE>
+hipError_t launch_type(const MxGemmJob &j, int num_cus, hipStream_t s) {
+    const auto tiles = [&](int b) { return (((int64_t)j.M + b - 1) / b) * (((int64_t)j.N + b - 1) / b); };
+    if (tiles(256) >= num_cus) return launch_tile<T256, TYPE>(j, s);
+    if (tiles(128) >= num_cus) return launch_tile<T128, TYPE>(j, s);
+    return launch_tile<T64, TYPE>(j, s);
+}
+
+}  // namespace
+
+hipError_t launch_mx4_gemm(const MxGemmJob &j, int num_cus, hipStream_t s) {
+    switch (j.type) {
+    case SGEMM_TYPE_F32: return launch_type<SGEMM_TYPE_F32>(j, num_cus, s);
+    case SGEMM_TYPE_BF16: return launch_type<SGEMM_TYPE_BF16>(j, num_cus, s);
+    case SGEMM_TYPE_F16: return launch_type<SGEMM_TYPE_F16>(j, num_cus, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace sgemm

@@ -9,6 +9,7 @@
 #include <mutex>
 #include <utility>
 
+#include "abi.h"
 #include "gemm_common.h"
 #include "kernels.h"
 #include "plan.h"
@@ -20,11 +21,6 @@ namespace sgemm {
 namespace {
 
 thread_local int g_last_hip_error = 0;
-
-int hip_fail(hipError_t e) {
-    g_last_hip_error = (int)e;
-    return SGEMM_ERR_HIP;
-}
 
 struct DeviceInfo {
     bool ready = false;
@@ -53,6 +49,15 @@ std::map<std::pair<int, hipStream_t>, Workspace> g_workspaces;
 constexpr int64_t kScratchBytes = SGEMM_F32_NOALLOC_SCRATCH_BYTES;
 static __device__ __align__(256) char scratch[kScratchBytes];
 std::map<int, char *> g_scratch;   // device -> address of its copy of `scratch`
+
+}  // namespace
+
+int hip_fail(hipError_t e) {
+    g_last_hip_error = (int)e;
+    return SGEMM_ERR_HIP;
+}
+
+namespace {
 
 hipError_t launch_cfg(int cfg, const KernelArgs &a, hipStream_t s, int trans_c = 0) {
     switch (kCfgs[cfg].kind) {
@@ -120,6 +125,8 @@ int scratch_of(int dev, char **out) {
     return SGEMM_OK;
 }
 
+}  // namespace
+
 // A device pointer of the current device whose allocation holds `bytes`
 // bytes from p on.
 int check_device_range(const void *p, int64_t bytes, int dev) {
@@ -142,6 +149,8 @@ int check_device_range(const void *p, int64_t bytes, int dev) {
     if (q < lo || q + (uint64_t)bytes > hi) return SGEMM_ERR_POINTER;
     return SGEMM_OK;
 }
+
+namespace {
 
 // Bytes spanned by a row-major rows x cols matrix with leading dimension ld.
 int64_t extent_bytes(int rows, int cols, int ld) {

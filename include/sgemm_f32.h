@@ -358,6 +358,77 @@ int sgemm_f32_gemm_plan(int trans_a, int trans_b, int M, int N, int K, int confi
  */
 int sgemm_f32_release(void);
 
+/*
+ * Microscaled 4-bit matrices (MXFP4).
+ *
+ * A matrix of `rows` x `cols` values is held in blocks of 32 values along a
+ * row: a 4-bit code each (sign, then the index into 0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6) and one scale byte s for the block, standing for 2^(s - 127); s = 255
+ * makes the whole block NaN.  With kp = cols rounded up to 128 and rp = rows
+ * rounded up to 32, it is two device arrays:
+ *   codes   rows x kp / 2 bytes: column k of a row in its byte k / 2, even k
+ *           in the low four bits; zeros beyond cols
+ *   scales  kp / 128 x rp x 4 bytes: the scale of block b of row r at
+ *           ((b / 4) * rp + r) * 4 + b % 4; zeros beyond rows and cols
+ * codes must be 16-byte aligned, scales 4-byte aligned.  The products rely on
+ * the zeros beyond cols (sgemm_f32_mx4_quantize writes them).  A value is
+ * code * 2^(s - 127); where that exceeds the largest float (s above 252) it
+ * is infinite.  rows and cols are at most SGEMM_MX4_MAX_DIM.
+ *
+ * Common to the calls below: float matrices are row-major, of one of the
+ * types SGEMM_TYPE_*, with a leading dimension in elements; they need the
+ * alignment of one element only (16-byte aligned rows are faster).  Work is
+ * enqueued on `stream` and nothing is allocated, synchronised or kept, so
+ * every call can be captured into a graph as it is; scratch memory is the
+ * caller's.  All arguments are checked before anything is enqueued:
+ * SGEMM_ERR_SHAPE, _LD, _NULL, _ALIGN, _ALIAS (an output overlaps an input
+ * or another output), _POINTER and _SCRATCH (too little scratch memory), and
+ * SGEMM_ERR_CONFIG for an unknown type, rule or flag.  Results do not depend
+ * on timing: repeated calls give the same bits.
+ */
+#define SGEMM_TYPE_F32   0
+#define SGEMM_TYPE_BF16  1
+#define SGEMM_TYPE_F16   2
+
+#define SGEMM_MX4_MAX_DIM (1 << 22)
+
+/* How a block's scale follows from its largest magnitude m > 0. */
+#define SGEMM_MX4_SCALE_FLOOR   0  /* 2^(floor(log2 m) - 2): values above 6 scales become 6 */
+#define SGEMM_MX4_SCALE_NOCLIP  1  /* the least power of two with m <= 6 scales */
+
+/* Bytes of the two arrays of a rows x cols matrix (either may be NULL). */
+int sgemm_f32_mx4_bytes(int rows, int cols, long long *codes_bytes, long long *scales_bytes);
+
+/*
+ * Quantises the rows x cols matrix X: into (codes, scales) with blocks along
+ * its rows, into (codes_t, scales_t), the cols x rows matrix X^T with blocks
+ * along X's columns, or both in one pass over X.  An array pair that is not
+ * wanted is NULL (not both pairs).  Each value divided by its block's scale
+ * is rounded to the nearest code, ties to the even one, and held at 6.  A
+ * block of zeros, or of values too small for the least scale, has s = 0; a
+ * block that holds a NaN or an infinity has s = 255 and zero codes.
+ */
+int sgemm_f32_mx4_quantize(int rows, int cols, int type, const void *X, int ldx, int rule,
+                           void *codes, void *scales, void *codes_t, void *scales_t,
+                           hipStream_t stream);
+
+/* Y (rows x cols) = the values of a 4-bit matrix, rounded to Y's type. */
+int sgemm_f32_mx4_dequantize(int rows, int cols, const void *codes, const void *scales,
+                             int type, void *Y, int ldy, hipStream_t stream);
+
+/*
+ * C = alpha * A * B^T + beta * C for 4-bit matrices A (M x K) and B (N x K),
+ * sums in fp32, rounded once to C's type.  As in sgemm_f32_gemm, beta == 0
+ * means C is not read, and alpha == 0 or K == 0 that A and B are not (nor
+ * checked).  A training step takes its three products from it: with W (N x K)
+ * and the layer Y = X W^T, dX = dY W multiplies dY and W^T, dW = dY^T X
+ * multiplies dY^T and X^T, each quantised along the sum.
+ */
+int sgemm_f32_mx4_gemm(int M, int N, int K, float alpha,
+                       const void *a_codes, const void *a_scales,
+                       const void *b_codes, const void *b_scales, float beta,
+                       int type, void *C, int ldc, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
