@@ -10,7 +10,7 @@ import os
 
 from . import mx4 as _mx4
 from .mx4 import Mx4, mx4_dequantize, mx4_gemm, mx4_quantize, mx4_quantize_both  # noqa: F401
-from .mx4 import mx4_train_backward, mx4_train_forward  # noqa: F401
+from .mx4 import mx4_linear, mx4_moe, mx4_train_backward, mx4_train_forward  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # The in-tree build; SGEMM_F32_LIBRARY may name another build of the same sources.

@@ -87,6 +87,18 @@ __device__ __forceinline__ void mx_store8(typename MxType<TYPE>::T *p, const flo
     }
 }
 
+// Eight values of a row from column c on, zeros at and after `cols`.
+template <int TYPE>
+__device__ __forceinline__ void mx_load_edge8(const typename MxType<TYPE>::T *row, int c, int cols, bool vec,
+                                              float (&v)[8]) {
+    if (vec && c + 8 <= cols) {
+        mx_load8<TYPE>(row + c, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? MxType<TYPE>::load(row + c + i) : 0.0f;
+}
+
 // ---- host: one job per launcher ----
 
 struct MxQuantJob {

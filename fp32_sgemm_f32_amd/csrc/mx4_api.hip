@@ -5,7 +5,7 @@
 #include <atomic>
 
 #include "abi.h"
-#include "mx4.h"
+#include "mx4_thin.h"
 
 #define SGEMM_API extern "C" __attribute__((visibility("default")))
 
@@ -127,4 +127,59 @@ SGEMM_API int sgemm_f32_mx4_gemm(int M, int N, int K, float alpha, const void *a
     if (status != SGEMM_OK) return status;
     return done(launch_mx4_gemm({(const uint8_t *)a, (const uint8_t *)sa, (const uint8_t *)b, (const uint8_t *)sb, M, N, k,
                                  type, alpha, beta, C, ldc}, cus, stream));
+}
+
+SGEMM_API int sgemm_f32_mx4_linear(int M, int N, int K, int type, const void *X, int ldx, const void *c, const void *s,
+                                   void *Y, int ldy, hipStream_t stream) {
+    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return SGEMM_ERR_SHAPE;
+    if (!known_type(type)) return SGEMM_ERR_CONFIG;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    if (ldx < K || ldy < N) return SGEMM_ERR_LD;
+    const Span spans[] = {floats(X, M, K, ldx, type, false), codes(c, N, K, false), scales(s, N, K, false),
+                          floats(Y, M, N, ldy, type, true)};
+    int dev = 0;
+    const int status = check_spans(spans, &dev);
+    if (status != SGEMM_OK) return status;
+    return done(launch_mx4_linear({X, ldx, (const uint8_t *)c, (const uint8_t *)s, M, N, K, type, Y, ldy}, stream));
+}
+
+// Sizes of an expert layer: SGEMM_OK, or what is wrong with them.
+static int moe_sizes(int tokens, int hidden, int inner, int experts, int top, int type) {
+    if (tokens < 0 || tokens > SGEMM_MX4_MAX_TOKENS || experts < 1 || experts > SGEMM_MX4_MAX_EXPERTS || top < 1 ||
+        top > experts || top > SGEMM_MX4_MAX_TOP || hidden < 1 || inner < 1 ||
+        (int64_t)experts * 2 * inner > SGEMM_MX4_MAX_DIM || (int64_t)experts * hidden > SGEMM_MX4_MAX_DIM)
+        return SGEMM_ERR_SHAPE;
+    return known_type(type) ? SGEMM_OK : SGEMM_ERR_CONFIG;
+}
+
+SGEMM_API int sgemm_f32_mx4_moe_scratch(int tokens, int hidden, int inner, int experts, int top, int type,
+                                        long long *bytes) {
+    const int status = moe_sizes(tokens, hidden, inner, experts, top, type);
+    if (status != SGEMM_OK) return status;
+    if (!bytes) return SGEMM_ERR_NULL;
+    *bytes = mx4_moe_scratch(tokens, hidden, inner, experts, top, type);
+    return SGEMM_OK;
+}
+
+SGEMM_API int sgemm_f32_mx4_moe(int tokens, int hidden, int inner, int experts, int top, int norm, int type, const void *X,
+                                int ldx, const void *router, int ldr, const void *up, const void *sup, const void *down,
+                                const void *sdown, void *Y, int ldy, void *scratch, long long scratch_bytes,
+                                hipStream_t stream) {
+    int status = moe_sizes(tokens, hidden, inner, experts, top, type);
+    if (status != SGEMM_OK) return status;
+    if (norm != 0 && norm != 1) return SGEMM_ERR_CONFIG;
+    if (tokens == 0) return SGEMM_OK;
+    if (ldx < hidden || ldr < hidden || ldy < hidden) return SGEMM_ERR_LD;
+    const int64_t need = mx4_moe_scratch(tokens, hidden, inner, experts, top, type);
+    const int ur = experts * 2 * inner, dr = experts * hidden;
+    const Span spans[] = {floats(X, tokens, hidden, ldx, type, false), floats(router, experts, hidden, ldr, type, false),
+                          codes(up, ur, hidden, false), scales(sup, ur, hidden, false),
+                          codes(down, dr, inner, false), scales(sdown, dr, inner, false),
+                          floats(Y, tokens, hidden, ldy, type, true), Span{scratch, need, 256, true}};
+    if (scratch && scratch_bytes < need) return SGEMM_ERR_SCRATCH;
+    int dev = 0;
+    if ((status = check_spans(spans, &dev)) != SGEMM_OK) return status;
+    return done(launch_mx4_moe({X, router, ldx, ldr, (const uint8_t *)up, (const uint8_t *)sup, (const uint8_t *)down,
+                                (const uint8_t *)sdown, tokens, hidden, inner, experts, top, norm, type, Y, ldy,
+                                (char *)scratch}, stream));
 }

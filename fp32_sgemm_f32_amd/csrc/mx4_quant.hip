@@ -51,18 +51,6 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t s) {
     return c;
 }
 
-// Eight values of a row from column c on, zeros at and after `cols`.
-template <int TYPE>
-__device__ __forceinline__ void load_edge8(const typename MxType<TYPE>::T *row, int c, int cols, bool vec,
-                                           float (&v)[8]) {
-    if (vec && c + 8 <= cols) {
-        mx_load8<TYPE>(row + c, v);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? MxType<TYPE>::load(row + c + i) : 0.0f;
-}
-
 // Along the rows.  A lane holds 8 adjacent values, four lanes a block, a wave
 // 2 rows x 256 columns (full lines both ways), a workgroup 8 rows x 256
 // columns.  Rows up to the padding's end get zero scales.
@@ -75,7 +63,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(MxQuantJob j, int vec) 
     float v[8];
     const bool real = r < j.rows;
     const auto *row = (const typename MxType<TYPE>::T *)j.x + (real ? r : 0) * j.ldx;
-    load_edge8<TYPE>(row, c, real ? j.cols : 0, vec, v);
+    mx_load_edge8<TYPE>(row, c, real ? j.cols : 0, vec, v);
     uint32_t m = max_bits8(v);
     m = umax(m, quad_xor1(m));
     m = umax(m, quad_xor2(m));
@@ -111,7 +99,7 @@ __global__ __launch_bounds__(512) void quant_tile_kernel(MxQuantJob j, int vec) 
         const int64_t r = r0 + 32 * i + lr;
         const bool real = r < j.rows;
         const T *row = (const T *)j.x + (real ? r : 0) * j.ldx;
-        load_edge8<TYPE>(row, c0 + lc, real ? j.cols : 0, vec, v[i]);
+        mx_load_edge8<TYPE>(row, c0 + lc, real ? j.cols : 0, vec, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -22,7 +22,10 @@ def _bind(lib):
     lib.sgemm_f32_mx4_quantize.argtypes = [i, i, i, p, i, i, p, p, p, p, p]
     lib.sgemm_f32_mx4_dequantize.argtypes = [i, i, p, p, i, p, i, p]
     lib.sgemm_f32_mx4_gemm.argtypes = [i, i, i, f, p, p, p, p, f, i, p, i, p]
-    for name in ("bytes", "quantize", "dequantize", "gemm"):
+    lib.sgemm_f32_mx4_linear.argtypes = [i, i, i, i, p, i, p, p, p, i, p]
+    lib.sgemm_f32_mx4_moe.argtypes = [i, i, i, i, i, i, i, p, i, p, i, p, p, p, p, p, i, p, ll, p]
+    lib.sgemm_f32_mx4_moe_scratch.argtypes = [i, i, i, i, i, i, ctypes.POINTER(ll)]
+    for name in ("bytes", "quantize", "dequantize", "gemm", "linear", "moe", "moe_scratch"):
         getattr(lib, "sgemm_f32_mx4_" + name).restype = i
 
 
@@ -145,6 +148,14 @@ class _Run:
             raise SgemmError(st, "sgemm_f32_" + name)
 
 
+def _result(run, out, shape, dtype):
+    if out is None:
+        return run.empty(shape, dtype)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
+        raise ValueError(f"out must be {tuple(shape)} of {dtype}")
+    return out
+
+
 def _quantize(X, along, down, rule, stream):
     if rule not in _RULES:
         raise ValueError(f"rule must be one of {sorted(_RULES)}")
@@ -245,3 +256,61 @@ def mx4_train_backward(dY, saved, dW=None, stream=None):
     if dW is None:
         return dX, mx4_gemm(dt, xt, dtype=torch.float32, stream=stream)
     return dX, mx4_gemm(dt, xt, out=dW, beta=1.0, stream=stream)
+
+
+def mx4_linear(X, W, out=None, stream=None):
+    """X @ W^T for float rows X (M, K) and 4-bit weights W (N, K), in X's type.
+
+    X is used as it is (no rounding to 4 bits), sums are in fp32.  Made for one
+    token or a few: W is read once for up to 64 rows.
+    """
+    ty, ldx = _floats(X, "X")
+    _packed(W, "W", X.device)
+    M, K = X.shape
+    if K != W.shape[1]:
+        raise ValueError(f"inner dimensions differ: {K} vs {W.shape[1]}")
+    N = W.shape[0]
+    run = _Run(X.device, stream)
+    out = _result(run, out, (M, N), X.dtype)
+    _, ldy = _floats(out, "out", X.device)
+    run.call("mx4_linear", (X, W, out), M, N, K, ty, X.data_ptr(), ldx, W.codes.data_ptr(), W.scales.data_ptr(),
+             out.data_ptr(), ldy)
+    return out
+
+
+def mx4_moe(X, router, gate_up, down, top, norm=True, out=None, stream=None):
+    """A mixture-of-experts layer for up to 64 tokens X (T, H), in X's type.
+
+    router (E, H) in X's type; gate_up an Mx4 of (E * 2 * F, H), expert after
+    expert, F gate rows and then F up rows; down an Mx4 of (E * H, F).  A token
+    goes to the `top` experts of largest logit X router^T (lower index first on
+    equal ones) and gets the sum of p_e D_e (silu(G_e x) * (U_e x)), with p the
+    softmax over those (norm) or over all experts.
+    """
+    import torch
+
+    from . import OK, SgemmError, library
+
+    ty, ldx = _floats(X, "X")
+    tr, ldr = _floats(router, "router", X.device)
+    _packed(gate_up, "gate_up", X.device)
+    _packed(down, "down", X.device)
+    T, H = X.shape
+    E, F = router.shape[0], down.shape[1]
+    if tr != ty:
+        raise TypeError("router must have X's type")
+    if router.shape[1] != H or gate_up.shape != (E * 2 * F, H) or down.shape[0] != E * H:
+        raise ValueError(f"router {tuple(router.shape)}, gate_up {gate_up.shape} and down {down.shape} do not fit "
+                         f"together with {H} columns of X")
+    need = ctypes.c_longlong()
+    st = library().sgemm_f32_mx4_moe_scratch(T, H, F, E, top, ty, ctypes.byref(need))
+    if st != OK:
+        raise SgemmError(st, "sgemm_f32_mx4_moe")
+    run = _Run(X.device, stream)
+    out = _result(run, out, (T, H), X.dtype)
+    _, ldy = _floats(out, "out", X.device)
+    scratch = run.empty((need.value,), torch.uint8)
+    run.call("mx4_moe", (X, router, gate_up, down, out), T, H, F, E, top, int(bool(norm)), ty, X.data_ptr(), ldx,
+             router.data_ptr(), ldr, gate_up.codes.data_ptr(), gate_up.scales.data_ptr(), down.codes.data_ptr(),
+             down.scales.data_ptr(), out.data_ptr(), ldy, scratch.data_ptr(), need.value)
+    return out

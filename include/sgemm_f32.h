@@ -429,6 +429,50 @@ int sgemm_f32_mx4_gemm(int M, int N, int K, float alpha,
                        const void *b_codes, const void *b_scales, float beta,
                        int type, void *C, int ldc, hipStream_t stream);
 
+/*
+ * Y = X * W^T for float rows X (M x K) and 4-bit weights W (N x K), Y (M x N)
+ * in X's type: the product of one token or a few with a layer whose weights
+ * alone are in 4 bits.  X is not rounded: every product is exact, the sums
+ * are in fp32.  W is read once for up to 64 rows of X; longer X run 64 rows
+ * at a time (sgemm_f32_mx4_gemm, on quantised X, is the call for those).
+ */
+int sgemm_f32_mx4_linear(int M, int N, int K, int type, const void *X, int ldx,
+                         const void *codes, const void *scales,
+                         void *Y, int ldy, hipStream_t stream);
+
+/*
+ * A mixture-of-experts layer for a few tokens, experts in 4 bits:
+ *
+ *     l = X * router^T                      (tokens x experts)
+ *     S = the `top` largest l of a token, lower index first on equal ones
+ *         (NaN counts as largest)
+ *     p_e = exp(l_e - max l) / sum          over S (norm = 1), or over all
+ *                                           experts (norm = 0)
+ *     Y = sum over e in S of p_e * D_e * (silu(G_e X) * (U_e X))
+ *
+ * X, Y: tokens x hidden; router: experts x hidden, in X's type.  `up` is a
+ * 4-bit matrix of experts * 2 * inner rows and hidden columns: expert after
+ * expert, first the inner rows of G_e, then those of U_e.  `down`: experts *
+ * hidden rows, inner columns.  The choice is made on sums in 64 bits.  The
+ * inner activations are held to 24 bits for fp32, to 16 for 16-bit types.
+ * tokens <= 64, 1 <= top <= min(experts, 16), experts <= 1024; hidden and
+ * inner at least 1.  scratch: device memory of at least the bytes that
+ * sgemm_f32_mx4_moe_scratch gives, 256-byte aligned, overlapping nothing;
+ * its contents do not matter before or after.
+ */
+#define SGEMM_MX4_MAX_TOKENS   64
+#define SGEMM_MX4_MAX_TOP      16
+#define SGEMM_MX4_MAX_EXPERTS  1024
+int sgemm_f32_mx4_moe(int tokens, int hidden, int inner, int experts, int top, int norm,
+                      int type, const void *X, int ldx, const void *router, int ldr,
+                      const void *up_codes, const void *up_scales,
+                      const void *down_codes, const void *down_scales,
+                      void *Y, int ldy, void *scratch, long long scratch_bytes,
+                      hipStream_t stream);
+/* Bytes of scratch memory of such a call. */
+int sgemm_f32_mx4_moe_scratch(int tokens, int hidden, int inner, int experts, int top,
+                              int type, long long *bytes);
+
 #ifdef __cplusplus
 }
 #endif
