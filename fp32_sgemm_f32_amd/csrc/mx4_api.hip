@@ -119,6 +119,7 @@ SGEMM_API int sgemm_f32_mx4_gemm(int M, int N, int K, float alpha, const void *a
     if (M == 0 || N == 0) return SGEMM_OK;
     if (ldc < N) return SGEMM_ERR_LD;
     const int k = alpha == 0.0f ? 0 : K;   // nothing of A and B is read then
+    if (K == 0) alpha = 0.0f;              // an empty sum stays zero whatever alpha
     const Span spans[] = {codes(a, M, k, false), scales(sa, M, k, false), codes(b, N, k, false),
                           scales(sb, N, k, false), floats(C, M, N, ldc, type, true)};
     int dev = 0, cus = 0;
