@@ -91,12 +91,15 @@ __device__ __forceinline__ void mx_store8(typename MxType<TYPE>::T *p, const flo
 template <int TYPE>
 __device__ __forceinline__ void mx_load_edge8(const typename MxType<TYPE>::T *row, int c, int cols, bool vec,
                                               float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
     if (vec && c + 8 <= cols) {
         mx_load8<TYPE>(row + c, v);
-        return;
-    }
+    } else if (c < cols) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? MxType<TYPE>::load(row + c + i) : 0.0f;
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols) v[i] = MxType<TYPE>::load(row + c + i);
+    }
 }
 
 // ---- host: one job per launcher ----

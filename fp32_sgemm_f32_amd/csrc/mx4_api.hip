@@ -130,18 +130,29 @@ SGEMM_API int sgemm_f32_mx4_gemm(int M, int N, int K, float alpha, const void *a
                                  type, alpha, beta, C, ldc}, cus, stream));
 }
 
+SGEMM_API int sgemm_f32_mx4_linear_scratch(int M, int N, int K, int type, long long *bytes) {
+    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return SGEMM_ERR_SHAPE;
+    if (!known_type(type)) return SGEMM_ERR_CONFIG;
+    if (!bytes) return SGEMM_ERR_NULL;
+    *bytes = mx4_linear_scratch(M, N, K, type);
+    return SGEMM_OK;
+}
+
 SGEMM_API int sgemm_f32_mx4_linear(int M, int N, int K, int type, const void *X, int ldx, const void *c, const void *s,
-                                   void *Y, int ldy, hipStream_t stream) {
+                                   void *Y, int ldy, void *scratch, long long scratch_bytes, hipStream_t stream) {
     if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return SGEMM_ERR_SHAPE;
     if (!known_type(type)) return SGEMM_ERR_CONFIG;
     if (M == 0 || N == 0) return SGEMM_OK;
     if (ldx < K || ldy < N) return SGEMM_ERR_LD;
+    const int64_t need = mx4_linear_scratch(M, N, K, type);
+    if (scratch && scratch_bytes < need) return SGEMM_ERR_SCRATCH;
     const Span spans[] = {floats(X, M, K, ldx, type, false), codes(c, N, K, false), scales(s, N, K, false),
-                          floats(Y, M, N, ldy, type, true)};
+                          floats(Y, M, N, ldy, type, true), Span{scratch, need, 256, true}};
     int dev = 0;
     const int status = check_spans(spans, &dev);
     if (status != SGEMM_OK) return status;
-    return done(launch_mx4_linear({X, ldx, (const uint8_t *)c, (const uint8_t *)s, M, N, K, type, Y, ldy}, stream));
+    return done(launch_mx4_linear({X, ldx, (const uint8_t *)c, (const uint8_t *)s, M, N, K, type, Y, ldy, (float *)scratch},
+                                  stream));
 }
 
 // Sizes of an expert layer: SGEMM_OK, or what is wrong with them.

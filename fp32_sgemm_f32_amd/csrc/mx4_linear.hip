@@ -1,234 +1,176 @@
 // Y = X W^T for a few rows X of floats and 4-bit weights W (N x K): the
 // product of single tokens, bound by reading W once (0.53 bytes a weight).
 //
-// A workgroup takes 16 R rows of W and up to 16 MT tokens; its 8 waves split
-// K slab by slab (neighbouring waves read neighbouring 64-byte pieces of the
-// same rows), each with U slabs of weights in flight, and their sums are
-// added in wave order through LDS: no partials in memory, the same bits every
-// time.  More tokens than 64 take further workgroups (blockIdx.y), which
-// find the weights in the caches.
-//
-// bf16 tokens whose rows start on 16-byte boundaries are loaded straight into
-// operand registers.  Other types and layouts go through LDS: a wave splits
-// its own slab of the tokens into bf16 pieces there, loaded one step ahead.
+// A workgroup takes up to 16 MT tokens, 8 KS slabs of K and a run of row
+// tiles (mx4_thin.h).  Where K is longer than that, several workgroups share
+// a row tile and write their sums to scratch memory, which a second kernel
+// adds in K order: the same bits every time.  More than 64 tokens run 64 at a
+// time.
 #include "mx4_thin.h"
 
 namespace sgemm {
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kPieceRow = 272;   // bytes of a token's 128 pieces in LDS: 16 more than they take, against bank conflicts
+constexpr int kMostTokens = 64;   // of one pass over the weights
 
-template <int TYPE, bool STAGE, int R, int MT>
-__global__ __launch_bounds__(64 * kWaves) void linear_kernel(MxLinearJob j, int vec) {
+// Whether the registers (128 a lane, without spills) let a CU hold two workgroups.
+constexpr bool two_on_a_cu(int pieces, int ks, int mt) { return pieces == 1 ? ks <= 2 && mt <= 2 : ks * mt == 1; }
+
+struct Args {
+    const void *x;
+    int64_t ldx;
+    MxWeights w;
+    int M, N, K, vec, per, parts;   // per: row tiles of a workgroup; parts: workgroups along K
+    void *y;
+    int64_t ldy;
+    float *partial;                 // parts x M x pitch, if parts > 1
+    int64_t pitch;
+};
+
+template <int TYPE, int KS, int MT, int G>
+__global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, MT) ? 4 : 2) void linear_kernel(Args a) {
     typedef typename MxType<TYPE>::T T;
-    constexpr int P = mx_pieces(TYPE), U = 4;
-    static_assert(STAGE || P == 1, "one piece without staging");
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int n0 = blockIdx.x * 16 * R, m0 = blockIdx.y * 16 * MT;
-    const int slabs = mx_slabs(j.K);
-    const int64_t plane = mx_plane_rows(j.N);
-    const int l16 = lane & 15, q = lane >> 4;
-    const int tokens = j.M - m0 < 16 * MT ? j.M - m0 : 16 * MT;
-
-    const uint8_t *row[R];
-    const uint32_t *words[R];
+    __shared__ __attribute__((aligned(16))) f32v4 red[kThinWaves * G * MT * 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int part = blockIdx.x % a.parts, first = blockIdx.x / a.parts * a.per, m0 = blockIdx.y * 16 * MT;
+    const int tiles = (a.N + 15) / 16, end = first + a.per < tiles ? first + a.per : tiles;
+    const int slab0 = part * kThinWaves * KS + wave;
+    const T *row[MT];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int n = n0 + 16 * r + l16 < j.N ? n0 + 16 * r + l16 : j.N - 1;   // rows past N: computed, not stored
-        row[r] = j.codes + n * ((int64_t)slabs * kMxSlabBytes);
-        words[r] = (const uint32_t *)j.scales + n;
+    for (int mt = 0; mt < MT; ++mt) {
+        const int t = m0 + mt * 16 + (lane & 15);
+        row[mt] = t < a.M ? (const T *)a.x + t * a.ldx : nullptr;
     }
-    const T *x = (const T *)j.x + m0 * j.ldx;
-
-    // Direct operands: token l16 of tile mt, columns of step s.
-    auto direct = [&](int mt, int k) -> uint4 {
-        if constexpr (!STAGE) {
-            const int t = mt * 16 + l16;
-            if (t < tokens) {
-                const T *p = x + t * j.ldx + k;
-                if (k + 8 <= j.K) return *(const uint4 *)p;
-                uint32_t u[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (k + i < j.K) u[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-                return uint4{u[0], u[1], u[2], u[3]};
+    MxTokens<TYPE, mx_pieces(TYPE), KS, MT> x;
+    x.load(row, slab0, a.K, a.vec, lane >> 4);
+    mx_stream<1, G>(
+        x, a.w, slab0, first, end, red, nullptr, true, true,
+        [&](int tile) -> int64_t {
+            const int n = tile * 16 + (lane & 15);
+            return n < a.N ? n : a.N - 1;   // rows past N: computed, not stored
+        },
+        [&](int tile, int mt, int l, const f32v4(&v)[1]) {
+            const int t = m0 + mt * 16 + (l & 15), n = tile * 16 + 4 * (l >> 4);
+            if (t >= a.M) return;
+            if (a.parts > 1) {
+                *(f32v4 *)(a.partial + ((int64_t)part * a.M + t) * a.pitch + n) = v[0];
+                return;
             }
-        }
-        return uint4{0, 0, 0, 0};
-    };
-
-    // Staged operands: this wave's 16 tokens x 128 columns, a lane taking
-    // columns 4 (lane % 32) .. + 3 of tokens lane / 32 + 2 i.
-    uint8_t *mine = lds + wave * (P * 16 * kPieceRow);
-    const int sk = 4 * (lane & 31), sh = lane >> 5;
-    float next[STAGE ? 8 : 1][4];
-    auto fetch = [&](int mt, int slab) {
-        if constexpr (STAGE) {
-            const int k = slab * kMxSlab + sk;
+            T *y = (T *)a.y + t * a.ldy + n;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int t = mt * 16 + sh + 2 * i;
-                const T *p = x + (t < tokens ? t : 0) * j.ldx + k;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) next[i][c] = 0.0f;
-                if (t >= tokens || slab >= slabs) continue;
-                if (vec && k + 4 <= j.K) {
-                    if constexpr (TYPE == SGEMM_TYPE_F32) {
-                        const f32v4 v = *(const f32v4 *)p;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) next[i][c] = v[c];
-                    } else {
-                        const uint2 v = *(const uint2 *)p;
-                        const uint16_t h[4] = {(uint16_t)v.x, (uint16_t)(v.x >> 16), (uint16_t)v.y, (uint16_t)(v.y >> 16)};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) next[i][c] = MxType<TYPE>::load(&h[c]);
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (k + c < j.K) next[i][c] = MxType<TYPE>::load(p + c);
-                }
-            }
-        }
-    };
-    auto stage = [&](int mt) {
-        if constexpr (STAGE) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (mt * 16 + 2 * i >= tokens) break;
-                uint16_t p[4][P];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) mx_split<P>(next[i][c], p[c]);
-#pragma unroll
-                for (int s = 0; s < P; ++s)
-                    *(uint2 *)(mine + (s * 16 + sh + 2 * i) * kPieceRow + 2 * sk) =
-                        uint2{(uint32_t)p[0][s] | (uint32_t)p[1][s] << 16, (uint32_t)p[2][s] | (uint32_t)p[3][s] << 16};
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-        }
-    };
-
-    f32v4 acc[R][MT];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) acc[r][mt] = f32v4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    if (STAGE) fetch(0, wave);
-    for (int s0 = wave; s0 < slabs; s0 += kWaves * U) {
-        MxBlock b[U][R];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                b[u][r] = mx_block(row[r], words[r], plane, s0 + kWaves * u, q, s0 + kWaves * u < slabs);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int slab = s0 + kWaves * u;
-            if (slab >= slabs) break;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                if (mt * 16 >= tokens) break;
-                if constexpr (STAGE) {
-                    stage(mt);
-                    if (mt + 1 < MT && (mt + 1) * 16 < tokens) fetch(mt + 1, slab);
-                    else fetch(0, slab + kWaves);
-                }
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    uint4 xs[P];
-                    if constexpr (STAGE) {
-                        const int t = mt * 16 + l16 < tokens ? l16 : tokens - 1 - mt * 16;   // unused columns: any token
-#pragma unroll
-                        for (int p = 0; p < P; ++p)
-                            xs[p] = *(const uint4 *)(mine + (p * 16 + t) * kPieceRow + 64 * q + 16 * s);
-                    } else {
-                        xs[0] = direct(mt, slab * kMxSlab + 32 * q + 8 * s);
-                    }
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const uint32_t c = s == 0 ? b[u][r].codes.x : s == 1 ? b[u][r].codes.y
-                                         : s == 2 ? b[u][r].codes.z : b[u][r].codes.w;
-                        const bf16v8 w = mx_bf16x8(c, mx_scale(b[u][r], q));
-#pragma unroll
-                        for (int p = 0; p < P; ++p) acc[r][mt] = mx_mfma(w, xs[p], acc[r][mt]);
-                    }
-                }
-                if constexpr (STAGE) {
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                    __builtin_amdgcn_wave_barrier();
-                }
-            }
-        }
-    }
-
-    // The waves' sums, added in wave order.  Lane l of a tile holds rows
-    // 4 (l / 16) .. + 3 of W for token l % 16.
-    __syncthreads();
-    f32v4 *red = (f32v4 *)lds;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) red[((wave * R + r) * MT + mt) * 64 + lane] = acc[r][mt];
-    __syncthreads();
-    for (int i = tid; i < R * MT * 64; i += 64 * kWaves) {
-        f32v4 sum = red[i];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) sum += red[w * (R * MT * 64) + i];
-        const int l = i & 63, mt = (i >> 6) % MT, r = (i >> 6) / MT;
-        const int t = mt * 16 + (l & 15), n = n0 + 16 * r + 4 * (l >> 4);
-        if (t >= tokens) continue;
-        T *y = (T *)j.y + (m0 + t) * j.ldy + n;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (n + c < j.N) y[c] = MxType<TYPE>::from(sum[c]);
-    }
+            for (int c = 0; c < 4; ++c)
+                if (n + c < a.N) y[c] = MxType<TYPE>::from(v[0][c]);
+        });
 }
 
-template <int TYPE, bool STAGE, int R, int MT>
-hipError_t launch_shape(const MxLinearJob &job, int vec, hipStream_t s) {
-    MxLinearJob j = job;
-    const int staged = STAGE ? kWaves * mx_pieces(TYPE) * 16 * kPieceRow : 0, sums = kWaves * R * MT * 1024;
-    const int bytes = staged > sums ? staged : sums;
-    const void *k = (const void *)linear_kernel<TYPE, STAGE, R, MT>;
-    const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return e;
-    void *params[] = {&j, &vec};
+// Adds the parts; a thread takes one value.
+template <int TYPE>
+__global__ __launch_bounds__(256) void join_kernel(Args a) {
+    const int n = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+    if (n >= a.N) return;
+    const float *p = a.partial + t * a.pitch + n;
+    float sum = *p;
+    for (int k = 1; k < a.parts; ++k) sum += p[k * a.M * a.pitch];
+    ((typename MxType<TYPE>::T *)a.y)[t * a.ldy + n] = MxType<TYPE>::from(sum);
+}
+
+// Slabs that a wave keeps: as many as hold K, up to `most` (the registers).
+int kept_slabs(int K, int most) {
+    const int need = (mx_slabs(K) + kThinWaves - 1) / kThinWaves;
+    return need >= most ? most : need > 2 ? 4 : need > 1 ? 2 : 1;
+}
+// That most, for 16 mt tokens.
+int most_slabs(int type, int mt) {
+    if (type == SGEMM_TYPE_BF16) return mt == 1 ? 4 : 2;
+    if (type == SGEMM_TYPE_F16) return mt < 4 ? 2 : 1;
+    return mt == 1 ? 2 : 1;
+}
+// Token tiles of a workgroup; fp32 stops at 2 (four would take 192 registers).
+int token_tiles(int M, int type) {
+    const int mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    return type == SGEMM_TYPE_F32 && mt > 2 ? 2 : mt;
+}
+int k_parts(int M, int K, int type) {
+    const int ks = kept_slabs(K, most_slabs(type, token_tiles(M, type)));
+    const int parts = (mx_slabs(K) + kThinWaves * ks - 1) / (kThinWaves * ks);
+    return parts > 0 ? parts : 1;
+}
+
+template <int TYPE, int KS, int MT>
+hipError_t launch_shape(Args a, hipStream_t s) {
+    constexpr int G = KS * MT >= 4 ? 2 : 4;
+    // Workgroups: as many as the CUs hold at once.
+    constexpr int kWant = two_on_a_cu(mx_pieces(TYPE), KS, MT) ? 512 : 256;
+    const int tiles = (a.N + 15) / 16, groups = kWant / a.parts > 0 ? kWant / a.parts : 1;
+    a.per = mx_share(tiles, groups < tiles ? groups : tiles, 1);
+    const int row_groups = (tiles + a.per - 1) / a.per;
+    void *params[] = {&a};
+    hipError_t e = hipLaunchKernel((const void *)linear_kernel<TYPE, KS, MT, G>,
+                                   dim3((unsigned)(row_groups * a.parts), (unsigned)((a.M + 16 * MT - 1) / (16 * MT))),
+                                   dim3(kThinThreads), params, 0, s);
+    if (e != hipSuccess || a.parts == 1) return e;
+    return hipLaunchKernel((const void *)join_kernel<TYPE>, dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M), dim3(256), params,
+                           0, s);
+}
+
+template <int TYPE, int MT>
+hipError_t launch_tokens(const Args &a, hipStream_t s) {
+    const int ks = kept_slabs(a.K, most_slabs(TYPE, MT));
+    if constexpr (TYPE == SGEMM_TYPE_BF16 && MT == 1)
+        if (ks == 4) return launch_shape<TYPE, 4, MT>(a, s);
+    if constexpr (!(TYPE == SGEMM_TYPE_F16 && MT == 4) && !(TYPE == SGEMM_TYPE_F32 && MT > 1))
+        if (ks == 2) return launch_shape<TYPE, 2, MT>(a, s);
+    return launch_shape<TYPE, 1, MT>(a, s);
+}
+
+template <int TYPE>
+hipError_t launch_type(const MxLinearJob &j, hipStream_t s) {
     const int64_t esize = TYPE == SGEMM_TYPE_F32 ? 4 : 2;
-    constexpr int kMost = 65535 * 16 * MT;   // rows of one launch (the grid's y limit)
-    for (int64_t m = 0; m < job.M; m += kMost) {
-        j.M = job.M - m < kMost ? (int)(job.M - m) : kMost;
-        j.x = (const char *)job.x + m * job.ldx * esize;
-        j.y = (char *)job.y + m * job.ldy * esize;
-        const hipError_t l = hipLaunchKernel(
-            k, dim3((unsigned)((j.N + 16 * R - 1) / (16 * R)), (unsigned)((j.M + 16 * MT - 1) / (16 * MT))),
-            dim3(64 * kWaves), params, bytes, s);
-        if (l != hipSuccess) return l;
+    for (int64_t m = 0; m < j.M; m += kMostTokens) {
+        Args a;
+        a.M = j.M - m < kMostTokens ? (int)(j.M - m) : kMostTokens;
+        a.x = (const char *)j.x + m * j.ldx * esize;
+        a.ldx = j.ldx;
+        a.w = mx_weights(j.codes, j.scales, j.N, j.K);
+        a.N = j.N;
+        a.K = j.K;
+        a.vec = ((uintptr_t)j.x & 15) == 0 && (j.ldx * esize & 15) == 0;
+        a.y = (char *)j.y + m * j.ldy * esize;
+        a.ldy = j.ldy;
+        a.parts = k_parts(a.M, a.K, TYPE);
+        a.partial = j.scratch;
+        a.pitch = ((int64_t)j.N + 15) / 16 * 16;
+        const int mt = token_tiles(a.M, TYPE);
+        hipError_t e;
+        if (mt == 1) e = launch_tokens<TYPE, 1>(a, s);
+        else if (mt == 2) e = launch_tokens<TYPE, 2>(a, s);
+        else if constexpr (TYPE != SGEMM_TYPE_F32) e = launch_tokens<TYPE, 4>(a, s);
+        else e = hipErrorInvalidValue;
+        if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
-template <int TYPE, bool STAGE>
-hipError_t launch_tokens(const MxLinearJob &j, int vec, hipStream_t s) {
-    if (j.M <= 16) return launch_shape<TYPE, STAGE, 1, 1>(j, vec, s);
-    if (j.M <= 32) return launch_shape<TYPE, STAGE, 1, 2>(j, vec, s);
-    return launch_shape<TYPE, STAGE, 2, 4>(j, vec, s);
-}
-
 }  // namespace
 
+int64_t mx4_linear_scratch(int M, int N, int K, int type) {
+    // The passes: full ones of 64 tokens, and the last.
+    int64_t most = 0;
+    const int sizes[] = {M < kMostTokens ? M : kMostTokens, M % kMostTokens};
+    for (int m : sizes) {
+        if (m == 0) continue;
+        const int64_t parts = k_parts(m, K, type);
+        const int64_t bytes = parts > 1 ? parts * m * (((int64_t)N + 15) / 16 * 16) * 4 : 0;
+        most = bytes > most ? bytes : most;
+    }
+    return most;
+}
+
 hipError_t launch_mx4_linear(const MxLinearJob &j, hipStream_t s) {
-    // Rows on 16-byte boundaries (8 for the staged 16-bit loads would do).
-    const int64_t bytes = j.type == SGEMM_TYPE_F32 ? 4 : 2;
-    const int vec = ((uintptr_t)j.x & 15) == 0 && (j.ldx * bytes & 15) == 0;
     switch (j.type) {
-    case SGEMM_TYPE_F32: return launch_tokens<SGEMM_TYPE_F32, true>(j, vec, s);
-    case SGEMM_TYPE_F16: return launch_tokens<SGEMM_TYPE_F16, true>(j, vec, s);
-    case SGEMM_TYPE_BF16:
-        return vec ? launch_tokens<SGEMM_TYPE_BF16, false>(j, vec, s) : launch_tokens<SGEMM_TYPE_BF16, true>(j, vec, s);
+    case SGEMM_TYPE_F32: return launch_type<SGEMM_TYPE_F32>(j, s);
+    case SGEMM_TYPE_F16: return launch_type<SGEMM_TYPE_F16>(j, s);
+    case SGEMM_TYPE_BF16: return launch_type<SGEMM_TYPE_BF16>(j, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -8,92 +8,115 @@
 // G_e and U_e are rows [2 e F, 2 e F + F) and [2 e F + F, 2 e F + 2 F) of
 // `up` (2 E F x H), D_e rows [e H, e H + H) of `down` (E H x F).
 //
-// Bound by reading the chosen experts once: 3 F H 0.53 bytes each.  Three
-// kernels:
-//   route   logits in 64 bits (which expert is chosen must not hang on the
-//           order of a sum), the tokens as bf16 pieces, and, by the last
-//           workgroup of a group of tokens to arrive, choice and weights
-//   up      a workgroup takes 16 inner columns of one expert: their gate and
-//           up rows, all tokens of the expert; writes silu(g) * u, again as
-//           bf16 pieces
-//   down    a workgroup takes 16 rows of the output and every expert: its
-//           waves share the (expert, slab) list evenly and add p_e times
-//           their part into sums of their own, which are added in wave order
-// Every sum has a fixed order: results repeat bit for bit.  Activations are
-// held to 24 bits (three pieces) for fp32 outputs and to 16 (two) for 16-bit
-// ones, whose own rounding is at least 32 times coarser.
+// Bound by reading the chosen experts once: 3 F H 0.53 bytes each.
+//
+// Logits are summed in 64 bits: which expert is chosen must not hang on the
+// order of a sum.  The inner activations enter the second product as bf16
+// pieces: three (24 bits) for fp32 outputs, two (16 bits) for
+// 16-bit ones, whose own rounding is at least 32 times coarser.  Every sum has
+// a fixed order: results repeat bit for bit.
+//
+// Few choices (tokens * top <= kFew): three kernels.
+//   logits    a wave takes an expert
+//   up_few    a workgroup takes one choice and a run of inner columns; it
+//             ranks the token's experts by itself (a kernel for that alone
+//             costs more than all of them doing it)
+//   down_few  a workgroup takes 16 rows of the output and all choices: its
+//             waves share the (choice, slab) list evenly and add p_e times
+//             their part into sums of their own, added in wave order
+// More: five.
+//   logits, choose
+//   up        a workgroup takes an expert and a run of inner columns, for all
+//             tokens of the expert, 16 at a time (mx4_thin.h)
+//   down      the same for rows of the output; writes each choice's part
+//   join      adds a token's parts, times their weights, best first
+#include <type_traits>
+
 #include "mx4_thin.h"
 
 namespace sgemm {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kFew = 16;
+// Row tiles that `up` adds up at a time, and whether its registers let a CU
+// hold two workgroups.
+constexpr int up_group(int ks) { return ks >= 2 ? 2 : 4; }
+constexpr bool up_two_on_a_cu(int pieces, int ks) { return pieces * ks <= 2; }
 constexpr int act_pieces(int type) { return type == SGEMM_TYPE_F32 ? 3 : 2; }
 
 // Scratch memory, every part 256-byte aligned.
 struct Scratch {
-    double *logits;      // tokens x experts
-    int *chosen;         // tokens x top
-    float *weight;       // tokens x top
-    uint16_t *x;         // pieces x tokens x hp
-    uint16_t *act;       // pieces x (tokens * top) x fp
-    int64_t bytes;
+    double *logits;   // tokens x experts
+    int *chosen;      // tokens x top
+    float *weight;    // tokens x top
+    uint16_t *act;    // pieces x (tokens * top) x ld_act (inner rounded up to 16), zeros beyond inner
+    float *part;      // (tokens * top) x ld_part; not with few choices
+    int64_t ld_act, ld_part, bytes;
 };
-
-inline __host__ __device__ int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 
 Scratch layout(char *p, int tokens, int hidden, int inner, int experts, int top, int type) {
     Scratch s;
     int64_t at = 0;
-    const auto take = [&](int64_t n) { const int64_t here = at; at += up256(n); return p + here; };
+    const auto take = [&](int64_t n) { const int64_t here = at; at += (n + 255) & ~(int64_t)255; return p + here; };
+    const int64_t all = (int64_t)tokens * top;
+    s.ld_act = ((int64_t)inner + 15) / 16 * 16;
+    s.ld_part = ((int64_t)hidden + 15) / 16 * 16;
     s.logits = (double *)take((int64_t)tokens * experts * 8);
-    s.chosen = (int *)take((int64_t)tokens * top * 4);
-    s.weight = (float *)take((int64_t)tokens * top * 4);
-    s.x = (uint16_t *)take((int64_t)mx_pieces(type) * tokens * mx_slabs(hidden) * kMxSlab * 2);
-    s.act = (uint16_t *)take((int64_t)act_pieces(type) * tokens * top * mx_slabs(inner) * kMxSlab * 2);
+    s.chosen = (int *)take(all * 4);
+    s.weight = (float *)take(all * 4);
+    s.act = (uint16_t *)take(act_pieces(type) * all * s.ld_act * 2);
+    s.part = (float *)take(all > kFew ? all * s.ld_part * 4 : 0);
     s.bytes = at;
     return s;
 }
 
-// ---- route ----
+// ---- router ----
 
+// A wave takes one expert and TT tokens.
 template <int TYPE, int TT>
 __global__ __launch_bounds__(256) void logits_kernel(MxMoeJob j, Scratch s, int vec) {
     typedef typename MxType<TYPE>::T T;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int e = blockIdx.x * 4 + wave, t0 = blockIdx.y * TT;
-    const int hp = mx_slabs(j.hidden) * kMxSlab;
     const T *r = (const T *)j.router + (e < j.experts ? e : 0) * j.ldr;
     const T *x[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) x[t] = (const T *)j.x + (t0 + t < j.tokens ? t0 + t : t0) * j.ldx;
     double sum[TT] = {};
-    for (int h = 8 * lane; h < j.hidden; h += 512) {
-        float w[8], v[8];
+    auto add = [&](const float (&w)[8], const float (&v)[TT][8]) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[t] = fma((double)w[i], (double)v[t][i], sum[t]);
+    };
+    int h = 8 * lane;
+    if (vec) {
+        // Two steps' loads in flight.
+        for (; h + 512 + 8 <= j.hidden; h += 1024) {
+            float w[2][8], v[2][TT][8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                mx_load8<TYPE>(r + h + 512 * k, w[k]);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) mx_load8<TYPE>(x[t] + h + 512 * k, v[k][t]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) add(w[k], v[k]);
+        }
+    }
+    for (; h < j.hidden; h += 512) {
+        float w[8], v[TT][8];
         mx_load_edge8<TYPE>(r, h, j.hidden, vec, w);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            mx_load_edge8<TYPE>(x[t], h, j.hidden, vec, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[t] = fma((double)w[i], (double)v[i], sum[t]);
-        }
+        for (int t = 0; t < TT; ++t) mx_load_edge8<TYPE>(x[t], h, j.hidden, vec, v[t]);
+        add(w, v);
     }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) sum[t] += __shfl_xor(sum[t], off, 64);
-        if (lane == 0 && e < j.experts && t0 + t < j.tokens) s.logits[(t0 + t) * j.experts + e] = sum[t];
+        if (lane == 0 && e < j.experts && t0 + t < j.tokens) s.logits[(int64_t)(t0 + t) * j.experts + e] = sum[t];
     }
-    // The tokens as pieces, zeros up to whole slabs; the group's workgroups share the columns.
-    constexpr int P = mx_pieces(TYPE);
-    for (int h = blockIdx.x * 256 + threadIdx.x; h < hp; h += gridDim.x * 256)
-        for (int t = 0; t < TT && t0 + t < j.tokens; ++t) {
-            uint16_t p[P];
-            const T *row = (const T *)j.x + (t0 + t) * j.ldx;
-            mx_split<P>(h < j.hidden ? MxType<TYPE>::load(row + h) : 0.0f, p);
-#pragma unroll
-            for (int i = 0; i < P; ++i) s.x[((int64_t)i * j.tokens + t0 + t) * hp + h] = p[i];
-        }
 }
 
 // A logit as an integer of the same order: NaN above all, -0 equal to 0.
@@ -103,277 +126,294 @@ __device__ __forceinline__ int64_t order_key(double v) {
     return b < 0 ? b ^ INT64_MAX : b;
 }
 
-// One workgroup per token: an expert's rank is the number of experts before it.
-__global__ __launch_bounds__(256) void choose_kernel(MxMoeJob j, Scratch s) {
-    __shared__ int64_t key[SGEMM_MX4_MAX_EXPERTS];
-    __shared__ float ex[SGEMM_MX4_MAX_EXPERTS];
-    __shared__ double best;
-    __shared__ float part[4];
-    __shared__ float picked[SGEMM_MX4_MAX_TOP];
-    const int t = blockIdx.x, tid = threadIdx.x;
-    const double *l = s.logits + (int64_t)t * j.experts;
-    for (int e = tid; e < j.experts; e += 256) key[e] = order_key(l[e]);
+struct Choice {
+    int64_t key[SGEMM_MX4_MAX_EXPERTS];
+    int rank[SGEMM_MX4_MAX_EXPERTS];
+    float part[kThinWaves];
+    float value[SGEMM_MX4_MAX_TOP];    // exponentials
+    int expert[SGEMM_MX4_MAX_TOP];
+};
+
+// Ranks a token's experts, by the whole workgroup: an expert's rank is the
+// number of experts before it, counted in as many pieces as there are threads
+// for.
+__device__ __forceinline__ void rank_experts(const MxMoeJob &j, const double *l, Choice &c) {
+    const int tid = threadIdx.x, n = j.experts;
+    for (int e = tid; e < n; e += kThinThreads) c.key[e] = order_key(l[e]), c.rank[e] = 0;
     __syncthreads();
-    int rank[SGEMM_MX4_MAX_EXPERTS / 256];
-#pragma unroll
-    for (int i = 0; i < SGEMM_MX4_MAX_EXPERTS / 256; ++i) {
-        const int e = tid + 256 * i;
-        rank[i] = 0;
-        if (e >= j.experts) continue;
-        const int64_t mine = key[e];
-        int n = 0;
-        for (int o = 0; o < j.experts; ++o) n += key[o] > mine || (key[o] == mine && o < e);
-        rank[i] = n;
-        if (n == 0) best = l[e];
+    const int pieces = n < kThinThreads ? kThinThreads / n : 1;
+    for (int i = tid; i < n * pieces; i += kThinThreads) {
+        const int e = i % n, piece = i / n, from = n * piece / pieces, to = n * (piece + 1) / pieces;
+        const int64_t mine = c.key[e];
+        int before = 0;
+#pragma unroll 8
+        for (int o = from; o < to; ++o) before += c.key[o] > mine || (c.key[o] == mine && o < e);
+        if (before > 0) atomicAdd(&c.rank[e], before);   // whole numbers: any order
     }
     __syncthreads();
+    for (int e = tid; e < n; e += kThinThreads) {
+        const int r = c.rank[e];
+        if (r < j.top) c.expert[r] = e;
+    }
+    __syncthreads();
+}
+
+// Writes the choices of token t, best first, and their weights, after
+// rank_experts.
+__device__ __forceinline__ void write_choice(const MxMoeJob &j, const Scratch &s, int t, const double *l, Choice &c) {
+    const int tid = threadIdx.x, n = j.experts;
+    const double best = l[c.expert[0]];
     float total = 0.0f;
-#pragma unroll
-    for (int i = 0; i < SGEMM_MX4_MAX_EXPERTS / 256; ++i) {
-        const int e = tid + 256 * i;
-        if (e >= j.experts) continue;
+    for (int e = tid; e < n; e += kThinThreads) {
         const float v = expf((float)(l[e] - best));
         total += v;
-        if (rank[i] < j.top) {
-            picked[rank[i]] = v;
-            s.chosen[t * j.top + rank[i]] = e;
-        }
+        if (c.rank[e] < j.top) c.value[c.rank[e]] = v;
     }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) total += __shfl_xor(total, off, 64);
-    if ((tid & 63) == 0) part[tid >> 6] = total;
+    if ((tid & 63) == 0) c.part[tid >> 6] = total;
     __syncthreads();
     if (tid < j.top) {
         float sum = 0.0f;
         if (j.norm)
-            for (int i = 0; i < j.top; ++i) sum += picked[i];
+            for (int i = 0; i < j.top; ++i) sum += c.value[i];
         else
-            sum = ((part[0] + part[1]) + part[2]) + part[3];
-        s.weight[t * j.top + tid] = picked[tid] / sum;
+            for (int i = 0; i < kThinWaves; ++i) sum += c.part[i];
+        s.chosen[t * j.top + tid] = c.expert[tid];
+        s.weight[t * j.top + tid] = c.value[tid] / sum;
     }
 }
 
+__global__ __launch_bounds__(kThinThreads) void choose_kernel(MxMoeJob j, Scratch s) {
+    __shared__ Choice c;
+    const double *l = s.logits + (int64_t)blockIdx.x * j.experts;
+    rank_experts(j, l, c);
+    write_choice(j, s, blockIdx.x, l, c);
+}
+
+// The choices of expert e, in any order (a token's result does not depend on
+// its place); returns their number.
+__device__ __forceinline__ int list_tokens(const int *chosen, int all, int e, int *list, int *count) {
+    if (threadIdx.x == 0) *count = 0;
+    __syncthreads();
+    for (int a = threadIdx.x; a < all; a += kThinThreads)
+        if (chosen[a] == e) list[atomicAdd(count, 1)] = a;
+    __syncthreads();
+    return *count;
+}
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
 // ---- up ----
 
-template <int TYPE, int MT>
-__global__ __launch_bounds__(64 * kWaves) void up_kernel(MxMoeJob j, Scratch s) {
-    constexpr int P = mx_pieces(TYPE), PA = act_pieces(TYPE), U = 2;
-    __shared__ __attribute__((aligned(16))) f32v4 red[kWaves * 2 * MT * 64];
-    __shared__ int list[SGEMM_MX4_MAX_TOKENS];
-    __shared__ int count, earlier;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int all = j.tokens * j.top, f0 = blockIdx.x * 16;
-    // blockIdx.y: an expert, or, with fewer choices than experts, a choice,
-    // which stands for its expert if none before it does.
-    const bool by_choice = all < j.experts;
-    const int e = by_choice ? s.chosen[blockIdx.y] : blockIdx.y;
-    if (tid == 0) count = 0, earlier = 0;
-    __syncthreads();
-    for (int a = tid; a < all; a += 64 * kWaves)
-        if (s.chosen[a] == e) {
-            list[atomicAdd(&count, 1)] = a;   // any order: a token's result does not depend on its place
-            if (by_choice && a < (int)blockIdx.y) earlier = 1;
-        }
-    __syncthreads();
-    const int n = count;
-    if (n == 0 || earlier) return;
-
-    const int slabs = mx_slabs(j.hidden), hp = slabs * kMxSlab, fp = mx_slabs(j.inner) * kMxSlab;
-    const int64_t rows = (int64_t)2 * j.experts * j.inner, plane = mx_plane_rows(rows);
-    const int l16 = lane & 15, q = lane >> 4;
-    const int f = f0 + l16 < j.inner ? f0 + l16 : j.inner - 1;
-    const int64_t rg = (int64_t)2 * e * j.inner + f, ru = rg + j.inner;
-    const int64_t rowb = (int64_t)slabs * kMxSlabBytes;
-    const uint16_t *x[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int i = mt * 16 + l16 < n ? mt * 16 + l16 : n - 1;
-        x[mt] = s.x + (int64_t)(list[i] / j.top) * hp + 32 * q;
+template <int TYPE, int KS, bool FEW>
+__global__ __launch_bounds__(kThinThreads, up_two_on_a_cu(mx_pieces(TYPE), KS) ? 4 : 2) void up_kernel(MxMoeJob j, Scratch s,
+                                                                                                      MxWeights w, int vec,
+                                                                                                      int per) {
+    typedef typename MxType<TYPE>::T T;
+    constexpr int G = up_group(KS), PA = act_pieces(TYPE);
+    const int all = j.tokens * j.top;
+    // red, then the sums kept from one piece of K to the next.
+    extern __shared__ __attribute__((aligned(16))) f32v4 red[];
+    __shared__ int list[SGEMM_MX4_MAX_TOKENS], count;
+    __shared__ std::conditional_t<FEW, Choice, int> choice;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15;
+    MxTokens<TYPE, mx_pieces(TYPE), KS, 1> x;
+    int e = blockIdx.y, n = 1;
+    if constexpr (FEW) {
+        // blockIdx.y: a choice.  Its token is known before its expert.
+        const int t = blockIdx.y / j.top;
+        const T *row[1] = {l16 == 0 ? (const T *)j.x + (int64_t)t * j.ldx : nullptr};
+        x.load(row, wave, j.hidden, vec, lane >> 4);
+        rank_experts(j, s.logits + (int64_t)t * j.experts, choice);
+        e = choice.expert[blockIdx.y % j.top];
+    } else {
+        n = list_tokens(s.chosen, all, e, list, &count);
     }
-    f32v4 acc[2][MT];
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) acc[r][mt] = f32v4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (f0 < j.inner)
-        for (int s0 = wave; s0 < slabs; s0 += kWaves * U) {
-            MxBlock b[U][2];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int slab = s0 + kWaves * u;
-                b[u][0] = mx_block(j.up + rg * rowb, (const uint32_t *)j.sup + rg, plane, slab, q, slab < slabs);
-                b[u][1] = mx_block(j.up + ru * rowb, (const uint32_t *)j.sup + ru, plane, slab, q, slab < slabs);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int slab = s0 + kWaves * u;
-                if (slab >= slabs) break;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    if (mt * 16 >= n) break;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint4 xs[P];
-#pragma unroll
-                        for (int p = 0; p < P; ++p)
-                            xs[p] = *(const uint4 *)(x[mt] + (int64_t)p * j.tokens * hp + slab * kMxSlab + 8 * k);
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const uint4 c = b[u][r].codes;
-                            const bf16v8 w = mx_bf16x8(k == 0 ? c.x : k == 1 ? c.y : k == 2 ? c.z : c.w, mx_scale(b[u][r], q));
-#pragma unroll
-                            for (int p = 0; p < P; ++p) acc[r][mt] = mx_mfma(w, xs[p], acc[r][mt]);
-                        }
-                    }
-                }
-            }
+    // Row tiles come in pairs: 16 rows of the gate, the same 16 of U.
+    const int tiles = 2 * ((j.inner + 15) / 16), first = blockIdx.x * per, end = first + per < tiles ? first + per : tiles;
+    const int64_t base = (int64_t)2 * e * j.inner;
+    const auto row_of = [&](int tile) -> int64_t {
+        const int f = (tile >> 1) * 16 + l16;
+        return base + (f < j.inner ? f : j.inner - 1) + (tile & 1 ? j.inner : 0);
+    };
+    for (int i0 = 0; i0 < n; i0 += 16) {
+        const T *row[1] = {nullptr};
+        if (i0 + l16 < n) {
+            const int a = FEW ? (int)blockIdx.y : list[i0 + l16];
+            row[0] = (const T *)j.x + (int64_t)(a / j.top) * j.ldx;
         }
+        for (int s0 = 0; s0 < w.slabs; s0 += kThinWaves * KS) {
+            if (!FEW || s0 > 0) x.load(row, s0 + wave, j.hidden, vec, lane >> 4);
+            mx_stream<2, G>(x, w, s0 + wave, first, end, red, red + kThinWaves * G * 64, s0 == 0, s0 + kThinWaves * KS >= w.slabs,
+                            row_of, [&](int tile, int, int l, const f32v4(&v)[2]) {
+                                const int i = i0 + (l & 15), f = (tile >> 1) * 16 + 4 * (l >> 4);
+                                if (i >= n) return;
+                                uint16_t p[4][PA];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+                                for (int c = 0; c < 4; ++c)
+                                    mx_split<PA>(f + c < j.inner ? silu(v[0][c]) * v[1][c] : 0.0f, p[c]);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) red[((wave * 2 + r) * MT + mt) * 64 + lane] = acc[r][mt];
-    __syncthreads();
-    for (int i = tid; i < MT * 64; i += 64 * kWaves) {
-        const int l = i & 63, mt = i >> 6, t = mt * 16 + (l & 15);
-        if (t >= n) continue;
-        f32v4 g = red[i], u = red[MT * 64 + i];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) g += red[w * (2 * MT * 64) + i], u += red[(w * 2 + 1) * MT * 64 + i];
-        const int fc = f0 + 4 * (l >> 4);
-        uint16_t p[4][PA];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            mx_split<PA>(fc + c < j.inner ? g[c] / (1.0f + expf(-g[c])) * u[c] : 0.0f, p[c]);
-#pragma unroll
-        for (int k = 0; k < PA; ++k)
-            *(uint2 *)(s.act + ((int64_t)k * all + list[t]) * fp + fc) =
-                uint2{(uint32_t)p[0][k] | (uint32_t)p[1][k] << 16, (uint32_t)p[2][k] | (uint32_t)p[3][k] << 16};
+                                for (int k = 0; k < PA; ++k)
+                                    *(uint2 *)(s.act + ((int64_t)k * all + (FEW ? (int)blockIdx.y : list[i])) * s.ld_act + f) =
+                                        uint2{(uint32_t)p[0][k] | (uint32_t)p[1][k] << 16,
+                                              (uint32_t)p[2][k] | (uint32_t)p[3][k] << 16};
+                            });
+        }
     }
+    if constexpr (FEW)
+        if (blockIdx.x == 0 && blockIdx.y % j.top == 0) {
+            const int t = blockIdx.y / j.top;
+            write_choice(j, s, t, s.logits + (int64_t)t * j.experts, choice);
+        }
 }
 
 // ---- down ----
 
-template <int TYPE, int MT>
-__global__ __launch_bounds__(64 * kWaves) void down_kernel(MxMoeJob j, Scratch s) {
-    typedef typename MxType<TYPE>::T T;
-    constexpr int PA = act_pieces(TYPE), U = 4;
-    __shared__ __attribute__((aligned(16))) float ys[kWaves * 16 * MT * 16];   // a wave's sums: token, row
-    __shared__ int first[SGEMM_MX4_MAX_EXPERTS + 1], place[SGEMM_MX4_MAX_EXPERTS], active[SGEMM_MX4_MAX_EXPERTS];
-    __shared__ uint16_t list[SGEMM_MX4_MAX_TOKENS * SGEMM_MX4_MAX_TOP];
-    __shared__ int n_active;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int all = j.tokens * j.top;
-    // The choices sorted by expert, and the experts that have any.
-    for (int e = tid; e < j.experts; e += 64 * kWaves) place[e] = 0;
-    for (int i = tid; i < kWaves * 16 * MT * 16; i += 64 * kWaves) ys[i] = 0.0f;
-    __syncthreads();
-    for (int a = tid; a < all; a += 64 * kWaves) atomicAdd(&place[s.chosen[a]], 1);
-    __syncthreads();
-    if (wave == 0) {
-        int sum = 0, act = 0;
-        for (int e0 = 0; e0 < j.experts; e0 += 64) {
-            const int e = e0 + lane, c = e < j.experts ? place[e] : 0;
-            int run = c;
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                const int v = __shfl_up(run, off, 64);
-                if (lane >= off) run += v;
-            }
-            const uint64_t some = __ballot(c > 0);
-            if (e < j.experts) first[e] = sum + run - c;
-            if (c > 0) active[act + __popcll(some & ((1ull << lane) - 1))] = e;
-            sum += __shfl(run, 63, 64);
-            act += __popcll(some);
+template <int TYPE, int KS>
+__global__ __launch_bounds__(kThinThreads, 2) void down_kernel(MxMoeJob j, Scratch s, MxWeights w, int per) {
+    constexpr int G = 4;
+    extern __shared__ __attribute__((aligned(16))) f32v4 red[];
+    __shared__ int list[SGEMM_MX4_MAX_TOKENS], count;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, e = blockIdx.y;
+    const int n = list_tokens(s.chosen, j.tokens * j.top, e, list, &count);
+    const int tiles = (j.hidden + 15) / 16, first = blockIdx.x * per, end = first + per < tiles ? first + per : tiles;
+    for (int i0 = 0; i0 < n; i0 += 16) {
+        const uint16_t *row = i0 + l16 < n ? s.act + (int64_t)list[i0 + l16] * s.ld_act : nullptr;
+        for (int s0 = 0; s0 < w.slabs; s0 += kThinWaves * KS) {
+            MxTokens<SGEMM_TYPE_BF16, act_pieces(TYPE), KS, 1> x;
+            x.load_pieces(row, (int64_t)j.tokens * j.top * s.ld_act, s0 + wave, (int)s.ld_act, lane >> 4);
+            mx_stream<1, G>(
+                x, w, s0 + wave, first, end, red, red + kThinWaves * G * 64, s0 == 0, s0 + kThinWaves * KS >= w.slabs,
+                [&](int tile) -> int64_t {
+                    const int h = tile * 16 + l16;
+                    return (int64_t)e * j.hidden + (h < j.hidden ? h : j.hidden - 1);
+                },
+                [&](int tile, int, int l, const f32v4(&v)[1]) {
+                    const int i = i0 + (l & 15);
+                    if (i < n) *(f32v4 *)(s.part + (int64_t)list[i] * s.ld_part + tile * 16 + 4 * (l >> 4)) = v[0];
+                });
         }
-        if (lane == 0) first[j.experts] = sum, n_active = act;
     }
-    __syncthreads();
-    for (int e = tid; e < j.experts; e += 64 * kWaves) place[e] = first[e];
-    __syncthreads();
-    for (int a = tid; a < all; a += 64 * kWaves) list[atomicAdd(&place[s.chosen[a]], 1)] = (uint16_t)a;
-    __syncthreads();
+}
 
-    const int slabs = mx_slabs(j.inner), fp = slabs * kMxSlab;
-    const int64_t plane = mx_plane_rows((int64_t)j.experts * j.hidden), rowb = (int64_t)slabs * kMxSlabBytes;
-    const int l16 = lane & 15, q = lane >> 4, h0 = blockIdx.x * 16;
+template <int TYPE>
+__global__ __launch_bounds__(256) void join_kernel(MxMoeJob j, Scratch s) {
+    const int h = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+    if (h >= j.hidden) return;
+    float sum = 0.0f;
+    for (int i = t * j.top; i < (t + 1) * j.top; ++i) sum = fmaf(s.weight[i], s.part[i * s.ld_part + h], sum);
+    ((typename MxType<TYPE>::T *)j.y)[t * j.ldy + h] = MxType<TYPE>::from(sum);
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kThinThreads) void down_few_kernel(MxMoeJob j, Scratch s, MxWeights w) {
+    typedef typename MxType<TYPE>::T T;
+    constexpr int P = act_pieces(TYPE), U = 4;
+    __shared__ float ys[kThinWaves][kFew][16];   // a wave's sums: token, row
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
+    const int all = j.tokens * j.top, h0 = blockIdx.x * 16;
     const int h = h0 + l16 < j.hidden ? h0 + l16 : j.hidden - 1;
-    float *mine = ys + wave * (16 * MT * 16);
-    // This wave's part of the (active expert, slab) list.
-    const int64_t items = (int64_t)n_active * slabs;
-    int64_t at = items * wave / kWaves;
-    const int64_t end = items * (wave + 1) / kWaves;
-    while (at < end) {
-        const int i = (int)(at / slabs), s_begin = (int)(at - (int64_t)i * slabs);
-        const int s_end = end - at < slabs - s_begin ? s_begin + (int)(end - at) : slabs;
+    for (int i = lane; i < kFew * 16; i += 64) (&ys[wave][0][0])[i] = 0.0f;
+    // This wave's part of the (choice, slab) list.
+    const int64_t items = (int64_t)all * w.slabs;
+    int64_t at = items * wave / kThinWaves;
+    const int64_t stop = items * (wave + 1) / kThinWaves;
+    while (at < stop) {
+        const int a = (int)(at / w.slabs), s_begin = (int)(at - (int64_t)a * w.slabs);
+        const int s_end = stop - at < w.slabs - s_begin ? s_begin + (int)(stop - at) : w.slabs;
         at += s_end - s_begin;
-        const int e = active[i], from = first[e], n = first[e + 1] - from;
-        const int64_t r = (int64_t)e * j.hidden + h;
-        const uint8_t *row = j.down + r * rowb;
-        const uint32_t *words = (const uint32_t *)j.sdown + r;
-        const uint16_t *x[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int k = mt * 16 + l16 < n ? mt * 16 + l16 : n - 1;
-            x[mt] = s.act + (int64_t)list[from + k] * fp + 32 * q;
-        }
-        f32v4 acc[MT];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) acc[mt] = f32v4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int64_t r = (int64_t)s.chosen[a] * j.hidden + h;
+        const float weight = s.weight[a];
+        const uint16_t *act = s.act + a * s.ld_act;
+        f32v4 acc{0.0f, 0.0f, 0.0f, 0.0f};
         for (int s0 = s_begin; s0 < s_end; s0 += U) {
             MxBlock b[U];
+            uint4 x[U][4][P];
 #pragma unroll
-            for (int u = 0; u < U; ++u) b[u] = mx_block(row, words, plane, s0 + u, q, s0 + u < s_end);
+            for (int u = 0; u < U; ++u) b[u] = s0 + u < s_end ? w.load(r, s0 + u, q) : MxBlock{uint4{0, 0, 0, 0}, 0};
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {   // one token: the operand's first column
+                        const int c = (s0 + u) * kMxSlab + 32 * q + 8 * k;
+                        x[u][k][p] = l16 == 0 && s0 + u < s_end && c < s.ld_act ? *(const uint4 *)(act + p * all * s.ld_act + c)
+                                                                                : uint4{0, 0, 0, 0};
+                    }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (s0 + u >= s_end) break;
+                const uint32_t c[4] = {b[u].codes.x, b[u].codes.y, b[u].codes.z, b[u].codes.w};
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    if (mt * 16 >= n) break;
+                for (int k = 0; k < 4; ++k) {
+                    const bf16v8 m = mx_bf16x8(c[k], mx_scale(b[u], q));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint4 c = b[u].codes;
-                        const bf16v8 w = mx_bf16x8(k == 0 ? c.x : k == 1 ? c.y : k == 2 ? c.z : c.w, mx_scale(b[u], q));
-#pragma unroll
-                        for (int p = 0; p < PA; ++p) {
-                            const uint4 xs = *(const uint4 *)(x[mt] + (int64_t)p * all * fp + (s0 + u) * kMxSlab + 8 * k);
-                            acc[mt] = mx_mfma(w, xs, acc[mt]);
-                        }
-                    }
+                    for (int p = 0; p < P; ++p) acc = mx_mfma(m, x[u][k][p], acc);
                 }
             }
         }
-        // Lane l: rows 4 (l / 16) .. + 3 for the expert's token l % 16.
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int k = mt * 16 + l16;
-            if (k < n) {
-                const int a = list[from + k];
-                const float p = s.weight[a];
-                f32v4 *y = (f32v4 *)(mine + (a / j.top) * 16 + 4 * q);
-                *y += p * acc[mt];
-            }
+        if (l16 == 0) {
+            f32v4 *y = (f32v4 *)&ys[wave][a / j.top][4 * q];
+            *y += weight * acc;
         }
     }
     __syncthreads();
-    for (int i = tid; i < j.tokens * 16; i += 64 * kWaves) {
+    for (int i = tid; i < j.tokens * 16; i += kThinThreads) {
         const int t = i >> 4, r = i & 15;
-        float sum = ys[i];
+        float sum = ys[0][t][r];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) sum += ys[w * (16 * MT * 16) + i];
+        for (int k = 1; k < kThinWaves; ++k) sum += ys[k][t][r];
         if (h0 + r < j.hidden) ((T *)j.y)[t * j.ldy + h0 + r] = MxType<TYPE>::from(sum);
     }
 }
 
-template <int TYPE, int MT>
-hipError_t launch_experts(MxMoeJob &j, Scratch &s, hipStream_t stream) {
-    void *params[] = {&j, &s};
-    const int all = j.tokens * j.top;
-    hipError_t e = hipLaunchKernel((const void *)up_kernel<TYPE, MT>,
-                                   dim3((unsigned)(mx_slabs(j.inner) * kMxSlab / 16), (unsigned)(all < j.experts ? all : j.experts)),
-                                   dim3(64 * kWaves), params, 0, stream);
-    if (e != hipSuccess) return e;
-    return hipLaunchKernel((const void *)down_kernel<TYPE, MT>, dim3((unsigned)((j.hidden + 15) / 16)), dim3(64 * kWaves),
-                           params, 0, stream);
+// ---- launches ----
+
+// Workgroups along the rows: enough that `slots` times as many are `fill`, and
+// not more tiles each than `most`.
+int groups_of(int tiles, int unit, int slots, int fill, int most) {
+    const int want = (fill + slots - 1) / slots, least = (tiles + most - 1) / most;
+    const int groups = want > least ? want : least, units = (tiles + unit - 1) / unit;
+    return groups < units ? groups : units;
+}
+
+// LDS of a streaming kernel, and the most tiles a workgroup takes, when K
+// comes in several pieces (their sums stay in LDS).
+constexpr int kCarryTiles = 32;
+
+template <int TYPE, int KS, bool FEW>
+hipError_t launch_up(MxMoeJob &j, Scratch &s, int vec, hipStream_t stream) {
+    constexpr int G = up_group(KS);
+    MxWeights w = mx_weights(j.up, j.sup, (int64_t)2 * j.experts * j.inner, j.hidden);
+    const int tiles = 2 * ((j.inner + 15) / 16), all = j.tokens * j.top, slots = FEW ? all : all < j.experts ? all : j.experts;
+    const bool pieces = w.slabs > kThinWaves * KS;
+    int per = mx_share(tiles, groups_of(tiles, 2, slots, FEW && !up_two_on_a_cu(mx_pieces(TYPE), KS) ? 256 : 512, pieces ? kCarryTiles : tiles), 2);
+    const int bytes = (kThinWaves * G + (pieces ? kCarryTiles : 0)) * 64 * 16;
+    void *params[] = {&j, &s, &w, &vec, &per};
+    return hipLaunchKernel((const void *)up_kernel<TYPE, KS, FEW>,
+                           dim3((unsigned)((tiles + per - 1) / per), (unsigned)(FEW ? all : j.experts)), dim3(kThinThreads), params,
+                           bytes, stream);
+}
+
+template <int TYPE, bool FEW>
+hipError_t launch_up_slabs(MxMoeJob &j, Scratch &s, int vec, hipStream_t stream) {
+    const int need = (mx_slabs(j.hidden) + kThinWaves - 1) / kThinWaves;
+    if constexpr (TYPE == SGEMM_TYPE_BF16)
+        if (need > 2) return launch_up<TYPE, 4, FEW>(j, s, vec, stream);
+    return need > 1 ? launch_up<TYPE, 2, FEW>(j, s, vec, stream) : launch_up<TYPE, 1, FEW>(j, s, vec, stream);
+}
+
+template <int TYPE, int KS>
+hipError_t launch_down(MxMoeJob &j, Scratch &s, hipStream_t stream) {
+    MxWeights w = mx_weights(j.down, j.sdown, (int64_t)j.experts * j.hidden, j.inner);
+    const int tiles = (j.hidden + 15) / 16, all = j.tokens * j.top, slots = all < j.experts ? all : j.experts;
+    const bool pieces = w.slabs > kThinWaves * KS;
+    int per = mx_share(tiles, groups_of(tiles, 1, slots, 512, pieces ? kCarryTiles : tiles), 1);
+    const int bytes = (kThinWaves * 4 + (pieces ? kCarryTiles : 0)) * 64 * 16;
+    void *params[] = {&j, &s, &w, &per};
+    return hipLaunchKernel((const void *)down_kernel<TYPE, KS>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)j.experts),
+                           dim3(kThinThreads), params, bytes, stream);
 }
 
 template <int TYPE>
@@ -381,7 +421,8 @@ hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
     MxMoeJob j = job;
     Scratch s = layout(j.scratch, j.tokens, j.hidden, j.inner, j.experts, j.top, TYPE);
     const int64_t b = TYPE == SGEMM_TYPE_F32 ? 4 : 2;
-    int vec = ((uintptr_t)j.x & 15) == 0 && ((uintptr_t)j.router & 15) == 0 && (j.ldx * b & 15) == 0 && (j.ldr * b & 15) == 0;
+    int vec_x = ((uintptr_t)j.x & 15) == 0 && (j.ldx * b & 15) == 0;
+    int vec = vec_x && ((uintptr_t)j.router & 15) == 0 && (j.ldr * b & 15) == 0;
     void *params[] = {&j, &s, &vec};
     const unsigned ge = (unsigned)((j.experts + 3) / 4);
     hipError_t e = j.tokens < 4 ? hipLaunchKernel((const void *)logits_kernel<TYPE, 1>, dim3(ge, (unsigned)j.tokens), dim3(256),
@@ -389,11 +430,22 @@ hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
                                 : hipLaunchKernel((const void *)logits_kernel<TYPE, 4>, dim3(ge, (unsigned)((j.tokens + 3) / 4)),
                                                   dim3(256), params, 0, stream);
     if (e != hipSuccess) return e;
-    e = hipLaunchKernel((const void *)choose_kernel, dim3((unsigned)j.tokens), dim3(256), params, 0, stream);
+    if (j.tokens * j.top <= kFew) {
+        e = launch_up_slabs<TYPE, true>(j, s, vec_x, stream);
+        if (e != hipSuccess) return e;
+        MxWeights w = mx_weights(j.down, j.sdown, (int64_t)j.experts * j.hidden, j.inner);
+        void *down[] = {&j, &s, &w};
+        return hipLaunchKernel((const void *)down_few_kernel<TYPE>, dim3((unsigned)((j.hidden + 15) / 16)), dim3(kThinThreads), down,
+                               0, stream);
+    }
+    e = hipLaunchKernel((const void *)choose_kernel, dim3((unsigned)j.tokens), dim3(kThinThreads), params, 0, stream);
     if (e != hipSuccess) return e;
-    if (j.tokens <= 16) return launch_experts<TYPE, 1>(j, s, stream);
-    if (j.tokens <= 32) return launch_experts<TYPE, 2>(j, s, stream);
-    return launch_experts<TYPE, 4>(j, s, stream);
+    e = launch_up_slabs<TYPE, false>(j, s, vec_x, stream);
+    if (e != hipSuccess) return e;
+    e = mx_slabs(j.inner) > kThinWaves ? launch_down<TYPE, 2>(j, s, stream) : launch_down<TYPE, 1>(j, s, stream);
+    if (e != hipSuccess) return e;
+    return hipLaunchKernel((const void *)join_kernel<TYPE>, dim3((unsigned)((j.hidden + 255) / 256), (unsigned)j.tokens), dim3(256),
+                           params, 0, stream);
 }
 
 }  // namespace

@@ -1,25 +1,36 @@
-// The inner step of the products of a few float rows ("tokens") with 4-bit
-// weights, shared by the thin product and the expert layer.
+// The products of a few float rows ("tokens") with 4-bit weights, shared by
+// the thin product and the expert layer.
 //
-// A wave takes 16 rows of weights and one slab (128 columns) at a time and
-// multiplies it with up to 16 tokens on v_mfma_f32_16x16x32_bf16, the weights
-// as the first operand: lane l loads the 16 bytes (one block, 32 codes) of
-// row l % 16 and block q = l / 16, so a wave reads 64 bytes of each row, and
-// matrix step j = 0..3 takes codes 8 j .. 8 j + 7 of every lane.  The sum's
-// order along K does not matter as long as the tokens follow it: they are
-// taken at column 32 q + 8 j.
+// A workgroup of 8 waves owns a piece of K and streams rows of weights past
+// it.  A wave keeps its tokens' part of KS slabs (128 columns each) in operand
+// registers for as long as it lives and takes 16 rows of weights and those
+// slabs at a time: lane l loads the 16 bytes (one block, 32 codes) of row
+// l % 16 and block q = l / 16, so a wave reads 64 bytes of each row and
+// neighbouring waves the 64 bytes beside them.  On v_mfma_f32_16x16x32_bf16,
+// the weights as the first operand, step j = 0..3 takes codes 8 j .. 8 j + 7
+// of every lane; the sum's order along K does not matter as long as the
+// tokens follow it, so they are taken at column 32 q + 8 j.  The eight waves'
+// sums meet in LDS and are added in wave order, G tiles of rows at a time.
+//
+// (A wave that took the tokens anew for every 16 rows read four to twelve
+// bytes of them for each byte of weights and split them again each time: 13
+// fp32 tokens x 16384 against 5001 rows took 71 us.)
 //
 // Nothing is rounded on the way in.  A code times its scale is exact in bf16
-// (two bits of significand; the conversion instruction applies the scale).
-// A token value is given as P bf16 pieces that add up to it exactly: one for
-// bf16, two for fp16 (11 bits), three for fp32 (24 bits); each piece costs
-// one more matrix step, which the load of the weights hides.
+// (two bits of significand; the conversion instruction applies the scale).  A
+// token value is cut into P bf16 pieces that add up to it: one for bf16, two
+// for fp16 (11 bits), three for fp32 (24 bits); each piece costs one more
+// matrix step, which the loads of the weights hide.  bf16 ends at 2^-133, so
+// where all of a wave's values of an fp32 token lie below 2^-60 they are
+// taken 2^32 times larger and the wave's sum 2^32 times smaller: both exact,
+// and far from overflow with the largest weight.
 #pragma once
 
 #include "mx4.h"
 
 namespace sgemm {
 
+constexpr int kThinWaves = 8, kThinThreads = 64 * kThinWaves;
 constexpr int mx_pieces(int type) { return type == SGEMM_TYPE_BF16 ? 1 : type == SGEMM_TYPE_F16 ? 2 : 3; }
 
 // Codes 0..7 of a register, times the scale, as bf16.
@@ -31,8 +42,8 @@ __device__ __forceinline__ bf16v8 mx_bf16x8(uint32_t codes, float scale) {
     return bf16v8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// v as P bf16 pieces, cut (not rounded) from the top so that their sum is v.
-// An infinity or NaN stays whole in the first.
+// v as P bf16 pieces, cut (not rounded) from the top.  An infinity or NaN
+// stays whole in the first.
 template <int P>
 __device__ __forceinline__ void mx_split(float v, uint16_t (&p)[P]) {
     const uint32_t b = __float_as_uint(v);
@@ -47,21 +58,117 @@ __device__ __forceinline__ void mx_split(float v, uint16_t (&p)[P]) {
     }
 }
 
+// Eight values as P operand registers of 16 bytes.
+template <int P>
+__device__ __forceinline__ void mx_split8(const float (&v)[8], uint4 (&x)[P]) {
+    uint16_t p[8][P];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx_split<P>(v[i], p[i]);
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+        x[k] = uint4{(uint32_t)p[0][k] | (uint32_t)p[1][k] << 16, (uint32_t)p[2][k] | (uint32_t)p[3][k] << 16,
+                     (uint32_t)p[4][k] | (uint32_t)p[5][k] << 16, (uint32_t)p[6][k] | (uint32_t)p[7][k] << 16};
+}
+
+// Eight bf16 values of a row from column c on, zeros at and after `cols`.
+__device__ __forceinline__ uint4 mx_bf16_edge8(const uint16_t *row, int c, int cols, bool vec) {
+    if (vec && c + 8 <= cols) return *(const uint4 *)(row + c);
+    uint32_t u[4] = {0, 0, 0, 0};
+    if (c < cols)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < cols) u[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
+    return uint4{u[0], u[1], u[2], u[3]};
+}
+
+// What fp32 values whose largest magnitude has these bits are multiplied by.
+__device__ __forceinline__ float mx_lift(uint32_t largest) { return largest < 0x21800000u ? 0x1p32f : 1.0f; }
+
+// A wave's tokens: MT tiles of 16, KS slabs, P pieces.
+template <int TYPE, int P, int KS, int MT>
+struct MxTokens {
+    typedef typename MxType<TYPE>::T T;
+    uint4 x[KS][MT][4][P];
+    float back[MT];   // what sums of a token are multiplied by
+
+    // The lane's tokens are in row[mt] (NULL: none, zeros), its columns in
+    // slabs slab0 + kThinWaves i.
+    __device__ __forceinline__ void load(const T *const (&row)[MT], int slab0, int cols, bool vec, int q) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            back[mt] = 1.0f;
+            if constexpr (TYPE == SGEMM_TYPE_BF16 && P == 1) {
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const int c = (slab0 + kThinWaves * i) * kMxSlab + 32 * q + 8 * s;
+                        x[i][mt][s][0] = row[mt] ? mx_bf16_edge8(row[mt], c, cols, vec) : uint4{0, 0, 0, 0};
+                    }
+            } else {
+                float v[KS][4][8];
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const int c = (slab0 + kThinWaves * i) * kMxSlab + 32 * q + 8 * s;
+                        mx_load_edge8<TYPE>(row[mt], c, row[mt] ? cols : 0, vec, v[i][s]);
+                    }
+                if constexpr (TYPE == SGEMM_TYPE_F32) {
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t b = __float_as_uint(v[i][s][k]) & 0x7fffffffu;
+                                m = m > b ? m : b;
+                            }
+                    // The token's other blocks lie with lanes l ^ 16, l ^ 32, l ^ 48.
+                    uint32_t o = __shfl_xor(m, 16, 64);
+                    m = m > o ? m : o;
+                    o = __shfl_xor(m, 32, 64);
+                    m = m > o ? m : o;
+                    const float lift = mx_lift(m);
+                    back[mt] = lift == 1.0f ? 1.0f : 0x1p-32f;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v[i][s][k] *= lift;
+                }
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) mx_split8<P>(v[i][s], x[i][mt][s]);
+            }
+        }
+    }
+
+    // The same from pieces in memory: piece p of a row at row + p * stride,
+    // `cols` a multiple of 8, rows 16-byte aligned.
+    __device__ __forceinline__ void load_pieces(const uint16_t *row, int64_t stride, int slab0, int cols, int q) {
+        static_assert(MT == 1 && TYPE == SGEMM_TYPE_BF16, "one tile");
+        back[0] = 1.0f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const int c = (slab0 + kThinWaves * i) * kMxSlab + 32 * q + 8 * s;
+                    x[i][0][s][p] = row && c < cols ? *(const uint4 *)(row + p * stride + c) : uint4{0, 0, 0, 0};
+                }
+    }
+};
+
 // A lane's weights of one slab: its block's codes and scale.
 struct MxBlock {
     uint4 codes;
     uint32_t word;   // the slab's four scale bytes of the row
 };
-
-__device__ __forceinline__ MxBlock mx_block(const uint8_t *row, const uint32_t *words, int64_t plane, int slab, int q,
-                                            bool real) {
-    MxBlock b{uint4{0, 0, 0, 0}, 0};
-    if (real) {
-        b.codes = *(const uint4 *)(row + (int64_t)slab * kMxSlabBytes + 16 * q);
-        b.word = words[slab * plane];
-    }
-    return b;
-}
 
 __device__ __forceinline__ float mx_scale(const MxBlock &b, int q) {
     return __uint_as_float((b.word >> (8 * q) & 255u) << 23);
@@ -71,6 +178,105 @@ __device__ __forceinline__ f32v4 mx_mfma(bf16v8 w, uint4 x, f32v4 acc) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16v8, x), acc, 0, 0, 0);
 }
 
+// A 4-bit matrix as the kernels take it.
+struct MxWeights {
+    const uint8_t *codes;
+    const uint32_t *words;
+    int64_t rowb, plane;   // bytes of a row of codes, words of a plane of scales
+    int slabs;
+
+    __device__ __forceinline__ MxBlock load(int64_t row, int slab, int q) const {
+        MxBlock b{uint4{0, 0, 0, 0}, 0};
+        if (slab < slabs) {
+            b.codes = *(const uint4 *)(codes + row * rowb + (int64_t)slab * kMxSlabBytes + 16 * q);
+            b.word = words[slab * plane + row];
+        }
+        return b;
+    }
+};
+
+inline __host__ __device__ MxWeights mx_weights(const uint8_t *codes, const uint8_t *scales, int64_t rows, int cols) {
+    return MxWeights{codes, (const uint32_t *)scales, (int64_t)mx_slabs(cols) * kMxSlabBytes, mx_plane_rows(rows), mx_slabs(cols)};
+}
+
+// Streams row tiles [first, end) past the tokens: row(tile) is the lane's row
+// of weights, emit(tile, mt, l, sums) takes the sums of U tiles (tile .. tile
+// + U - 1) for token l % 16 of tile mt, rows 4 (l / 16) .. + 3 of each.  red:
+// LDS for kThinWaves * G * MT * 64 sums.  With K in several pieces, carry
+// (LDS, (end - first) * MT * 64 sums) holds them from the first piece to the
+// last.  Every thread of the workgroup calls this.
+template <int U, int G, int TYPE, int P, int KS, int MT, class Row, class Emit>
+__device__ __forceinline__ void mx_stream(const MxTokens<TYPE, P, KS, MT> &x, const MxWeights &w, int slab0, int first, int end,
+                                          f32v4 *red, f32v4 *carry, bool first_piece, bool last_piece, Row row, Emit emit) {
+    static_assert(G % U == 0, "whole units in a group");
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4;
+    MxBlock b[G][KS];
+    auto fetch = [&](int g, int tile) {
+        if (tile < end) {
+            const int64_t r = row(tile);
+#pragma unroll
+            for (int i = 0; i < KS; ++i) b[g][i] = w.load(r, slab0 + kThinWaves * i, q);
+        }
+    };
+#pragma unroll
+    for (int g = 0; g < G; ++g) fetch(g, first + g);
+    for (int t0 = first; t0 < end; t0 += G) {
+        f32v4 acc[G][MT];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) acc[g][mt] = f32v4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (t0 + g < end) {
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    const float scale = mx_scale(b[g][i], q);
+                    const uint32_t c[4] = {b[g][i].codes.x, b[g][i].codes.y, b[g][i].codes.z, b[g][i].codes.w};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const bf16v8 v = mx_bf16x8(c[s], scale);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int p = 0; p < P; ++p) acc[g][mt] = mx_mfma(v, x.x[i][mt][s][p], acc[g][mt]);
+                    }
+                }
+                fetch(g, t0 + G + g);
+            }
+        }
+        if (t0 > first) __syncthreads();   // the group before has been added up
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if constexpr (TYPE == SGEMM_TYPE_F32) acc[g][mt] *= x.back[mt];
+                red[((wave * G + g) * MT + mt) * 64 + lane] = acc[g][mt];
+            }
+        __syncthreads();
+        for (int i = tid; i < G / U * MT * 64; i += kThinThreads) {
+            const int l = i & 63, mt = (i >> 6) % MT, g = (i >> 6) / MT * U;
+            if (t0 + g >= end) break;
+            f32v4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                v[u] = red[((g + u) * MT + mt) * 64 + l];
+#pragma unroll
+                for (int k = 1; k < kThinWaves; ++k) v[u] += red[((k * G + g + u) * MT + mt) * 64 + l];
+                f32v4 *kept = carry + ((t0 - first + g + u) * MT + mt) * 64 + l;
+                if (!first_piece) v[u] = *kept + v[u];
+                if (!last_piece) *kept = v[u];
+            }
+            if (last_piece) emit(t0 + g, mt, l, v);
+        }
+    }
+    __syncthreads();   // red is free
+}
+
+// The number of row tiles each workgroup of `groups` takes.
+inline int mx_share(int tiles, int groups, int unit) {
+    const int per = (tiles + groups - 1) / groups;
+    return (per + unit - 1) / unit * unit;
+}
+
 struct MxLinearJob {
     const void *x;
     int64_t ldx;
@@ -78,6 +284,7 @@ struct MxLinearJob {
     int M, N, K, type;
     void *y;
     int64_t ldy;
+    float *scratch;
 };
 
 struct MxMoeJob {
@@ -91,6 +298,7 @@ struct MxMoeJob {
 };
 
 hipError_t launch_mx4_linear(const MxLinearJob &j, hipStream_t s);
+int64_t mx4_linear_scratch(int M, int N, int K, int type);
 hipError_t launch_mx4_moe(const MxMoeJob &j, hipStream_t s);
 int64_t mx4_moe_scratch(int tokens, int hidden, int inner, int experts, int top, int type);
 

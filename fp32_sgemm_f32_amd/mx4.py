@@ -22,10 +22,11 @@ def _bind(lib):
     lib.sgemm_f32_mx4_quantize.argtypes = [i, i, i, p, i, i, p, p, p, p, p]
     lib.sgemm_f32_mx4_dequantize.argtypes = [i, i, p, p, i, p, i, p]
     lib.sgemm_f32_mx4_gemm.argtypes = [i, i, i, f, p, p, p, p, f, i, p, i, p]
-    lib.sgemm_f32_mx4_linear.argtypes = [i, i, i, i, p, i, p, p, p, i, p]
+    lib.sgemm_f32_mx4_linear.argtypes = [i, i, i, i, p, i, p, p, p, i, p, ll, p]
+    lib.sgemm_f32_mx4_linear_scratch.argtypes = [i, i, i, i, ctypes.POINTER(ll)]
     lib.sgemm_f32_mx4_moe.argtypes = [i, i, i, i, i, i, i, p, i, p, i, p, p, p, p, p, i, p, ll, p]
     lib.sgemm_f32_mx4_moe_scratch.argtypes = [i, i, i, i, i, i, ctypes.POINTER(ll)]
-    for name in ("bytes", "quantize", "dequantize", "gemm", "linear", "moe", "moe_scratch"):
+    for name in ("bytes", "quantize", "dequantize", "gemm", "linear", "linear_scratch", "moe", "moe_scratch"):
         getattr(lib, "sgemm_f32_mx4_" + name).restype = i
 
 
@@ -273,8 +274,14 @@ def mx4_linear(X, W, out=None, stream=None):
     run = _Run(X.device, stream)
     out = _result(run, out, (M, N), X.dtype)
     _, ldy = _floats(out, "out", X.device)
+    import torch
+
+    from . import library
+    need = ctypes.c_longlong()
+    library().sgemm_f32_mx4_linear_scratch(M, N, K, ty, ctypes.byref(need))
+    scratch = run.empty((need.value,), torch.uint8) if need.value else None
     run.call("mx4_linear", (X, W, out), M, N, K, ty, X.data_ptr(), ldx, W.codes.data_ptr(), W.scales.data_ptr(),
-             out.data_ptr(), ldy)
+             out.data_ptr(), ldy, None if scratch is None else scratch.data_ptr(), need.value)
     return out
 
 

@@ -433,12 +433,20 @@ int sgemm_f32_mx4_gemm(int M, int N, int K, float alpha,
  * Y = X * W^T for float rows X (M x K) and 4-bit weights W (N x K), Y (M x N)
  * in X's type: the product of one token or a few with a layer whose weights
  * alone are in 4 bits.  X is not rounded: every product is exact, the sums
- * are in fp32.  W is read once for up to 64 rows of X; longer X run 64 rows
- * at a time (sgemm_f32_mx4_gemm, on quantised X, is the call for those).
+ * are in fp32.  (Of fp32 values, what lies below 2^-133 is cut where a larger
+ * one than 2^-60 stands within the same thousand columns of the row.)  W is
+ * read once for up to 64 rows of X (32 in fp32); longer X run 64 rows at a
+ * time (sgemm_f32_mx4_gemm, on quantised X, is the call for those).  scratch:
+ * device memory of at least the bytes that sgemm_f32_mx4_linear_scratch
+ * gives (for short K none), 256-byte aligned, overlapping nothing; its
+ * contents do not matter before or after.
  */
 int sgemm_f32_mx4_linear(int M, int N, int K, int type, const void *X, int ldx,
                          const void *codes, const void *scales,
-                         void *Y, int ldy, hipStream_t stream);
+                         void *Y, int ldy, void *scratch, long long scratch_bytes,
+                         hipStream_t stream);
+/* Bytes of scratch memory of such a call. */
+int sgemm_f32_mx4_linear_scratch(int M, int N, int K, int type, long long *bytes);
 
 /*
  * A mixture-of-experts layer for a few tokens, experts in 4 bits:

@@ -373,6 +373,19 @@ def test_linear_strided(dev, dtype, m, pad, shift):
 
 
 @typed
+def test_linear_whole_type_range(dev, dtype):
+    """Token values from the least subnormal to the largest: each piece of the split is exact."""
+    rng = np.random.default_rng(14)
+    f = torch.finfo(dtype)
+    lo = int(np.log2(f.smallest_normal)) - (0 if dtype == torch.bfloat16 else 8)
+    k = 256
+    x = torch.from_numpy(rng.standard_normal((20, k)) * np.ldexp(1.0, rng.integers(lo, 10, (20, 1)))).to(dtype).to(dev)
+    w = random_mx4(rng, 40, k, dev, 127, 129)
+    X, W = host(x), values(w)
+    close(sg.mx4_linear(x, w), X @ W.T, product_bound(X, W, 3), dtype)
+
+
+@typed
 @pytest.mark.parametrize("m", [3, 30])
 def test_linear_nan_and_infinity_stay_in_their_rows(dev, dtype, m):
     rng = np.random.default_rng(15)

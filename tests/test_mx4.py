@@ -76,8 +76,8 @@ def test_gemm_refuses(status, args):
     assert gemm(**args) == status
 
 
-def linear(M=4, N=4, K=128, type=0, X=P, ldx=128, c=P * 2, s=P * 3, Y=P * 4, ldy=4):
-    return lib().sgemm_f32_mx4_linear(M, N, K, type, X, ldx, c, s, Y, ldy, None)
+def linear(M=4, N=4, K=128, type=0, X=P, ldx=128, c=P * 2, s=P * 3, Y=P * 4, ldy=4, scratch=None, nbytes=0):
+    return lib().sgemm_f32_mx4_linear(M, N, K, type, X, ldx, c, s, Y, ldy, scratch, nbytes, None)
 
 
 @pytest.mark.parametrize("status, args", [
@@ -85,9 +85,27 @@ def linear(M=4, N=4, K=128, type=0, X=P, ldx=128, c=P * 2, s=P * 3, Y=P * 4, ldy
     (sg.ERR_LD, dict(ldx=127)), (sg.ERR_LD, dict(ldy=3)), (sg.ERR_NULL, dict(X=None)), (sg.ERR_NULL, dict(c=None)),
     (sg.ERR_NULL, dict(Y=None)), (sg.ERR_ALIGN, dict(X=P + 1)), (sg.ERR_ALIGN, dict(c=P * 2 + 4)),
     (sg.ERR_ALIAS, dict(Y=P)), (sg.ERR_ALIAS, dict(Y=P * 3)),
+    # K long enough to be shared: scratch memory is needed
+    (sg.ERR_NULL, dict(K=16384, ldx=16384)), (sg.ERR_SCRATCH, dict(K=16384, ldx=16384, scratch=FAR, nbytes=16)),
+    (sg.ERR_ALIGN, dict(K=16384, ldx=16384, scratch=FAR + 64, nbytes=1 << 20)),
+    (sg.ERR_ALIAS, dict(K=16384, ldx=16384, scratch=P * 2, nbytes=1 << 20)),
 ])
 def test_linear_refuses(status, args):
     assert linear(**args) == status
+
+
+def test_linear_scratch():
+    n = ctypes.c_longlong()
+    call = lib().sgemm_f32_mx4_linear_scratch
+    assert call(4, 4, 128, 0, ctypes.byref(n)) == sg.OK and n.value == 0
+    assert call(4, 100, 16384, 0, ctypes.byref(n)) == sg.OK and n.value > 0
+    once = n.value
+    assert call(64, 100, 16384, 0, ctypes.byref(n)) == sg.OK and n.value >= once
+    most = n.value
+    assert call(64 * 100 + 4, 100, 16384, 0, ctypes.byref(n)) == sg.OK and n.value == most   # 64 rows at a time
+    assert call(4, 4, 128, 3, ctypes.byref(n)) == sg.ERR_CONFIG
+    assert call(-1, 4, 128, 0, ctypes.byref(n)) == sg.ERR_SHAPE
+    assert call(4, 4, 128, 0, None) == sg.ERR_NULL
 
 
 def moe(tokens=2, hidden=128, inner=32, experts=4, top=2, norm=1, type=0, X=FAR, ldx=128, router=FAR * 2, ldr=128,
