@@ -54,16 +54,21 @@ struct MxType<SGEMM_TYPE_F16> {
     static __device__ __forceinline__ T from(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 };
 
-// Eight adjacent values as floats, from a 16-byte aligned pointer.
+// 16 bytes at any element's address: the hardware takes wide loads and stores
+// of global memory at any alignment (a line more where they straddle one), so
+// odd leading dimensions and shifted views need no narrow path.
+typedef float f32v4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32v4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Eight adjacent values as floats.
 template <int TYPE>
 __device__ __forceinline__ void mx_load8(const typename MxType<TYPE>::T *p, float (&v)[8]) {
     if constexpr (TYPE == SGEMM_TYPE_F32) {
-        const f32v4 a = ((const f32v4 *)p)[0], b = ((const f32v4 *)p)[1];
+        const f32v4_any a = ((const f32v4_any *)p)[0], b = ((const f32v4_any *)p)[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
     } else {
-        const uint4 u = *(const uint4 *)p;
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        const u32v4_any w = *(const u32v4_any *)p;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint16_t lo = (uint16_t)w[i], hi = (uint16_t)(w[i] >> 16);
@@ -73,27 +78,12 @@ __device__ __forceinline__ void mx_load8(const typename MxType<TYPE>::T *p, floa
     }
 }
 
-template <int TYPE>
-__device__ __forceinline__ void mx_store8(typename MxType<TYPE>::T *p, const float (&v)[8]) {
-    if constexpr (TYPE == SGEMM_TYPE_F32) {
-        ((f32v4 *)p)[0] = f32v4{v[0], v[1], v[2], v[3]};
-        ((f32v4 *)p)[1] = f32v4{v[4], v[5], v[6], v[7]};
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = (uint32_t)MxType<TYPE>::from(v[2 * i]) | (uint32_t)MxType<TYPE>::from(v[2 * i + 1]) << 16;
-        *(uint4 *)p = uint4{w[0], w[1], w[2], w[3]};
-    }
-}
-
 // Eight values of a row from column c on, zeros at and after `cols`.
 template <int TYPE>
-__device__ __forceinline__ void mx_load_edge8(const typename MxType<TYPE>::T *row, int c, int cols, bool vec,
-                                              float (&v)[8]) {
+__device__ __forceinline__ void mx_load_edge8(const typename MxType<TYPE>::T *row, int c, int cols, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    if (vec && c + 8 <= cols) {
+    if (c + 8 <= cols) {
         mx_load8<TYPE>(row + c, v);
     } else if (c < cols) {
 #pragma unroll
@@ -126,7 +116,10 @@ struct MxGemmJob {
 };
 
 hipError_t launch_mx4_quantize(const MxQuantJob &j, hipStream_t s);
+hipError_t launch_mx4_quantize_two(const MxQuantJob &j, const MxQuantJob &k, hipStream_t s);
 hipError_t launch_mx4_dequantize(const MxDequantJob &j, hipStream_t s);
 hipError_t launch_mx4_gemm(const MxGemmJob &j, int num_cus, hipStream_t s);
+// Two products, the second with a result in fp32; in one launch if both are small.
+hipError_t launch_mx4_gemm_two(const MxGemmJob &j, const MxGemmJob &k, int num_cus, hipStream_t s);
 
 }  // namespace sgemm

@@ -49,9 +49,19 @@ int check_spans(const Span (&s)[N], int *dev) {
         }
     const hipError_t e = hipGetDevice(dev);
     if (e != hipSuccess) return hip_fail(e);
+    // An array inside an allocation that an earlier one of this call lies in
+    // needs no question to the runtime (half a microsecond each).
+    uintptr_t lo[N], hi[N];
+    int known = 0;
     for (const Span &x : s) {
-        const int st = check_device_range(x.p, x.bytes, *dev);
+        if (x.bytes <= 0) continue;
+        const uintptr_t p = (uintptr_t)x.p;
+        bool inside = false;
+        for (int i = 0; i < known && !inside; ++i) inside = p >= lo[i] && p < hi[i] && (uint64_t)x.bytes <= hi[i] - p;
+        if (inside) continue;
+        const int st = check_device_range(x.p, x.bytes, *dev, &lo[known], &hi[known]);
         if (st != SGEMM_OK) return st;
+        ++known;
     }
     return SGEMM_OK;
 }
@@ -128,6 +138,93 @@ SGEMM_API int sgemm_f32_mx4_gemm(int M, int N, int K, float alpha, const void *a
     if (status != SGEMM_OK) return status;
     return done(launch_mx4_gemm({(const uint8_t *)a, (const uint8_t *)sa, (const uint8_t *)b, (const uint8_t *)sb, M, N, k,
                                  type, alpha, beta, C, ldc}, cus, stream));
+}
+
+// Scratch memory of a training step: the matrices that only one call needs,
+// codes and scales 256-byte aligned.
+namespace {
+
+struct Packed {
+    uint8_t *codes, *scales;
+};
+
+int64_t up256(int64_t n) { return (n + 255) & ~(int64_t)255; }
+int64_t packed_bytes(int rows, int cols) { return up256(codes_bytes(rows, cols)) + up256(scales_bytes(rows, cols)); }
+Packed packed_at(void *base, int64_t at, int rows, int cols) {
+    uint8_t *p = (uint8_t *)base + at;
+    return {p, p + up256(codes_bytes(rows, cols))};
+}
+
+// A matrix both ways; with rows == 0 or cols == 0 there is nothing to do.
+MxQuantJob both_ways(const void *x, int ldx, int rows, int cols, int type, int rule, Packed q, Packed qt) {
+    return {x, ldx, rows, cols, type, rule == SGEMM_MX4_SCALE_NOCLIP, q.codes, q.scales, qt.codes, qt.scales};
+}
+
+}  // namespace
+
+SGEMM_API int sgemm_f32_mx4_train_scratch(int M, int N, int K, long long *forward, long long *backward) {
+    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return SGEMM_ERR_SHAPE;
+    if (forward) *forward = packed_bytes(M, K) + packed_bytes(N, K);
+    if (backward) *backward = packed_bytes(M, N) + packed_bytes(N, M);
+    return SGEMM_OK;
+}
+
+SGEMM_API int sgemm_f32_mx4_train_forward(int M, int N, int K, int type, const void *X, int ldx, int type_w, const void *W,
+                                          int ldw, int rule, void *Y, int ldy, void *xt, void *sxt, void *wt, void *swt,
+                                          void *scratch, long long scratch_bytes, hipStream_t stream) {
+    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return SGEMM_ERR_SHAPE;
+    if (!known_type(type) || !known_type(type_w) || (rule != SGEMM_MX4_SCALE_FLOOR && rule != SGEMM_MX4_SCALE_NOCLIP))
+        return SGEMM_ERR_CONFIG;
+    const bool x = M > 0 && K > 0, w = N > 0 && K > 0, y = M > 0 && N > 0;
+    if ((x && ldx < K) || (w && ldw < K) || (y && ldy < N)) return SGEMM_ERR_LD;
+    const int64_t need = packed_bytes(M, K) + packed_bytes(N, K);
+    if (scratch && scratch_bytes < need) return SGEMM_ERR_SCRATCH;
+    const Span spans[] = {floats(X, M, K, ldx, type, false), floats(W, N, K, ldw, type_w, false),
+                          floats(Y, M, N, ldy, type, true), codes(xt, K, M, true), scales(sxt, K, M, true),
+                          codes(wt, K, N, true), scales(swt, K, N, true), Span{scratch, need, 256, true}};
+    int dev = 0, cus = 0;
+    int status = check_spans(spans, &dev);
+    if (status == SGEMM_OK) status = compute_units(dev, &cus);
+    if (status != SGEMM_OK) return status;
+    const Packed q = packed_at(scratch, 0, M, K), v = packed_at(scratch, packed_bytes(M, K), N, K);
+    const MxQuantJob jx = both_ways(X, ldx, M, K, type, rule, q, {(uint8_t *)xt, (uint8_t *)sxt});
+    const MxQuantJob jw = both_ways(W, ldw, N, K, type_w, rule, v, {(uint8_t *)wt, (uint8_t *)swt});
+    hipError_t e = x && w ? launch_mx4_quantize_two(jx, jw, stream)
+                   : x    ? launch_mx4_quantize(jx, stream)
+                   : w    ? launch_mx4_quantize(jw, stream)
+                          : hipSuccess;
+    if (e == hipSuccess && y)
+        e = launch_mx4_gemm({q.codes, q.scales, v.codes, v.scales, M, N, K, type, K > 0 ? 1.0f : 0.0f, 0.0f, Y, ldy}, cus, stream);
+    return done(e);
+}
+
+SGEMM_API int sgemm_f32_mx4_train_backward(int M, int N, int K, int type, const void *dY, int ldd, int rule, const void *xt,
+                                           const void *sxt, const void *wt, const void *swt, void *dX, int lddx, float beta,
+                                           void *dW, int lddw, void *scratch, long long scratch_bytes, hipStream_t stream) {
+    if (!dim_ok(M) || !dim_ok(N) || !dim_ok(K)) return SGEMM_ERR_SHAPE;
+    if (!known_type(type) || (rule != SGEMM_MX4_SCALE_FLOOR && rule != SGEMM_MX4_SCALE_NOCLIP)) return SGEMM_ERR_CONFIG;
+    const bool d = M > 0 && N > 0, x = M > 0 && K > 0, w = N > 0 && K > 0;
+    if ((d && ldd < N) || (x && lddx < K) || (w && lddw < K)) return SGEMM_ERR_LD;
+    const int64_t need = packed_bytes(M, N) + packed_bytes(N, M);
+    if (scratch && scratch_bytes < need) return SGEMM_ERR_SCRATCH;
+    const Span spans[] = {floats(dY, M, N, ldd, type, false), codes(xt, K, M, false), scales(sxt, K, M, false),
+                          codes(wt, K, N, false), scales(swt, K, N, false), floats(dX, M, K, lddx, type, true),
+                          floats(dW, N, K, lddw, SGEMM_TYPE_F32, true), Span{scratch, need, 256, true}};
+    int dev = 0, cus = 0;
+    int status = check_spans(spans, &dev);
+    if (status == SGEMM_OK) status = compute_units(dev, &cus);
+    if (status != SGEMM_OK) return status;
+    const Packed q = packed_at(scratch, 0, M, N), qt = packed_at(scratch, packed_bytes(M, N), N, M);
+    hipError_t e = d ? launch_mx4_quantize(both_ways(dY, ldd, M, N, type, rule, q, qt), stream) : hipSuccess;
+    const MxGemmJob gx{q.codes, q.scales, (const uint8_t *)wt, (const uint8_t *)swt, M, K, N, type, N > 0 ? 1.0f : 0.0f, 0.0f, dX,
+                       lddx};
+    const MxGemmJob gw{qt.codes, qt.scales, (const uint8_t *)xt, (const uint8_t *)sxt, N, K, M, SGEMM_TYPE_F32,
+                       M > 0 ? 1.0f : 0.0f, beta, dW, lddw};
+    if (e == hipSuccess) e = x && w ? launch_mx4_gemm_two(gx, gw, cus, stream)
+                             : x    ? launch_mx4_gemm(gx, cus, stream)
+                             : w    ? launch_mx4_gemm(gw, cus, stream)
+                                    : hipSuccess;
+    return done(e);
 }
 
 SGEMM_API int sgemm_f32_mx4_linear_scratch(int M, int N, int K, int type, long long *bytes) {

@@ -91,7 +91,7 @@ struct Args {
 };
 
 template <int F, class T>
-struct __attribute__((packed, aligned(sizeof(T) * F))) Vec {
+struct __attribute__((packed, aligned(sizeof(T)))) Vec {   // stored at any element's address
     T v[F];
 };
 
@@ -116,8 +116,9 @@ struct Tile {
     __device__ __forceinline__ static int b_col(int r) { return r / WTN * WTN + FN * (r % 32) + r % WTN / 32; }
 };
 
+// The tile of workgroup `block` of the product g.
 template <class TL, int TYPE>
-__global__ __launch_bounds__(TL::NT, 1) void mx4_gemm_kernel(Args g) {
+__device__ __forceinline__ void compute_tile(const Args &g, int block) {
     typedef typename MxType<TYPE>::T T;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -129,7 +130,7 @@ __global__ __launch_bounds__(TL::NT, 1) void mx4_gemm_kernel(Args g) {
     int tm, tn;
     {
         const int tiles = g.tiles_m * g.tiles_n, per = tiles >> 3, rest = tiles & 7;
-        const int x = blockIdx.x & 7, y = blockIdx.x >> 3;
+        const int x = block & 7, y = block >> 3;
         const int t = x * per + (x < rest ? x : rest) + y;
         const int group = 8 * g.tiles_n, gi = t / group, first = gi * 8;
         const int rows = g.tiles_m - first < 8 ? g.tiles_m - first : 8;
@@ -337,7 +338,7 @@ __global__ __launch_bounds__(TL::NT, 1) void mx4_gemm_kernel(Args g) {
     // Lane l holds columns FN (l % 32) + 0 .. FN-1 of its wave's tile, rows
     // 8 (r / 4) + 4 (l / 32) + r % 4 of each fragment.
     const int col = n0 + wn * TL::WTN + TL::FN * fr;
-    const bool wide = col + TL::FN <= g.N && (g.ldc % TL::FN) == 0 && ((uintptr_t)g.c % (TL::FN * sizeof(T))) == 0;
+    const bool wide = col + TL::FN <= g.N;
 #pragma unroll
     for (int i = 0; i < TL::FM; ++i)
 #pragma unroll
@@ -369,6 +370,19 @@ __global__ __launch_bounds__(TL::NT, 1) void mx4_gemm_kernel(Args g) {
         }
 }
 
+template <class TL, int TYPE>
+__global__ __launch_bounds__(TL::NT, 1) void mx4_gemm_kernel(Args g) {
+    compute_tile<TL, TYPE>(g, blockIdx.x);
+}
+
+// Two products in one launch: the first tiles0 workgroups compute g, the
+// others k.
+template <class TL, int TYPE>
+__global__ __launch_bounds__(TL::NT, 1) void mx4_gemm_two_kernel(Args g, Args k, int tiles0) {
+    if ((int)blockIdx.x < tiles0) compute_tile<TL, TYPE>(g, blockIdx.x);
+    else compute_tile<TL, SGEMM_TYPE_F32>(k, blockIdx.x - tiles0);
+}
+
 // Waves 2 x 4 everywhere but in the smallest: two waves on a SIMD cover each
 // other's waits (2 x 2 waves of 128 x 128 read a third less LDS and were 4 to
 // 12 % slower).
@@ -378,10 +392,15 @@ typedef Tile<128, 128, 256, 2, 4, 2> T128;       // 8 waves of 64 x 32, 68 KiB: 
 typedef Tile<64, 64, 256, 2, 2, 2> T64;          // 4 waves of 32 x 32, 34 KiB: four workgroups on a CU
 typedef Tile<64, 64, 256, 2, 2, 4> T64Deep;      // the same, 68 KiB
 
+template <class TL>
+Args arguments(const MxGemmJob &j) {
+    return Args{j.a, j.sa, j.b, j.sb, j.c, j.ldc, j.M, j.N, mx_slabs(j.K), (int)(((int64_t)j.M + TL::BM - 1) / TL::BM),
+                (int)(((int64_t)j.N + TL::BN - 1) / TL::BN), j.alpha, j.beta};
+}
+
 template <class TL, int TYPE>
 hipError_t launch_tile(const MxGemmJob &j, hipStream_t s) {
-    Args g{j.a, j.sa, j.b, j.sb, j.c, j.ldc, j.M, j.N, mx_slabs(j.K), (int)(((int64_t)j.M + TL::BM - 1) / TL::BM),
-           (int)(((int64_t)j.N + TL::BN - 1) / TL::BN), j.alpha, j.beta};
+    Args g = arguments<TL>(j);
     const void *k = (const void *)mx4_gemm_kernel<TL, TYPE>;
     const int bytes = TL::S * TL::STAGE;
     hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -390,9 +409,23 @@ hipError_t launch_tile(const MxGemmJob &j, hipStream_t s) {
     return hipLaunchKernel(k, dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(TL::NT), params, bytes, s);
 }
 
+template <class TL, int TYPE>
+hipError_t launch_two(const MxGemmJob &first, const MxGemmJob &second, hipStream_t s) {
+    Args g = arguments<TL>(first), h = arguments<TL>(second);
+    const void *k = (const void *)mx4_gemm_two_kernel<TL, TYPE>;
+    const int bytes = TL::S * TL::STAGE;
+    hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    int tiles0 = g.tiles_m * g.tiles_n;
+    void *params[] = {&g, &h, &tiles0};
+    return hipLaunchKernel(k, dim3((unsigned)(tiles0 + h.tiles_m * h.tiles_n)), dim3(TL::NT), params, bytes, s);
+}
+
+int64_t tiles_of(const MxGemmJob &j, int b) { return (((int64_t)j.M + b - 1) / b) * (((int64_t)j.N + b - 1) / b); }
+
 template <int TYPE>
 hipError_t launch_type(const MxGemmJob &j, int num_cus, hipStream_t s) {
-    const auto tiles = [&](int b) { return (((int64_t)j.M + b - 1) / b) * (((int64_t)j.N + b - 1) / b); };
+    const auto tiles = [&](int b) { return tiles_of(j, b); };
     // The largest tile that gives every CU one.  A row of an even number of
     // slabs is whole 128-byte lines, which chunks of two slabs read at once
     // (16384^3: 1957 us, in chunks of one 2109); rows of an odd number split
@@ -406,6 +439,16 @@ hipError_t launch_type(const MxGemmJob &j, int num_cus, hipStream_t s) {
     return tiles(64) <= num_cus ? launch_tile<T64Deep, TYPE>(j, s) : launch_tile<T64, TYPE>(j, s);
 }
 
+template <int TYPE>
+hipError_t launch_pair(const MxGemmJob &j, const MxGemmJob &k, int num_cus, hipStream_t s) {
+    // Tiles of either that fill the CUs by themselves gain nothing from the other's.
+    if (tiles_of(j, 128) >= num_cus || tiles_of(k, 128) >= num_cus) {
+        const hipError_t e = launch_type<TYPE>(j, num_cus, s);
+        return e == hipSuccess ? launch_type<SGEMM_TYPE_F32>(k, num_cus, s) : e;
+    }
+    return tiles_of(j, 64) + tiles_of(k, 64) <= num_cus ? launch_two<T64Deep, TYPE>(j, k, s) : launch_two<T64, TYPE>(j, k, s);
+}
+
 }  // namespace
 
 hipError_t launch_mx4_gemm(const MxGemmJob &j, int num_cus, hipStream_t s) {
@@ -413,6 +456,15 @@ hipError_t launch_mx4_gemm(const MxGemmJob &j, int num_cus, hipStream_t s) {
     case SGEMM_TYPE_F32: return launch_type<SGEMM_TYPE_F32>(j, num_cus, s);
     case SGEMM_TYPE_BF16: return launch_type<SGEMM_TYPE_BF16>(j, num_cus, s);
     case SGEMM_TYPE_F16: return launch_type<SGEMM_TYPE_F16>(j, num_cus, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_mx4_gemm_two(const MxGemmJob &j, const MxGemmJob &k, int num_cus, hipStream_t s) {
+    switch (j.type) {
+    case SGEMM_TYPE_F32: return launch_pair<SGEMM_TYPE_F32>(j, k, num_cus, s);
+    case SGEMM_TYPE_BF16: return launch_pair<SGEMM_TYPE_BF16>(j, k, num_cus, s);
+    case SGEMM_TYPE_F16: return launch_pair<SGEMM_TYPE_F16>(j, k, num_cus, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -20,7 +20,7 @@ struct Args {
     const void *x;
     int64_t ldx;
     MxWeights w;
-    int M, N, K, vec, per, parts;   // per: row tiles of a workgroup; parts: workgroups along K
+    int M, N, K, per, parts;   // per: row tiles of a workgroup; parts: workgroups along K
     void *y;
     int64_t ldy;
     float *partial;                 // parts x M x pitch, if parts > 1
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, MT) 
         row[mt] = t < a.M ? (const T *)a.x + t * a.ldx : nullptr;
     }
     MxTokens<TYPE, mx_pieces(TYPE), KS, MT> x;
-    x.load(row, slab0, a.K, a.vec, lane >> 4);
+    x.load(row, slab0, a.K, lane >> 4);
     mx_stream<1, G>(
         x, a.w, slab0, first, end, red, nullptr, true, true,
         [&](int tile) -> int64_t {
@@ -134,7 +134,6 @@ hipError_t launch_type(const MxLinearJob &j, hipStream_t s) {
         a.w = mx_weights(j.codes, j.scales, j.N, j.K);
         a.N = j.N;
         a.K = j.K;
-        a.vec = ((uintptr_t)j.x & 15) == 0 && (j.ldx * esize & 15) == 0;
         a.y = (char *)j.y + m * j.ldy * esize;
         a.ldy = j.ldy;
         a.parts = k_parts(a.M, a.K, TYPE);

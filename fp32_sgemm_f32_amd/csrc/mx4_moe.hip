@@ -74,7 +74,7 @@ Scratch layout(char *p, int tokens, int hidden, int inner, int experts, int top,
 
 // A wave takes one expert and TT tokens.
 template <int TYPE, int TT>
-__global__ __launch_bounds__(256) void logits_kernel(MxMoeJob j, Scratch s, int vec) {
+__global__ __launch_bounds__(256) void logits_kernel(MxMoeJob j, Scratch s) {
     typedef typename MxType<TYPE>::T T;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int e = blockIdx.x * 4 + wave, t0 = blockIdx.y * TT;
@@ -90,25 +90,23 @@ __global__ __launch_bounds__(256) void logits_kernel(MxMoeJob j, Scratch s, int 
             for (int i = 0; i < 8; ++i) sum[t] = fma((double)w[i], (double)v[t][i], sum[t]);
     };
     int h = 8 * lane;
-    if (vec) {
-        // Two steps' loads in flight.
-        for (; h + 512 + 8 <= j.hidden; h += 1024) {
-            float w[2][8], v[2][TT][8];
+    // Two steps' loads in flight.
+    for (; h + 512 + 8 <= j.hidden; h += 1024) {
+        float w[2][8], v[2][TT][8];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                mx_load8<TYPE>(r + h + 512 * k, w[k]);
+        for (int k = 0; k < 2; ++k) {
+            mx_load8<TYPE>(r + h + 512 * k, w[k]);
 #pragma unroll
-                for (int t = 0; t < TT; ++t) mx_load8<TYPE>(x[t] + h + 512 * k, v[k][t]);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) add(w[k], v[k]);
+            for (int t = 0; t < TT; ++t) mx_load8<TYPE>(x[t] + h + 512 * k, v[k][t]);
         }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) add(w[k], v[k]);
     }
     for (; h < j.hidden; h += 512) {
         float w[8], v[TT][8];
-        mx_load_edge8<TYPE>(r, h, j.hidden, vec, w);
+        mx_load_edge8<TYPE>(r, h, j.hidden, w);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) mx_load_edge8<TYPE>(x[t], h, j.hidden, vec, v[t]);
+        for (int t = 0; t < TT; ++t) mx_load_edge8<TYPE>(x[t], h, j.hidden, v[t]);
         add(w, v);
     }
 #pragma unroll
@@ -208,8 +206,7 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
 template <int TYPE, int KS, bool FEW>
 __global__ __launch_bounds__(kThinThreads, up_two_on_a_cu(mx_pieces(TYPE), KS) ? 4 : 2) void up_kernel(MxMoeJob j, Scratch s,
-                                                                                                      MxWeights w, int vec,
-                                                                                                      int per) {
+                                                                                                      MxWeights w, int per) {
     typedef typename MxType<TYPE>::T T;
     constexpr int G = up_group(KS), PA = act_pieces(TYPE);
     const int all = j.tokens * j.top;
@@ -224,7 +221,7 @@ __global__ __launch_bounds__(kThinThreads, up_two_on_a_cu(mx_pieces(TYPE), KS) ?
         // blockIdx.y: a choice.  Its token is known before its expert.
         const int t = blockIdx.y / j.top;
         const T *row[1] = {l16 == 0 ? (const T *)j.x + (int64_t)t * j.ldx : nullptr};
-        x.load(row, wave, j.hidden, vec, lane >> 4);
+        x.load(row, wave, j.hidden, lane >> 4);
         rank_experts(j, s.logits + (int64_t)t * j.experts, choice);
         e = choice.expert[blockIdx.y % j.top];
     } else {
@@ -244,7 +241,7 @@ __global__ __launch_bounds__(kThinThreads, up_two_on_a_cu(mx_pieces(TYPE), KS) ?
             row[0] = (const T *)j.x + (int64_t)(a / j.top) * j.ldx;
         }
         for (int s0 = 0; s0 < w.slabs; s0 += kThinWaves * KS) {
-            if (!FEW || s0 > 0) x.load(row, s0 + wave, j.hidden, vec, lane >> 4);
+            if (!FEW || s0 > 0) x.load(row, s0 + wave, j.hidden, lane >> 4);
             mx_stream<2, G>(x, w, s0 + wave, first, end, red, red + kThinWaves * G * 64, s0 == 0, s0 + kThinWaves * KS >= w.slabs,
                             row_of, [&](int tile, int, int l, const f32v4(&v)[2]) {
                                 const int i = i0 + (l & 15), f = (tile >> 1) * 16 + 4 * (l >> 4);
@@ -383,25 +380,25 @@ int groups_of(int tiles, int unit, int slots, int fill, int most) {
 constexpr int kCarryTiles = 32;
 
 template <int TYPE, int KS, bool FEW>
-hipError_t launch_up(MxMoeJob &j, Scratch &s, int vec, hipStream_t stream) {
+hipError_t launch_up(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     constexpr int G = up_group(KS);
     MxWeights w = mx_weights(j.up, j.sup, (int64_t)2 * j.experts * j.inner, j.hidden);
     const int tiles = 2 * ((j.inner + 15) / 16), all = j.tokens * j.top, slots = FEW ? all : all < j.experts ? all : j.experts;
     const bool pieces = w.slabs > kThinWaves * KS;
     int per = mx_share(tiles, groups_of(tiles, 2, slots, FEW && !up_two_on_a_cu(mx_pieces(TYPE), KS) ? 256 : 512, pieces ? kCarryTiles : tiles), 2);
     const int bytes = (kThinWaves * G + (pieces ? kCarryTiles : 0)) * 64 * 16;
-    void *params[] = {&j, &s, &w, &vec, &per};
+    void *params[] = {&j, &s, &w, &per};
     return hipLaunchKernel((const void *)up_kernel<TYPE, KS, FEW>,
                            dim3((unsigned)((tiles + per - 1) / per), (unsigned)(FEW ? all : j.experts)), dim3(kThinThreads), params,
                            bytes, stream);
 }
 
 template <int TYPE, bool FEW>
-hipError_t launch_up_slabs(MxMoeJob &j, Scratch &s, int vec, hipStream_t stream) {
+hipError_t launch_up_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     const int need = (mx_slabs(j.hidden) + kThinWaves - 1) / kThinWaves;
     if constexpr (TYPE == SGEMM_TYPE_BF16)
-        if (need > 2) return launch_up<TYPE, 4, FEW>(j, s, vec, stream);
-    return need > 1 ? launch_up<TYPE, 2, FEW>(j, s, vec, stream) : launch_up<TYPE, 1, FEW>(j, s, vec, stream);
+        if (need > 2) return launch_up<TYPE, 4, FEW>(j, s, stream);
+    return need > 1 ? launch_up<TYPE, 2, FEW>(j, s, stream) : launch_up<TYPE, 1, FEW>(j, s, stream);
 }
 
 template <int TYPE, int KS>
@@ -420,10 +417,7 @@ template <int TYPE>
 hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
     MxMoeJob j = job;
     Scratch s = layout(j.scratch, j.tokens, j.hidden, j.inner, j.experts, j.top, TYPE);
-    const int64_t b = TYPE == SGEMM_TYPE_F32 ? 4 : 2;
-    int vec_x = ((uintptr_t)j.x & 15) == 0 && (j.ldx * b & 15) == 0;
-    int vec = vec_x && ((uintptr_t)j.router & 15) == 0 && (j.ldr * b & 15) == 0;
-    void *params[] = {&j, &s, &vec};
+    void *params[] = {&j, &s};
     const unsigned ge = (unsigned)((j.experts + 3) / 4);
     hipError_t e = j.tokens < 4 ? hipLaunchKernel((const void *)logits_kernel<TYPE, 1>, dim3(ge, (unsigned)j.tokens), dim3(256),
                                                   params, 0, stream)
@@ -431,7 +425,7 @@ hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
                                                   dim3(256), params, 0, stream);
     if (e != hipSuccess) return e;
     if (j.tokens * j.top <= kFew) {
-        e = launch_up_slabs<TYPE, true>(j, s, vec_x, stream);
+        e = launch_up_slabs<TYPE, true>(j, s, stream);
         if (e != hipSuccess) return e;
         MxWeights w = mx_weights(j.down, j.sdown, (int64_t)j.experts * j.hidden, j.inner);
         void *down[] = {&j, &s, &w};
@@ -440,7 +434,7 @@ hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
     }
     e = hipLaunchKernel((const void *)choose_kernel, dim3((unsigned)j.tokens), dim3(kThinThreads), params, 0, stream);
     if (e != hipSuccess) return e;
-    e = launch_up_slabs<TYPE, false>(j, s, vec_x, stream);
+    e = launch_up_slabs<TYPE, false>(j, s, stream);
     if (e != hipSuccess) return e;
     e = mx_slabs(j.inner) > kThinWaves ? launch_down<TYPE, 2>(j, s, stream) : launch_down<TYPE, 1>(j, s, stream);
     if (e != hipSuccess) return e;

@@ -71,8 +71,8 @@ __device__ __forceinline__ void mx_split8(const float (&v)[8], uint4 (&x)[P]) {
 }
 
 // Eight bf16 values of a row from column c on, zeros at and after `cols`.
-__device__ __forceinline__ uint4 mx_bf16_edge8(const uint16_t *row, int c, int cols, bool vec) {
-    if (vec && c + 8 <= cols) return *(const uint4 *)(row + c);
+__device__ __forceinline__ uint4 mx_bf16_edge8(const uint16_t *row, int c, int cols) {
+    if (c + 8 <= cols) return __builtin_bit_cast(uint4, *(const u32v4_any *)(row + c));
     uint32_t u[4] = {0, 0, 0, 0};
     if (c < cols)
 #pragma unroll
@@ -93,7 +93,7 @@ struct MxTokens {
 
     // The lane's tokens are in row[mt] (NULL: none, zeros), its columns in
     // slabs slab0 + kThinWaves i.
-    __device__ __forceinline__ void load(const T *const (&row)[MT], int slab0, int cols, bool vec, int q) {
+    __device__ __forceinline__ void load(const T *const (&row)[MT], int slab0, int cols, int q) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             back[mt] = 1.0f;
@@ -103,7 +103,7 @@ struct MxTokens {
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
                         const int c = (slab0 + kThinWaves * i) * kMxSlab + 32 * q + 8 * s;
-                        x[i][mt][s][0] = row[mt] ? mx_bf16_edge8(row[mt], c, cols, vec) : uint4{0, 0, 0, 0};
+                        x[i][mt][s][0] = row[mt] ? mx_bf16_edge8(row[mt], c, cols) : uint4{0, 0, 0, 0};
                     }
             } else {
                 float v[KS][4][8];
@@ -113,7 +113,7 @@ struct MxTokens {
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
                         const int c = (slab0 + kThinWaves * i) * kMxSlab + 32 * q + 8 * s;
-                        mx_load_edge8<TYPE>(row[mt], c, row[mt] ? cols : 0, vec, v[i][s]);
+                        mx_load_edge8<TYPE>(row[mt], c, row[mt] ? cols : 0, v[i][s]);
                     }
                 if constexpr (TYPE == SGEMM_TYPE_F32) {
 #pragma unroll

@@ -129,7 +129,7 @@ int scratch_of(int dev, char **out) {
 
 // A device pointer of the current device whose allocation holds `bytes`
 // bytes from p on.
-int check_device_range(const void *p, int64_t bytes, int dev) {
+int check_device_range(const void *p, int64_t bytes, int dev, uintptr_t *allocation_lo, uintptr_t *allocation_hi) {
     if (bytes <= 0) return SGEMM_OK;
     hipPointerAttribute_t attr;
     hipError_t e = hipPointerGetAttributes(&attr, p);
@@ -147,6 +147,8 @@ int check_device_range(const void *p, int64_t bytes, int dev) {
     }
     const uintptr_t lo = (uintptr_t)base, hi = lo + size, q = (uintptr_t)p;
     if (q < lo || q + (uint64_t)bytes > hi) return SGEMM_ERR_POINTER;
+    if (allocation_lo) *allocation_lo = lo;
+    if (allocation_hi) *allocation_hi = hi;
     return SGEMM_OK;
 }
 

@@ -420,14 +420,36 @@ int sgemm_f32_mx4_dequantize(int rows, int cols, const void *codes, const void *
  * C = alpha * A * B^T + beta * C for 4-bit matrices A (M x K) and B (N x K),
  * sums in fp32, rounded once to C's type.  As in sgemm_f32_gemm, beta == 0
  * means C is not read, and alpha == 0 or K == 0 that A and B are not (nor
- * checked).  A training step takes its three products from it: with W (N x K)
- * and the layer Y = X W^T, dX = dY W multiplies dY and W^T, dW = dY^T X
- * multiplies dY^T and X^T, each quantised along the sum.
+ * checked).
  */
 int sgemm_f32_mx4_gemm(int M, int N, int K, float alpha,
                        const void *a_codes, const void *a_scales,
                        const void *b_codes, const void *b_scales, float beta,
                        int type, void *C, int ldc, hipStream_t stream);
+
+/*
+ * A training step of the layer Y = X W^T in 4 bits, X (M x K), W (N x K), in
+ * two calls of few launches each: forward quantises X and W both ways, gives
+ * Y = q(X) q(W)^T in X's type and leaves X^T and W^T (K x M and K x N, 4-bit)
+ * for the backward call; that quantises dY both ways and gives dX = q(dY)
+ * q(W^T)^T in dY's type and dW = q(dY^T) q(X^T)^T + beta dW in fp32: the
+ * gradients with the rounding taken as the identity.  rule: as above.
+ * scratch: device memory of at least the bytes that
+ * sgemm_f32_mx4_train_scratch gives for the call (either may be NULL),
+ * 256-byte aligned, overlapping nothing.
+ */
+int sgemm_f32_mx4_train_forward(int M, int N, int K, int type, const void *X, int ldx,
+                                int type_w, const void *W, int ldw, int rule,
+                                void *Y, int ldy, void *xt_codes, void *xt_scales,
+                                void *wt_codes, void *wt_scales,
+                                void *scratch, long long scratch_bytes, hipStream_t stream);
+int sgemm_f32_mx4_train_backward(int M, int N, int K, int type, const void *dY, int lddy,
+                                 int rule, const void *xt_codes, const void *xt_scales,
+                                 const void *wt_codes, const void *wt_scales,
+                                 void *dX, int lddx, float beta, void *dW, int lddw,
+                                 void *scratch, long long scratch_bytes, hipStream_t stream);
+int sgemm_f32_mx4_train_scratch(int M, int N, int K, long long *forward_bytes,
+                                long long *backward_bytes);
 
 /*
  * Y = X * W^T for float rows X (M x K) and 4-bit weights W (N x K), Y (M x N)

@@ -321,6 +321,44 @@ def test_train(dev, dtype, m, n, k):
     close(both, host(start) + r(D.T) @ r(X.T).T, product_bound(r(D.T), r(X.T)) + 2.0 ** -22 * (np.abs(host(start)) + np.abs(host(dw))))
 
 
+def test_train_of_two_types_and_of_views(dev):
+    """X and W of different types, column-major, strided: the same results as of the plain copies."""
+    rng = np.random.default_rng(29)
+    m, n, k = 70, 90, 200
+    x, w, dy = normal(rng, m, k, torch.bfloat16, dev), normal(rng, n, k, torch.float32, dev), normal(rng, m, n, torch.bfloat16, dev)
+    y, saved = sg.mx4_train_forward(x, w)
+    want = (y, *sg.mx4_train_backward(dy, saved))
+    close(y, ref.rounded(host(x)) @ ref.rounded(host(w)).T, product_bound(ref.rounded(host(x)), ref.rounded(host(w))), torch.bfloat16)
+    columns = lambda t: t.t().contiguous().t()
+    for a, b, d in ((columns(x), w, dy), (x, columns(w), columns(dy)), (strided(x, 3, 1), strided(w, 1, 0), strided(dy, 5, 2))):
+        y, saved = sg.mx4_train_forward(a, b)
+        for got, exp in zip((y, *sg.mx4_train_backward(d, saved)), want):
+            assert torch.equal(got, exp)
+
+
+@pytest.mark.parametrize("m, n, k", [(0, 5, 7), (5, 0, 7), (5, 7, 0), (0, 0, 0)])
+def test_train_of_nothing(dev, m, n, k):
+    x, w, dy = (torch.ones(s, device=dev) for s in ((m, k), (n, k), (m, n)))
+    y, saved = sg.mx4_train_forward(x, w)
+    dw = torch.ones(n, k, device=dev)
+    dx, same = sg.mx4_train_backward(dy, saved, dW=dw)
+    assert torch.equal(y, torch.zeros(m, n, device=dev)) and torch.equal(dx, torch.zeros(m, k, device=dev))
+    assert same is dw and torch.equal(dw, torch.ones(n, k, device=dev))
+    assert torch.equal(sg.mx4_train_backward(dy, saved)[1], torch.zeros(n, k, device=dev))
+
+
+def test_train_refuses_what_does_not_fit(dev):
+    x, w = torch.zeros(4, 64, device=dev), torch.zeros(6, 64, device=dev)
+    y, saved = sg.mx4_train_forward(x, w)
+    for call, kind in ((lambda: sg.mx4_train_forward(x, w[:, :32]), ValueError), (lambda: sg.mx4_train_forward(x, w.double()), TypeError),
+                       (lambda: sg.mx4_train_forward(x, w, rule="up"), ValueError),
+                       (lambda: sg.mx4_train_backward(y[:3], saved), ValueError), (lambda: sg.mx4_train_backward(x, saved), ValueError),
+                       (lambda: sg.mx4_train_backward(y, saved, dW=w.bfloat16()), ValueError),
+                       (lambda: sg.mx4_train_backward(y, saved, dW=w[:5]), ValueError)):
+        with pytest.raises(kind):
+            call()
+
+
 def test_train_gradient_against_differences(dev):
     """On values that 4 bits hold exactly, before and after a step, the layer is bilinear: central differences of
     sum(dY * Y) are its gradient, exactly, up to the sums' fp32."""
@@ -561,6 +599,41 @@ def test_graph_replays(dev):
         torch.cuda.synchronize()
         for a, b in zip(outs, want):
             assert torch.equal(a, b)
+
+
+def test_many_rows(dev):
+    """More rows than one grid dimension counts, in every operator."""
+    rows, cols = 700001, 32
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(30)
+    x = torch.randn(rows, cols, generator=gen, device=dev)
+    q, qt = sg.mx4_quantize_both(x)
+    y = sg.mx4_dequantize(q)
+    yt = sg.mx4_dequantize(qt)
+    for r in (0, 262144, 524288, 699968):       # whole blocks along the columns; the last has one row more
+        assert np.array_equal(host(yt[:, r:r + 32]), ref.rounded(host(x[r:r + 32]).T))
+    pick = torch.tensor([0, 1, 262143, 262144, 524287, 524288, 700000], device=dev)
+    assert np.array_equal(host(y[pick]), ref.rounded(host(x[pick])))
+    again = sg.mx4_quantize(x)
+    assert torch.equal(again.codes, q.codes) and torch.equal(again.scales, q.scales)
+    a = sg.mx4_quantize(x[:5])
+    close(sg.mx4_gemm(q, a)[pick], host(y[pick]) @ ref.rounded(host(x[:5])).T, product_bound(host(y[pick]), ref.rounded(host(x[:5]))))
+    close(sg.mx4_linear(x[:3], q)[:, pick], host(x[:3]) @ host(y[pick]).T, product_bound(host(x[:3]), host(y[pick]), 3))
+
+
+def test_refuses_memory_that_is_not_the_devices(dev):
+    """Addresses outside an allocation of the device, and arrays that reach past their allocation's end."""
+    x, q = torch.zeros(4, 128, device=dev), sg.mx4_quantize(torch.zeros(4, 128, device=dev))
+    c, s = q.codes.data_ptr(), q.scales.data_ptr()
+    on_host = torch.zeros(4096, dtype=torch.uint8).data_ptr() & ~15
+    call = sg.library().sgemm_f32_mx4_quantize
+    stream = torch.cuda.current_stream().cuda_stream
+    assert call(4, 128, 0, x.data_ptr(), 128, 0, c, on_host, None, None, stream) == sg.ERR_POINTER
+    assert call(4, 128, 0, on_host, 128, 0, c, s, None, None, stream) == sg.ERR_POINTER
+    big = torch.empty(64 << 20, dtype=torch.uint8, device=dev)     # an allocation of its own
+    assert call(1 << 20, 128, 0, big.data_ptr(), 128, 0, c, s, None, None, stream) != sg.OK
+    assert call(4, 128, 0, x.data_ptr(), 128, 0, c, s, None, None, stream) == sg.OK
+    torch.cuda.synchronize()
 
 
 def test_offsets_past_32_bits(dev):

@@ -108,6 +108,48 @@ def test_linear_scratch():
     assert call(4, 4, 128, 0, None) == sg.ERR_NULL
 
 
+def forward(M=4, N=8, K=128, type=0, X=FAR, ldx=128, type_w=0, W=FAR * 2, ldw=128, rule=0, Y=FAR * 3, ldy=8, xt=FAR * 4, sxt=FAR * 5,
+            wt=FAR * 6, swt=FAR * 7, scratch=FAR * 8, nbytes=1 << 20):
+    return lib().sgemm_f32_mx4_train_forward(M, N, K, type, X, ldx, type_w, W, ldw, rule, Y, ldy, xt, sxt, wt, swt, scratch,
+                                             nbytes, None)
+
+
+def backward(M=4, N=8, K=128, type=0, D=FAR, ldd=8, rule=0, xt=FAR * 2, sxt=FAR * 3, wt=FAR * 4, swt=FAR * 5, dX=FAR * 6, lddx=128,
+             dW=FAR * 7, lddw=128, scratch=FAR * 8, nbytes=1 << 20):
+    return lib().sgemm_f32_mx4_train_backward(M, N, K, type, D, ldd, rule, xt, sxt, wt, swt, dX, lddx, 0.0, dW, lddw, scratch,
+                                              nbytes, None)
+
+
+@pytest.mark.parametrize("status, args", [
+    (sg.ERR_SHAPE, dict(M=-1)), (sg.ERR_SHAPE, dict(N=-1)), (sg.ERR_SHAPE, dict(K=-1)), (sg.ERR_CONFIG, dict(type=3)),
+    (sg.ERR_CONFIG, dict(type_w=3)), (sg.ERR_CONFIG, dict(rule=2)), (sg.ERR_LD, dict(ldx=127)), (sg.ERR_LD, dict(ldw=127)),
+    (sg.ERR_LD, dict(ldy=7)), (sg.ERR_NULL, dict(X=None)), (sg.ERR_NULL, dict(Y=None)), (sg.ERR_NULL, dict(swt=None)),
+    (sg.ERR_NULL, dict(scratch=None)), (sg.ERR_ALIGN, dict(scratch=FAR * 8 + 16)), (sg.ERR_ALIGN, dict(xt=FAR * 4 + 8)),
+    (sg.ERR_SCRATCH, dict(nbytes=100)), (sg.ERR_ALIAS, dict(Y=FAR)), (sg.ERR_ALIAS, dict(scratch=FAR * 2)),
+    (sg.ERR_ALIAS, dict(xt=FAR * 6)),
+])
+def test_train_forward_refuses(status, args):
+    assert forward(**args) == status
+
+
+@pytest.mark.parametrize("status, args", [
+    (sg.ERR_SHAPE, dict(M=-1)), (sg.ERR_CONFIG, dict(type=3)), (sg.ERR_CONFIG, dict(rule=-1)), (sg.ERR_LD, dict(ldd=7)),
+    (sg.ERR_LD, dict(lddx=127)), (sg.ERR_LD, dict(lddw=127)), (sg.ERR_NULL, dict(D=None)), (sg.ERR_NULL, dict(dW=None)),
+    (sg.ERR_NULL, dict(xt=None)), (sg.ERR_NULL, dict(scratch=None)), (sg.ERR_ALIGN, dict(dW=FAR * 7 + 2)),
+    (sg.ERR_SCRATCH, dict(nbytes=100)), (sg.ERR_ALIAS, dict(dX=FAR * 7)), (sg.ERR_ALIAS, dict(dW=FAR)),
+])
+def test_train_backward_refuses(status, args):
+    assert backward(**args) == status
+
+
+def test_train_scratch():
+    f, b = ctypes.c_longlong(), ctypes.c_longlong()
+    call = lib().sgemm_f32_mx4_train_scratch
+    assert call(4, 8, 128, ctypes.byref(f), ctypes.byref(b)) == sg.OK and f.value > 0 and b.value > 0
+    assert call(4, 8, 128, None, None) == sg.OK
+    assert call(-1, 8, 128, None, None) == sg.ERR_SHAPE
+
+
 def moe(tokens=2, hidden=128, inner=32, experts=4, top=2, norm=1, type=0, X=FAR, ldx=128, router=FAR * 2, ldr=128,
         up=FAR * 3, sup=FAR * 4, down=FAR * 5, sdown=FAR * 6, Y=FAR * 7, ldy=128, scratch=FAR * 8, nbytes=1 << 30):
     return lib().sgemm_f32_mx4_moe(tokens, hidden, inner, experts, top, norm, type, X, ldx, router, ldr, up, sup, down,
@@ -143,6 +185,7 @@ def test_empty_calls_touch_nothing():
     assert dequantize(cols=0, c=None, s=None, Y=None) == sg.OK
     assert gemm(M=0, a=None, sa=None, C=None) == sg.OK
     assert linear(N=0, c=None, s=None, Y=None) == sg.OK
+    assert gemm(N=0, b=None, sb=None, C=None) == sg.OK
     assert moe(tokens=0, X=None, Y=None, scratch=None) == sg.OK
 
 
