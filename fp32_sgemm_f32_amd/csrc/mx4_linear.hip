@@ -14,7 +14,9 @@ namespace {
 constexpr int kMostTokens = 64;   // of one pass over the weights
 
 // Whether the registers (128 a lane, without spills) let a CU hold two workgroups.
-constexpr bool two_on_a_cu(int pieces, int ks, int mt) { return pieces == 1 ? ks <= 2 && mt <= 2 : ks * mt == 1; }
+constexpr bool two_on_a_cu(int pieces, int ks, int mt) { return pieces == 1 ? mt == 1 || (mt == 2 && ks == 1) : ks * mt == 1; }
+// Row tiles that a wave adds up at a time.
+constexpr int group_of(int ks, int mt) { return mt > 1 ? 2 : ks == 4 ? 1 : 4; }
 
 struct Args {
     const void *x;
@@ -30,25 +32,27 @@ struct Args {
 template <int TYPE, int KS, int MT, int G>
 __global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, MT) ? 4 : 2) void linear_kernel(Args a) {
     typedef typename MxType<TYPE>::T T;
-    __shared__ __attribute__((aligned(16))) f32v4 red[kThinWaves * G * MT * 64];
+    __shared__ __attribute__((aligned(16))) f32v4 red[kThinSums<G, MT>];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int part = blockIdx.x % a.parts, first = blockIdx.x / a.parts * a.per, m0 = blockIdx.y * 16 * MT;
     const int tiles = (a.N + 15) / 16, end = first + a.per < tiles ? first + a.per : tiles;
-    const int slab0 = part * kThinWaves * KS + wave;
+    const int slab0 = (part * kThinWaves + wave) * KS;
+    const auto row_of = [&](int tile, int m) -> int64_t {
+        const int n = tile * 16 + m;
+        return n < a.N ? n : a.N - 1;   // rows past N: computed, not stored
+    };
     const T *row[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         const int t = m0 + mt * 16 + (lane & 15);
         row[mt] = t < a.M ? (const T *)a.x + t * a.ldx : nullptr;
     }
-    MxTokens<TYPE, mx_pieces(TYPE), KS, MT> x;
+    MxTokens<TYPE, mx_pieces(TYPE), KS, kThinWaves, MT> x;
     x.load(row, slab0, a.K, lane >> 4);
-    mx_stream<1, G>(
-        x, a.w, slab0, first, end, red, nullptr, true, true,
-        [&](int tile) -> int64_t {
-            const int n = tile * 16 + (lane & 15);
-            return n < a.N ? n : a.N - 1;   // rows past N: computed, not stored
-        },
+    MxStream<1, G, KS, kThinWaves, false> stream;
+    stream.begin(a.w, slab0, first, end, row_of);
+    stream.run(
+        x, a.w, slab0, first, end, red, nullptr, true, true, row_of,
         [&](int tile, int mt, int l, const f32v4(&v)[1]) {
             const int t = m0 + mt * 16 + (l & 15), n = tile * 16 + 4 * (l >> 4);
             if (t >= a.M) return;
@@ -98,7 +102,7 @@ int k_parts(int M, int K, int type) {
 
 template <int TYPE, int KS, int MT>
 hipError_t launch_shape(Args a, hipStream_t s) {
-    constexpr int G = KS * MT >= 4 ? 2 : 4;
+    constexpr int G = group_of(KS, MT);
     // Workgroups: as many as the CUs hold at once.
     constexpr int kWant = two_on_a_cu(mx_pieces(TYPE), KS, MT) ? 512 : 256;
     const int tiles = (a.N + 15) / 16, groups = kWant / a.parts > 0 ? kWant / a.parts : 1;

@@ -38,10 +38,10 @@ namespace sgemm {
 namespace {
 
 constexpr int kFew = 16;
-// Row tiles that `up` adds up at a time, and whether its registers let a CU
-// hold two workgroups.
-constexpr int up_group(int ks) { return ks >= 2 ? 2 : 4; }
-constexpr bool up_two_on_a_cu(int pieces, int ks) { return pieces * ks <= 2; }
+// Row tiles that a wave adds up at a time (as many loads in flight as the
+// registers hold), and whether the registers let a CU hold two workgroups.
+constexpr int group_of(int pieces, int ks, bool few) { return few || ks * pieces > 4 ? 2 : 4; }
+constexpr bool two_on_a_cu(int pieces, int ks, bool few) { return ks * (16 * pieces + 5 * group_of(pieces, ks, few)) <= 56; }
 constexpr int act_pieces(int type) { return type == SGEMM_TYPE_F32 ? 3 : 2; }
 
 // Scratch memory, every part 256-byte aligned.
@@ -204,46 +204,47 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
 // ---- up ----
 
-template <int TYPE, int KS, bool FEW>
-__global__ __launch_bounds__(kThinThreads, up_two_on_a_cu(mx_pieces(TYPE), KS) ? 4 : 2) void up_kernel(MxMoeJob j, Scratch s,
+template <int TYPE, int KS, int WK, bool FEW>
+__global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, FEW) ? 4 : 2) void up_kernel(MxMoeJob j, Scratch s,
                                                                                                       MxWeights w, int per) {
     typedef typename MxType<TYPE>::T T;
-    constexpr int G = up_group(KS), PA = act_pieces(TYPE);
+    constexpr int G = group_of(mx_pieces(TYPE), KS, FEW), PA = act_pieces(TYPE);
     const int all = j.tokens * j.top;
     // red, then the sums kept from one piece of K to the next.
     extern __shared__ __attribute__((aligned(16))) f32v4 red[];
     __shared__ int list[SGEMM_MX4_MAX_TOKENS], count;
     __shared__ std::conditional_t<FEW, Choice, int> choice;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15;
-    MxTokens<TYPE, mx_pieces(TYPE), KS, 1> x;
+    const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK, l16 = lane & 15;
+    MxTokens<TYPE, mx_pieces(TYPE), KS, WK, 1> x;
+    MxStream<2, G, KS, WK, true> stream;
+    // Row tiles come in pairs: 16 rows of the gate, the same 16 of U.
+    const int tiles = 2 * ((j.inner + 15) / 16), first = blockIdx.x * per, end = first + per < tiles ? first + per : tiles;
     int e = blockIdx.y, n = 1;
+    const auto row_of = [&](int tile, int m) -> int64_t {
+        const int f = (tile >> 1) * 16 + m;
+        return (int64_t)2 * e * j.inner + (f < j.inner ? f : j.inner - 1) + (tile & 1 ? j.inner : 0);
+    };
     if constexpr (FEW) {
         // blockIdx.y: a choice.  Its token is known before its expert.
         const int t = blockIdx.y / j.top;
         const T *row[1] = {l16 == 0 ? (const T *)j.x + (int64_t)t * j.ldx : nullptr};
-        x.load(row, wave, j.hidden, lane >> 4);
+        x.load(row, kw * KS, j.hidden, lane >> 4);
         rank_experts(j, s.logits + (int64_t)t * j.experts, choice);
         e = choice.expert[blockIdx.y % j.top];
     } else {
         n = list_tokens(s.chosen, all, e, list, &count);
     }
-    // Row tiles come in pairs: 16 rows of the gate, the same 16 of U.
-    const int tiles = 2 * ((j.inner + 15) / 16), first = blockIdx.x * per, end = first + per < tiles ? first + per : tiles;
-    const int64_t base = (int64_t)2 * e * j.inner;
-    const auto row_of = [&](int tile) -> int64_t {
-        const int f = (tile >> 1) * 16 + l16;
-        return base + (f < j.inner ? f : j.inner - 1) + (tile & 1 ? j.inner : 0);
-    };
     for (int i0 = 0; i0 < n; i0 += 16) {
         const T *row[1] = {nullptr};
         if (i0 + l16 < n) {
             const int a = FEW ? (int)blockIdx.y : list[i0 + l16];
             row[0] = (const T *)j.x + (int64_t)(a / j.top) * j.ldx;
         }
-        for (int s0 = 0; s0 < w.slabs; s0 += kThinWaves * KS) {
-            if (!FEW || s0 > 0) x.load(row, s0 + wave, j.hidden, lane >> 4);
-            mx_stream<2, G>(x, w, s0 + wave, first, end, red, red + kThinWaves * G * 64, s0 == 0, s0 + kThinWaves * KS >= w.slabs,
-                            row_of, [&](int tile, int, int l, const f32v4(&v)[2]) {
+        for (int s0 = 0; s0 < w.slabs; s0 += WK * KS) {
+            if (!FEW || s0 > 0) x.load(row, s0 + kw * KS, j.hidden, lane >> 4);
+            stream.begin(w, s0 + kw * KS, first, end, row_of);
+            stream.run(x, w, s0 + kw * KS, first, end, red, red + kThinSums<G, 1>, s0 == 0, s0 + WK * KS >= w.slabs, row_of,
+                       [&](int tile, int, int l, const f32v4(&v)[2]) {
                                 const int i = i0 + (l & 15), f = (tile >> 1) * 16 + 4 * (l >> 4);
                                 if (i >= n) return;
                                 uint16_t p[4][PA];
@@ -267,25 +268,28 @@ __global__ __launch_bounds__(kThinThreads, up_two_on_a_cu(mx_pieces(TYPE), KS) ?
 
 // ---- down ----
 
-template <int TYPE, int KS>
-__global__ __launch_bounds__(kThinThreads, 2) void down_kernel(MxMoeJob j, Scratch s, MxWeights w, int per) {
-    constexpr int G = 4;
+template <int P, int KS, int WK>
+__global__ __launch_bounds__(kThinThreads, two_on_a_cu(P, KS, false) ? 4 : 2) void down_kernel(MxMoeJob j, Scratch s, MxWeights w,
+                                                                                             int per) {
+    constexpr int G = group_of(P, KS, false);
     extern __shared__ __attribute__((aligned(16))) f32v4 red[];
     __shared__ int list[SGEMM_MX4_MAX_TOKENS], count;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, e = blockIdx.y;
-    const int n = list_tokens(s.chosen, j.tokens * j.top, e, list, &count);
+    const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK, l16 = lane & 15, e = blockIdx.y;
     const int tiles = (j.hidden + 15) / 16, first = blockIdx.x * per, end = first + per < tiles ? first + per : tiles;
+    const auto row_of = [&](int tile, int m) -> int64_t {
+        const int h = tile * 16 + m;
+        return (int64_t)e * j.hidden + (h < j.hidden ? h : j.hidden - 1);
+    };
+    MxStream<1, G, KS, WK, true> stream;
+    const int n = list_tokens(s.chosen, j.tokens * j.top, e, list, &count);
     for (int i0 = 0; i0 < n; i0 += 16) {
         const uint16_t *row = i0 + l16 < n ? s.act + (int64_t)list[i0 + l16] * s.ld_act : nullptr;
-        for (int s0 = 0; s0 < w.slabs; s0 += kThinWaves * KS) {
-            MxTokens<SGEMM_TYPE_BF16, act_pieces(TYPE), KS, 1> x;
-            x.load_pieces(row, (int64_t)j.tokens * j.top * s.ld_act, s0 + wave, (int)s.ld_act, lane >> 4);
-            mx_stream<1, G>(
-                x, w, s0 + wave, first, end, red, red + kThinWaves * G * 64, s0 == 0, s0 + kThinWaves * KS >= w.slabs,
-                [&](int tile) -> int64_t {
-                    const int h = tile * 16 + l16;
-                    return (int64_t)e * j.hidden + (h < j.hidden ? h : j.hidden - 1);
-                },
+        for (int s0 = 0; s0 < w.slabs; s0 += WK * KS) {
+            MxTokens<SGEMM_TYPE_BF16, P, KS, WK, 1> x;
+            x.load_pieces(row, (int64_t)j.tokens * j.top * s.ld_act, s0 + kw * KS, (int)s.ld_act, lane >> 4);
+            stream.begin(w, s0 + kw * KS, first, end, row_of);
+            stream.run(
+                x, w, s0 + kw * KS, first, end, red, red + kThinSums<G, 1>, s0 == 0, s0 + WK * KS >= w.slabs, row_of,
                 [&](int tile, int, int l, const f32v4(&v)[1]) {
                     const int i = i0 + (l & 15);
                     if (i < n) *(f32v4 *)(s.part + (int64_t)list[i] * s.ld_part + tile * 16 + 4 * (l >> 4)) = v[0];
@@ -299,6 +303,7 @@ __global__ __launch_bounds__(256) void join_kernel(MxMoeJob j, Scratch s) {
     const int h = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
     if (h >= j.hidden) return;
     float sum = 0.0f;
+#pragma unroll 8
     for (int i = t * j.top; i < (t + 1) * j.top; ++i) sum = fmaf(s.weight[i], s.part[i * s.ld_part + h], sum);
     ((typename MxType<TYPE>::T *)j.y)[t * j.ldy + h] = MxType<TYPE>::from(sum);
 }
@@ -379,38 +384,71 @@ int groups_of(int tiles, int unit, int slots, int fill, int most) {
 // comes in several pieces (their sums stay in LDS).
 constexpr int kCarryTiles = 32;
 
-template <int TYPE, int KS, bool FEW>
+// More than 64 KiB of LDS has to be asked for.
+hipError_t allow_lds(const void *kernel, int bytes) {
+    return bytes > 48 * 1024 ? hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) : hipSuccess;
+}
+
+template <int TYPE, int KS, int WK, bool FEW>
 hipError_t launch_up(MxMoeJob &j, Scratch &s, hipStream_t stream) {
-    constexpr int G = up_group(KS);
+    constexpr int G = group_of(mx_pieces(TYPE), KS, FEW);
     MxWeights w = mx_weights(j.up, j.sup, (int64_t)2 * j.experts * j.inner, j.hidden);
     const int tiles = 2 * ((j.inner + 15) / 16), all = j.tokens * j.top, slots = FEW ? all : all < j.experts ? all : j.experts;
-    const bool pieces = w.slabs > kThinWaves * KS;
-    int per = mx_share(tiles, groups_of(tiles, 2, slots, FEW && !up_two_on_a_cu(mx_pieces(TYPE), KS) ? 256 : 512, pieces ? kCarryTiles : tiles), 2);
-    const int bytes = (kThinWaves * G + (pieces ? kCarryTiles : 0)) * 64 * 16;
+    const bool pieces = w.slabs > WK * KS;
+    const int fill = FEW && !two_on_a_cu(mx_pieces(TYPE), KS, FEW) ? 256 : 512;
+    int per = mx_share(tiles, groups_of(tiles, 2, slots, fill, pieces ? kCarryTiles : tiles), 2);
+    const int bytes = (kThinSums<G, 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
     void *params[] = {&j, &s, &w, &per};
-    return hipLaunchKernel((const void *)up_kernel<TYPE, KS, FEW>,
+    const hipError_t e = allow_lds((const void *)up_kernel<TYPE, KS, WK, FEW>, bytes);
+    if (e != hipSuccess) return e;
+    return hipLaunchKernel((const void *)up_kernel<TYPE, KS, WK, FEW>,
                            dim3((unsigned)((tiles + per - 1) / per), (unsigned)(FEW ? all : j.experts)), dim3(kThinThreads), params,
                            bytes, stream);
 }
 
+// (slabs a wave keeps, waves along K) for a number of slabs: few idle places,
+// and no more slabs than the pieces leave registers for.
 template <int TYPE, bool FEW>
 hipError_t launch_up_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
-    const int need = (mx_slabs(j.hidden) + kThinWaves - 1) / kThinWaves;
+    const int n = mx_slabs(j.hidden);
+    if constexpr (!FEW) {   // (few choices: latency counts, all waves along K)
+        if (n <= 2) return launch_up<TYPE, 1, 2, FEW>(j, s, stream);
+        if (n <= 4) return launch_up<TYPE, 1, 4, FEW>(j, s, stream);
+        if (n <= 8) return launch_up<TYPE, 2, 4, FEW>(j, s, stream);
+        if constexpr (TYPE == SGEMM_TYPE_BF16) {
+            if (n <= 12) return launch_up<TYPE, 3, 4, FEW>(j, s, stream);
+            if (n > 16 && n <= 24) return launch_up<TYPE, 3, 8, FEW>(j, s, stream);
+        }
+    }
     if constexpr (TYPE == SGEMM_TYPE_BF16)
-        if (need > 2) return launch_up<TYPE, 4, FEW>(j, s, stream);
-    return need > 1 ? launch_up<TYPE, 2, FEW>(j, s, stream) : launch_up<TYPE, 1, FEW>(j, s, stream);
+        if (n > 16) return launch_up<TYPE, 4, 8, FEW>(j, s, stream);
+    return n > 8 ? launch_up<TYPE, 2, 8, FEW>(j, s, stream) : launch_up<TYPE, 1, 8, FEW>(j, s, stream);
 }
 
-template <int TYPE, int KS>
+template <int P, int KS, int WK>
 hipError_t launch_down(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     MxWeights w = mx_weights(j.down, j.sdown, (int64_t)j.experts * j.hidden, j.inner);
     const int tiles = (j.hidden + 15) / 16, all = j.tokens * j.top, slots = all < j.experts ? all : j.experts;
-    const bool pieces = w.slabs > kThinWaves * KS;
+    const bool pieces = w.slabs > WK * KS;
     int per = mx_share(tiles, groups_of(tiles, 1, slots, 512, pieces ? kCarryTiles : tiles), 1);
-    const int bytes = (kThinWaves * 4 + (pieces ? kCarryTiles : 0)) * 64 * 16;
+    const int bytes = (kThinSums<group_of(P, KS, false), 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
     void *params[] = {&j, &s, &w, &per};
-    return hipLaunchKernel((const void *)down_kernel<TYPE, KS>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)j.experts),
+    const hipError_t e = allow_lds((const void *)down_kernel<P, KS, WK>, bytes);
+    if (e != hipSuccess) return e;
+    return hipLaunchKernel((const void *)down_kernel<P, KS, WK>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)j.experts),
                            dim3(kThinThreads), params, bytes, stream);
+}
+
+template <int P>
+hipError_t launch_down_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
+    const int n = mx_slabs(j.inner);
+    if (n <= 1) return launch_down<P, 1, 1>(j, s, stream);
+    if (n <= 2) return launch_down<P, 1, 2>(j, s, stream);
+    if (n <= 4) return launch_down<P, 2, 2>(j, s, stream);
+    if (n <= 6) return launch_down<P, 3, 2>(j, s, stream);
+    if (n <= 8) return launch_down<P, 2, 4>(j, s, stream);
+    if (n <= 16) return launch_down<P, 2, 8>(j, s, stream);
+    return launch_down<P, 3, 8>(j, s, stream);
 }
 
 template <int TYPE>
@@ -436,7 +474,7 @@ hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
     if (e != hipSuccess) return e;
     e = launch_up_slabs<TYPE, false>(j, s, stream);
     if (e != hipSuccess) return e;
-    e = mx_slabs(j.inner) > kThinWaves ? launch_down<TYPE, 2>(j, s, stream) : launch_down<TYPE, 1>(j, s, stream);
+    e = launch_down_slabs<act_pieces(TYPE)>(j, s, stream);
     if (e != hipSuccess) return e;
     return hipLaunchKernel((const void *)join_kernel<TYPE>, dim3((unsigned)((j.hidden + 255) / 256), (unsigned)j.tokens), dim3(256),
                            params, 0, stream);

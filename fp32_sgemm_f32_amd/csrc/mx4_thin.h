@@ -2,7 +2,7 @@
 // the thin product and the expert layer.
 //
 // A workgroup of 8 waves owns a piece of K and streams rows of weights past
-// it.  A wave keeps its tokens' part of KS slabs (128 columns each) in operand
+// it; where K is short, sets of WK < 8 waves own it and share the rows.  A wave keeps its tokens' part of KS slabs (128 columns each) in operand
 // registers for as long as it lives and takes 16 rows of weights and those
 // slabs at a time: lane l loads the 16 bytes (one block, 32 codes) of row
 // l % 16 and block q = l / 16, so a wave reads 64 bytes of each row and
@@ -70,6 +70,29 @@ __device__ __forceinline__ void mx_split8(const float (&v)[8], uint4 (&x)[P]) {
                      (uint32_t)p[4][k] | (uint32_t)p[5][k] << 16, (uint32_t)p[6][k] | (uint32_t)p[7][k] << 16};
 }
 
+// The same for P > 1 and finite values, in half the instructions: the first
+// piece is cut (rounded, the largest floats would become infinite), the
+// others are rounded to nearest, two at a time; of three the last is exact.
+template <int P>
+__device__ __forceinline__ void mx_split8_finite(const float (&v)[8], uint4 (&x)[P]) {
+    uint32_t w[P][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = __float_as_uint(v[2 * i]), b = __float_as_uint(v[2 * i + 1]);
+        w[0][i] = __builtin_amdgcn_perm(b, a, 0x07060302u);   // the upper halves of both
+        float ra = v[2 * i] - __uint_as_float(a & 0xffff0000u), rb = v[2 * i + 1] - __uint_as_float(b & 0xffff0000u);
+#pragma unroll
+        for (int k = 1; k < P; ++k) {
+            const bf16v2 p{(__bf16)ra, (__bf16)rb};
+            w[k][i] = __builtin_bit_cast(uint32_t, p);
+            ra -= __uint_as_float(w[k][i] << 16);
+            rb -= __uint_as_float(w[k][i] & 0xffff0000u);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < P; ++k) x[k] = uint4{w[k][0], w[k][1], w[k][2], w[k][3]};
+}
+
 // Eight bf16 values of a row from column c on, zeros at and after `cols`.
 __device__ __forceinline__ uint4 mx_bf16_edge8(const uint16_t *row, int c, int cols) {
     if (c + 8 <= cols) return __builtin_bit_cast(uint4, *(const u32v4_any *)(row + c));
@@ -84,15 +107,15 @@ __device__ __forceinline__ uint4 mx_bf16_edge8(const uint16_t *row, int c, int c
 // What fp32 values whose largest magnitude has these bits are multiplied by.
 __device__ __forceinline__ float mx_lift(uint32_t largest) { return largest < 0x21800000u ? 0x1p32f : 1.0f; }
 
-// A wave's tokens: MT tiles of 16, KS slabs, P pieces.
-template <int TYPE, int P, int KS, int MT>
+// A wave's tokens: MT tiles of 16, KS slabs, P pieces; WK waves share K.
+template <int TYPE, int P, int KS, int WK, int MT>
 struct MxTokens {
     typedef typename MxType<TYPE>::T T;
     uint4 x[KS][MT][4][P];
     float back[MT];   // what sums of a token are multiplied by
 
     // The lane's tokens are in row[mt] (NULL: none, zeros), its columns in
-    // slabs slab0 + kThinWaves i.
+    // slabs slab0 + i.
     __device__ __forceinline__ void load(const T *const (&row)[MT], int slab0, int cols, int q) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -102,7 +125,7 @@ struct MxTokens {
                 for (int i = 0; i < KS; ++i)
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
-                        const int c = (slab0 + kThinWaves * i) * kMxSlab + 32 * q + 8 * s;
+                        const int c = (slab0 + i) * kMxSlab + 32 * q + 8 * s;
                         x[i][mt][s][0] = row[mt] ? mx_bf16_edge8(row[mt], c, cols) : uint4{0, 0, 0, 0};
                     }
             } else {
@@ -112,7 +135,7 @@ struct MxTokens {
                 for (int i = 0; i < KS; ++i)
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
-                        const int c = (slab0 + kThinWaves * i) * kMxSlab + 32 * q + 8 * s;
+                        const int c = (slab0 + i) * kMxSlab + 32 * q + 8 * s;
                         mx_load_edge8<TYPE>(row[mt], c, row[mt] ? cols : 0, v[i][s]);
                     }
                 if constexpr (TYPE == SGEMM_TYPE_F32) {
@@ -139,10 +162,17 @@ struct MxTokens {
 #pragma unroll
                             for (int k = 0; k < 8; ++k) v[i][s][k] *= lift;
                 }
+                if (TYPE == SGEMM_TYPE_F32 && P > 1 && m < 0x7f800000u) {
 #pragma unroll
-                for (int i = 0; i < KS; ++i)
+                    for (int i = 0; i < KS; ++i)
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) mx_split8<P>(v[i][s], x[i][mt][s]);
+                        for (int s = 0; s < 4; ++s) mx_split8_finite<P>(v[i][s], x[i][mt][s]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) mx_split8<P>(v[i][s], x[i][mt][s]);
+                }
             }
         }
     }
@@ -158,11 +188,15 @@ struct MxTokens {
             for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    const int c = (slab0 + kThinWaves * i) * kMxSlab + 32 * q + 8 * s;
+                    const int c = (slab0 + i) * kMxSlab + 32 * q + 8 * s;
                     x[i][0][s][p] = row && c < cols ? *(const uint4 *)(row + p * stride + c) : uint4{0, 0, 0, 0};
                 }
     }
 };
+
+// Sums in LDS of a stream.
+template <int G, int MT>
+constexpr int kThinSums = 2 * kThinWaves * G * MT * 64;
 
 // A lane's weights of one slab: its block's codes and scale.
 struct MxBlock {
@@ -185,13 +219,16 @@ struct MxWeights {
     int64_t rowb, plane;   // bytes of a row of codes, words of a plane of scales
     int slabs;
 
+    // Zeros past the last slab.
+    template <bool NT>
+    __device__ __forceinline__ uint4 codes16(int64_t row, int slab, int q) const {
+        if (slab >= slabs) return uint4{0, 0, 0, 0};
+        const i32v4 *p = (const i32v4 *)(codes + row * rowb + (int64_t)slab * kMxSlabBytes + 16 * q);
+        return __builtin_bit_cast(uint4, NT ? __builtin_nontemporal_load(p) : *p);
+    }
+    __device__ __forceinline__ uint32_t word(int64_t row, int slab) const { return slab < slabs ? words[slab * plane + row] : 0; }
     __device__ __forceinline__ MxBlock load(int64_t row, int slab, int q) const {
-        MxBlock b{uint4{0, 0, 0, 0}, 0};
-        if (slab < slabs) {
-            b.codes = *(const uint4 *)(codes + row * rowb + (int64_t)slab * kMxSlabBytes + 16 * q);
-            b.word = words[slab * plane + row];
-        }
-        return b;
+        return MxBlock{codes16<true>(row, slab, q), word(row, slab)};
     }
 };
 
@@ -199,77 +236,136 @@ inline __host__ __device__ MxWeights mx_weights(const uint8_t *codes, const uint
     return MxWeights{codes, (const uint32_t *)scales, (int64_t)mx_slabs(cols) * kMxSlabBytes, mx_plane_rows(rows), mx_slabs(cols)};
 }
 
-// Streams row tiles [first, end) past the tokens: row(tile) is the lane's row
-// of weights, emit(tile, mt, l, sums) takes the sums of U tiles (tile .. tile
-// + U - 1) for token l % 16 of tile mt, rows 4 (l / 16) .. + 3 of each.  red:
-// LDS for kThinWaves * G * MT * 64 sums.  With K in several pieces, carry
-// (LDS, (end - first) * MT * 64 sums) holds them from the first piece to the
-// last.  Every thread of the workgroup calls this.
-template <int U, int G, int TYPE, int P, int KS, int MT, class Row, class Emit>
-__device__ __forceinline__ void mx_stream(const MxTokens<TYPE, P, KS, MT> &x, const MxWeights &w, int slab0, int first, int end,
-                                          f32v4 *red, f32v4 *carry, bool first_piece, bool last_piece, Row row, Emit emit) {
+// Streams row tiles [first, end) past the tokens.  WK waves share K,
+// kThinWaves / WK sets of them the row tiles; a wave takes G tiles at a time,
+// U of them next to each other (whose sums one thread then holds), and loads
+// the next G while it multiplies.
+// NT: the weights are read past the caches (used once, and more of them than
+// the caches hold).
+template <int U, int G, int KS, int WK, bool NT>
+struct MxStream {
     static_assert(G % U == 0, "whole units in a group");
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4;
+    static constexpr int WR = kThinWaves / WK;
     MxBlock b[G][KS];
-    auto fetch = [&](int g, int tile) {
-        if (tile < end) {
-            const int64_t r = row(tile);
-#pragma unroll
-            for (int i = 0; i < KS; ++i) b[g][i] = w.load(r, slab0 + kThinWaves * i, q);
-        }
-    };
-#pragma unroll
-    for (int g = 0; g < G; ++g) fetch(g, first + g);
-    for (int t0 = first; t0 < end; t0 += G) {
-        f32v4 acc[G][MT];
+
+    // Slot g's tile in the group that begins at t0.
+    static __device__ __forceinline__ int tile_of(int t0, int g) {
+        return t0 + g / U * (WR * U) + (int)(threadIdx.x >> 6) / WK * U + g % U;
+    }
+    // Whether slabs i and i + 1 are loaded together.
+    static constexpr bool pair(int i) { return i % 2 == 0 && i + 1 < KS; }
+
+    // Sends for slab i, or the pair i, i + 1, of every slot's tile in the group
+    // that begins at t0 (past the end: nothing; what is computed from what
+    // the registers hold is dropped).
+    template <class Row>
+    __device__ __forceinline__ void fetch(const MxWeights &w, int slab0, int i, int t0, int end, Row row) {
+        const int m = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) acc[g][mt] = f32v4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (t0 + g < end) {
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    const float scale = mx_scale(b[g][i], q);
-                    const uint32_t c[4] = {b[g][i].codes.x, b[g][i].codes.y, b[g][i].codes.z, b[g][i].codes.w};
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const bf16v8 v = mx_bf16x8(c[s], scale);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                            for (int p = 0; p < P; ++p) acc[g][mt] = mx_mfma(v, x.x[i][mt][s][p], acc[g][mt]);
-                    }
-                }
-                fetch(g, t0 + G + g);
+            const int tile = tile_of(t0, g);
+            if (tile >= end) continue;
+            const int64_t r = row(tile, m);
+            if (pair(i)) {
+                b[g][i].codes = w.codes16<NT>(row(tile, m & 7), slab0 + i + (m >> 3), q);
+                b[g][i + 1].codes = w.codes16<NT>(row(tile, 8 + (m & 7)), slab0 + i + (m >> 3), q);
+                b[g][i + 1].word = w.word(r, slab0 + i + 1);
+            } else {
+                b[g][i].codes = w.codes16<NT>(r, slab0 + i, q);
             }
+            b[g][i].word = w.word(r, slab0 + i);
         }
-        if (t0 > first) __syncthreads();   // the group before has been added up
+    }
+
+    // The registers of a pair as loaded -> slab i and slab i + 1 of row l % 16.
+    __device__ __forceinline__ void exchange(uint4 &x, uint4 &y) {
+        const bool upper = threadIdx.x & 8;
+        const auto one = [&](uint32_t &p, uint32_t &r) {
+            const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(upper ? p : r), 0x128, 15, 15, true);   // of lane l ^ 8
+            if (upper) p = got;
+            else r = got;
+        };
+        one(x.x, y.x), one(x.y, y.y), one(x.z, y.z), one(x.w, y.w);
+    }
+
+    // Sends for the first group's weights; row(tile, m) is row m of a tile,
+    // slab0 the wave's first slab.
+    template <class Row>
+    __device__ __forceinline__ void begin(const MxWeights &w, int slab0, int first, int end, Row row) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                if constexpr (TYPE == SGEMM_TYPE_F32) acc[g][mt] *= x.back[mt];
-                red[((wave * G + g) * MT + mt) * 64 + lane] = acc[g][mt];
-            }
-        __syncthreads();
-        for (int i = tid; i < G / U * MT * 64; i += kThinThreads) {
-            const int l = i & 63, mt = (i >> 6) % MT, g = (i >> 6) / MT * U;
-            if (t0 + g >= end) break;
-            f32v4 v[U];
+            for (int i = 0; i < KS; ++i) b[g][i] = MxBlock{uint4{0, 0, 0, 0}, 0};
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                v[u] = red[((g + u) * MT + mt) * 64 + l];
-#pragma unroll
-                for (int k = 1; k < kThinWaves; ++k) v[u] += red[((k * G + g + u) * MT + mt) * 64 + l];
-                f32v4 *kept = carry + ((t0 - first + g + u) * MT + mt) * 64 + l;
-                if (!first_piece) v[u] = *kept + v[u];
-                if (!last_piece) *kept = v[u];
-            }
-            if (last_piece) emit(t0 + g, mt, l, v);
-        }
+        for (int i = 0; i < KS; i += pair(i) ? 2 : 1) fetch(w, slab0, i, first, end, row);
     }
-    __syncthreads();   // red is free
-}
+
+    // After begin with the same arguments.  emit(tile, mt, l, sums) takes the
+    // sums of U tiles (tile .. tile + U - 1) for token l % 16 of tile mt, rows
+    // 4 (l / 16) .. + 3 of each.  red: LDS for kThinSums<G, MT> sums.
+    // With K in several pieces, carry (LDS, (end - first) * MT * 64 sums)
+    // holds them from the first piece to the last.  Every thread of the
+    // workgroup calls this.
+    template <int TYPE, int P, int MT, class Row, class Emit>
+    __device__ __forceinline__ void run(const MxTokens<TYPE, P, KS, WK, MT> &x, const MxWeights &w, int slab0, int first, int end,
+                                        f32v4 *red, f32v4 *carry, bool first_piece, bool last_piece, Row row, Emit emit) {
+        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4;
+        for (int t0 = first; t0 < end; t0 += G * WR) {
+            f32v4 acc[G][MT];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) acc[g][mt] = f32v4{0.0f, 0.0f, 0.0f, 0.0f};
+            // The G tiles in turn: their products do not wait for each other.
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                if (pair(i)) {
+#pragma unroll
+                    for (int g = 0; g < G; ++g) exchange(b[g][i].codes, b[g][i + 1 < KS ? i + 1 : i].codes);
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const uint4 c = b[g][i].codes;
+                        const bf16v8 v = mx_bf16x8(s == 0 ? c.x : s == 1 ? c.y : s == 2 ? c.z : c.w, mx_scale(b[g][i], q));
+#pragma unroll
+                        for (int p = 0; p < P; ++p)
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) acc[g][mt] = mx_mfma(v, x.x[i][mt][s][p], acc[g][mt]);
+                    }
+                if (!pair(i)) fetch(w, slab0, i % 2 == 1 ? i - 1 : i, t0 + G * WR, end, row);
+            }
+            // Two halves of red in turn: one meeting for a group.
+            f32v4 *half = red + ((t0 - first) / (G * WR) & 1) * (kThinWaves * G * MT * 64);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    if constexpr (TYPE == SGEMM_TYPE_F32) acc[g][mt] *= x.back[mt];
+                    half[((wave * G + g) * MT + mt) * 64 + lane] = acc[g][mt];
+                }
+            __syncthreads();
+            for (int i = tid; i < G / U * WR * MT * 64; i += kThinThreads) {
+                const int l = i & 63, mt = (i >> 6) % MT, unit = (i >> 6) / MT, set = unit % WR, g = unit / WR * U;
+                if (t0 + unit * U >= end) break;
+                f32v4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const f32v4 *from = half + ((set * WK * G + g + u) * MT + mt) * 64 + l;
+                    v[u] = *from;
+#pragma unroll
+                    for (int k = 1; k < WK; ++k) v[u] += from[k * G * MT * 64];
+                    f32v4 *kept = carry + ((t0 - first + unit * U + u) * MT + mt) * 64 + l;
+                    if (!first_piece) v[u] = *kept + v[u];
+                    if (!last_piece) *kept = v[u];
+                }
+                if (last_piece) emit(t0 + unit * U, mt, l, v);
+            }
+        }
+        __syncthreads();   // red is free
+    }
+};
 
 // The number of row tiles each workgroup of `groups` takes.
 inline int mx_share(int tiles, int groups, int unit) {

@@ -460,7 +460,9 @@ def moe_want(x, router, up, down, top, norm, dtype):
 
 MOES = [(1, 1, 1, 1, 1), (1, 4, 128, 32, 2), (1, 8, 256, 96, 8), (2, 8, 100, 33, 3), (5, 16, 130, 64, 4), (16, 8, 257, 129, 2),
         (17, 6, 64, 200, 6), (33, 60, 96, 40, 4), (48, 16, 128, 160, 8), (64, 5, 72, 48, 1), (64, 128, 64, 32, 16), (3, 300, 40, 16, 5),
-        (1, 1024, 33, 16, 16), (1, 16, 1200, 520, 3), (4, 8, 640, 1100, 2)]
+        (1, 1024, 33, 16, 16), (1, 16, 1200, 520, 3), (4, 8, 640, 1100, 2),
+        (3, 4, 4200, 40, 4), (20, 4, 4200, 70, 2), (1, 4, 2200, 100, 2), (33, 3, 2200, 150, 2), (2, 3, 100, 3400, 2), (18, 2, 80, 3400, 2),
+        (17, 3, 900, 900, 2), (40, 4, 1500, 300, 3), (30, 2, 2700, 450, 1)]
 
 
 @typed
