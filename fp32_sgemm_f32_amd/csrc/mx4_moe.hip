@@ -38,10 +38,14 @@ namespace sgemm {
 namespace {
 
 constexpr int kFew = 16;
-// Row tiles that a wave adds up at a time (as many loads in flight as the
-// registers hold), and whether the registers let a CU hold two workgroups.
-constexpr int group_of(int pieces, int ks, bool few) { return few || ks * pieces > 4 ? 2 : 4; }
-constexpr bool two_on_a_cu(int pieces, int ks, bool few) { return ks * (16 * pieces + 5 * group_of(pieces, ks, few)) <= 56; }
+// Whether the registers let a CU hold two workgroups, which hide each other's
+// beginnings and meetings (`down` of 128 experts x 4096 x 1536: 105 us so, 112
+// with one of twice the loads in flight), and the row tiles that a wave adds
+// up at a time: as many loads in flight as the registers hold.
+constexpr bool two_on_a_cu(int pieces, int ks, bool few) { return ks <= 2 && pieces * ks <= (few ? 2 : 4); }
+constexpr int group_of(int pieces, int ks, bool few) {
+    return few ? 2 : two_on_a_cu(pieces, ks, few) ? (ks == 1 && pieces <= 2 ? 4 : 2) : pieces == 1 ? 4 : 2;
+}
 constexpr int act_pieces(int type) { return type == SGEMM_TYPE_F32 ? 3 : 2; }
 
 // Scratch memory, every part 256-byte aligned.
