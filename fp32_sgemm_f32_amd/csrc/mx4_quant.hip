@@ -18,7 +18,7 @@
 namespace sgemm {
 namespace {
 
-constexpr int kDequantRows = 8;   // rows of a workgroup of the way back
+constexpr int kDequantLanes = 512;   // of a workgroup of the way back
 
 // Eight values rounded to a 16-bit type.
 template <int TYPE>
@@ -76,12 +76,13 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t s) {
 
 // Along the rows.  A lane holds 8 adjacent values, four lanes a block, a wave
 // 2 rows x 256 columns (full lines both ways), a workgroup 8 rows x 256
-// columns.  Rows up to the padding's end get zero scales.
+// columns, and workgroups go along a row first (8191 x 16388 floats: 109 us,
+// down the rows first 126).  Rows up to the padding's end get zero scales.
 template <int TYPE>
 __global__ __launch_bounds__(256) void quant_rows_kernel(MxQuantJob j) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t r = (int64_t)blockIdx.x * 8 + wave * 2 + (lane >> 5);
-    const int c = blockIdx.y * 256 + (lane & 31) * 8;
+    const int64_t r = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 8 + wave * 2 + (lane >> 5);
+    const int c = blockIdx.x * 256 + (lane & 31) * 8;
     const int slab = c / kMxSlab, slabs = mx_slabs(j.cols);
     float v[8];
     const bool real = r < j.rows;
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(MxQuantJob j) {
     uint32_t word = s << (8 * ((lane >> 2) & 3));
     word |= __shfl_xor(word, 4, 64);
     word |= __shfl_xor(word, 8, 64);
-    if (slab >= slabs) return;
+    if (slab >= slabs || r >= mx_plane_rows(j.rows)) return;
     if (real) ((uint32_t *)j.codes)[r * (16 * (int64_t)slabs) + c / 8] = code;
     if ((lane & 15) == 0) ((uint32_t *)j.scales)[slab * mx_plane_rows(j.rows) + r] = word;
 }
@@ -169,53 +170,36 @@ __global__ __launch_bounds__(512) void quant_tile_kernel(MxQuantJob j0, MxQuantJ
     if (b == 0 && c0 + c < mx_plane_rows(j.cols)) ((uint32_t *)j.scales_t)[by * mx_plane_rows(j.cols) + c0 + c] = word;
 }
 
-// Back to floats.  A lane writes 16 bytes of a row, so that every store of a
-// wave is one run of 1 KiB (two stores 16 bytes apart in turn: 203 us for 8191
-// x 16388 floats, now 142); workgroups go along a row first.  Rows that do not
-// start on 16-byte boundaries are stored past the caches: 16388 x 8191 floats
-// 138 us against 162, but aligned ones 148 against 142.
-template <int TYPE, bool ALIGNED>
-__global__ __launch_bounds__(256) void dequant_kernel(MxDequantJob j) {
+// Back to floats.  A workgroup takes one run of a row, a lane 16 bytes of it,
+// stored past the caches.  Workgroups side by side run on different XCDs, and
+// a line that two of them write part of costs memory a read: the fewer, longer
+// runs, the better (8191 x 16388 and 16388 x 8191 floats: 104 and 89 us, with
+// runs of 1 KiB over 8 rows 143 and 139; a fill of as many bytes takes 81).
+template <int TYPE>
+__global__ __launch_bounds__(kDequantLanes) void dequant_kernel(MxDequantJob j) {
     typedef typename MxType<TYPE>::T T;
-    constexpr int V = 16 / sizeof(T), N = kDequantRows / 4;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = (blockIdx.x * 64 + lane) * V;
-    if (c >= j.cols) return;
-    const int64_t rowb = (int64_t)mx_slabs(j.cols) * kMxSlabBytes, r0 = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * kDequantRows + wave;
-    const uint8_t *codes = j.codes + c / 2, *scales = j.scales + (c / kMxSlab) * mx_plane_rows(j.rows) * 4 + (c >> 5 & 3);
-    const auto put = [](auto *p, auto x) {
-        if constexpr (ALIGNED) *p = x;
-        else __builtin_nontemporal_store(x, p);
-    };
-    uint32_t code[N], scale[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int64_t r = r0 + 4 * i < j.rows ? r0 + 4 * i : j.rows - 1;
-        if constexpr (V == 4) code[i] = *(const uint16_t *)(codes + r * rowb);
-        else code[i] = *(const uint32_t *)(codes + r * rowb);
-        scale[i] = scales[4 * r];
+    constexpr int V = 16 / sizeof(T);
+    const int c = (blockIdx.x * kDequantLanes + threadIdx.x) * V;
+    const int64_t r = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+    if (c >= j.cols || r >= j.rows) return;
+    const uint8_t *codes = j.codes + r * ((int64_t)mx_slabs(j.cols) * kMxSlabBytes) + c / 2;
+    const uint32_t code = V == 4 ? *(const uint16_t *)codes : *(const uint32_t *)codes;
+    const uint32_t s = j.scales[((c / kMxSlab) * mx_plane_rows(j.rows) + r) * 4 + (c >> 5 & 3)];
+    const float f = __uint_as_float(s << 23);   // 0: 2^-127; 255: NaN
+    const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, f, 0), v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, f, 1);
+    float v[8] = {v0[0], v0[1], v1[0], v1[1]};
+    if constexpr (V == 8) {
+        const auto v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, f, 2), v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, f, 3);
+        v[4] = v2[0], v[5] = v2[1], v[6] = v3[0], v[7] = v3[1];
     }
+    T *y = (T *)j.y + r * j.ldy + c;
+    if (c + V <= j.cols) {
+        if constexpr (V == 4) __builtin_nontemporal_store(f32v4_any{v[0], v[1], v[2], v[3]}, (f32v4_any *)y);
+        else __builtin_nontemporal_store(pack8<TYPE>(v), (u32v4_any *)y);
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int64_t r = r0 + 4 * i;
-        if (r >= j.rows) return;
-        const float f = __uint_as_float(scale[i] << 23);   // 0: 2^-127; 255: NaN
-        float v[8];
-        const auto v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[i], f, 0), v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[i], f, 1);
-        v[0] = v0[0], v[1] = v0[1], v[2] = v1[0], v[3] = v1[1];
-        if constexpr (V == 8) {
-            const auto v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[i], f, 2), v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[i], f, 3);
-            v[4] = v2[0], v[5] = v2[1], v[6] = v3[0], v[7] = v3[1];
-        }
-        T *y = (T *)j.y + r * j.ldy + c;
-        if (c + V <= j.cols) {
-            if constexpr (V == 4) put((f32v4_any *)y, f32v4_any{v[0], v[1], v[2], v[3]});
-            else put((u32v4_any *)y, pack8<TYPE>(v));
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                if (c + k < j.cols) y[k] = MxType<TYPE>::from(v[k]);
-        }
+        for (int k = 0; k < V; ++k)
+            if (c + k < j.cols) y[k] = MxType<TYPE>::from(v[k]);
     }
 }
 
@@ -224,9 +208,9 @@ hipError_t launch_quant(const MxQuantJob &job, const MxQuantJob *second, hipStre
     MxQuantJob j = job, k = second ? *second : job;
     if (!j.codes_t) {
         void *params[] = {&j};
+        const unsigned groups = (unsigned)(mx_plane_rows(j.rows) / 8), y = groups < 32768 ? groups : 32768;
         return hipLaunchKernel((const void *)quant_rows_kernel<TYPE>,
-                               dim3((unsigned)(mx_plane_rows(j.rows) / 8), (unsigned)((j.cols + 255) / 256)), dim3(256),
-                               params, 0, s);
+                               dim3((unsigned)((j.cols + 255) / 256), y, (groups + y - 1) / y), dim3(256), params, 0, s);
     }
     int64_t tiles = (int64_t)mx_slabs(j.cols) * mx_slabs(j.rows);
     const int64_t more = second ? (int64_t)mx_slabs(k.cols) * mx_slabs(k.rows) : 0;
@@ -239,11 +223,10 @@ template <int TYPE>
 hipError_t launch_dequant(const MxDequantJob &job, hipStream_t s) {
     MxDequantJob j = job;
     void *params[] = {&j};
-    constexpr int kBytes = sizeof(typename MxType<TYPE>::T), kCols = 64 * 16 / kBytes;
-    const unsigned groups = (unsigned)((j.rows + kDequantRows - 1) / kDequantRows), y = groups < 32768 ? groups : 32768;
-    const bool aligned = ((uintptr_t)j.y & 15) == 0 && (j.ldy * kBytes & 15) == 0;
-    return hipLaunchKernel(aligned ? (const void *)dequant_kernel<TYPE, true> : (const void *)dequant_kernel<TYPE, false>,
-                           dim3((unsigned)((j.cols + kCols - 1) / kCols), y, (groups + y - 1) / y), dim3(256), params, 0, s);
+    constexpr int kCols = kDequantLanes * 16 / sizeof(typename MxType<TYPE>::T);
+    const unsigned y = j.rows < 32768 ? j.rows : 32768;
+    return hipLaunchKernel((const void *)dequant_kernel<TYPE>,
+                           dim3((unsigned)((j.cols + kCols - 1) / kCols), y, (j.rows + y - 1) / y), dim3(kDequantLanes), params, 0, s);
 }
 
 }  // namespace
