@@ -664,3 +664,20 @@ def test_offsets_past_32_bits(dev):
     # Values of 4 bits under their own scales survive the way back, blocks of largest code below 4 under other scales.
     again = sg.mx4_quantize(y)
     assert torch.equal(sg.mx4_dequantize(again, dtype=torch.bfloat16)[pick.to(dev)], y[pick.to(dev)])
+
+
+def test_example(dev):
+    """The example's parts: training lowers the loss, serving is as far off as 4 bits make it, graph and eager agree."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "four_bit_block.py")
+    spec = importlib.util.spec_from_file_location("four_bit_block", path)
+    block = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(block)
+    W, first, last = block.train(60, dev)
+    assert last < 0.2 * first
+    # Rounding to levels a sixth to a half apart: an error of at most a quarter of each weight, far less on average.
+    assert 0.0 < block.serve(W, 4, dev) < 0.25
+    eager, replayed = block.decode(3, dev)
+    assert torch.equal(eager, replayed) and bool(torch.isfinite(eager).all())
