@@ -24,6 +24,8 @@
 //   down_few  a workgroup takes 16 rows of the output and all choices: its
 //             waves share the (choice, slab) list evenly and add p_e times
 //             their part into sums of their own, added in wave order
+// (2 tokens, 8 of 64 experts of 2048 x 768: 28.8 us so, 32.6 by the five below;
+// 4 tokens 45 against 36.)
 // More: five.
 //   logits, choose
 //   up        a workgroup takes an expert and a run of inner columns, for all
@@ -193,16 +195,29 @@ __global__ __launch_bounds__(kThinThreads) void choose_kernel(MxMoeJob j, Scratc
     write_choice(j, s, blockIdx.x, l, c);
 }
 
-// The choices of expert e, in any order (a token's result does not depend on
-// its place); returns their number.
-__device__ __forceinline__ int list_tokens(const int *chosen, int all, int e, int *list, int *count) {
-    if (threadIdx.x == 0) *count = 0;
+// The expert of a workgroup and its choices, in any order (a token's result
+// does not depend on its place).  blockIdx.y is the expert, or, with fewer
+// choices than experts, a choice, which stands for its expert if none before
+// it does (4 tokens, 8 of 64 experts of 2048 x 768: 35.1 us, 35.9 with a row of
+// workgroups for every expert).
+struct Listed {
+    int list[SGEMM_MX4_MAX_TOKENS], count, earlier;
+};
+__device__ __forceinline__ int list_tokens(const MxMoeJob &j, const int *chosen, int &e, Listed &l) {
+    const int all = j.tokens * j.top;
+    const bool by_choice = all < j.experts;
+    e = by_choice ? chosen[blockIdx.y] : (int)blockIdx.y;
+    if (threadIdx.x == 0) l.count = 0, l.earlier = 0;
     __syncthreads();
     for (int a = threadIdx.x; a < all; a += kThinThreads)
-        if (chosen[a] == e) list[atomicAdd(count, 1)] = a;
+        if (chosen[a] == e) {
+            l.list[atomicAdd(&l.count, 1)] = a;
+            if (by_choice && a < (int)blockIdx.y) l.earlier = 1;
+        }
     __syncthreads();
-    return *count;
+    return l.earlier ? 0 : l.count;
 }
+int expert_rows(const MxMoeJob &j) { return j.tokens * j.top < j.experts ? j.tokens * j.top : j.experts; }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
@@ -216,8 +231,7 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, FEW)
     const int all = j.tokens * j.top;
     // red, then the sums kept from one piece of K to the next.
     extern __shared__ __attribute__((aligned(16))) f32v4 red[];
-    __shared__ int list[SGEMM_MX4_MAX_TOKENS], count;
-    __shared__ std::conditional_t<FEW, Choice, int> choice;
+    __shared__ std::conditional_t<FEW, Choice, Listed> choice;
     const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK, l16 = lane & 15;
     MxTokens<TYPE, mx_pieces(TYPE), KS, WK, 1> x;
     MxStream<2, G, KS, WK, true> stream;
@@ -236,12 +250,13 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, FEW)
         rank_experts(j, s.logits + (int64_t)t * j.experts, choice);
         e = choice.expert[blockIdx.y % j.top];
     } else {
-        n = list_tokens(s.chosen, all, e, list, &count);
+        n = list_tokens(j, s.chosen, e, choice);
     }
     for (int i0 = 0; i0 < n; i0 += 16) {
         const T *row[1] = {nullptr};
         if (i0 + l16 < n) {
-            const int a = FEW ? (int)blockIdx.y : list[i0 + l16];
+            int a = blockIdx.y;
+            if constexpr (!FEW) a = choice.list[i0 + l16];
             row[0] = (const T *)j.x + (int64_t)(a / j.top) * j.ldx;
         }
         for (int s0 = 0; s0 < w.slabs; s0 += WK * KS) {
@@ -251,13 +266,15 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, FEW)
                        [&](int tile, int, int l, const f32v4(&v)[2]) {
                                 const int i = i0 + (l & 15), f = (tile >> 1) * 16 + 4 * (l >> 4);
                                 if (i >= n) return;
+                                int a = blockIdx.y;
+                                if constexpr (!FEW) a = choice.list[i];
                                 uint16_t p[4][PA];
 #pragma unroll
                                 for (int c = 0; c < 4; ++c)
                                     mx_split<PA>(f + c < j.inner ? silu(v[0][c]) * v[1][c] : 0.0f, p[c]);
 #pragma unroll
                                 for (int k = 0; k < PA; ++k)
-                                    *(uint2 *)(s.act + ((int64_t)k * all + (FEW ? (int)blockIdx.y : list[i])) * s.ld_act + f) =
+                                    *(uint2 *)(s.act + ((int64_t)k * all + a) * s.ld_act + f) =
                                         uint2{(uint32_t)p[0][k] | (uint32_t)p[1][k] << 16,
                                               (uint32_t)p[2][k] | (uint32_t)p[3][k] << 16};
                             });
@@ -277,15 +294,17 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(P, KS, false) ? 4 : 2) vo
                                                                                              int per) {
     constexpr int G = group_of(P, KS, false);
     extern __shared__ __attribute__((aligned(16))) f32v4 red[];
-    __shared__ int list[SGEMM_MX4_MAX_TOKENS], count;
-    const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK, l16 = lane & 15, e = blockIdx.y;
+    __shared__ Listed choice;
+    const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK, l16 = lane & 15;
+    int e;
+    const int n = list_tokens(j, s.chosen, e, choice);
+    const int *list = choice.list;
     const int tiles = (j.hidden + 15) / 16, first = blockIdx.x * per, end = first + per < tiles ? first + per : tiles;
     const auto row_of = [&](int tile, int m) -> int64_t {
         const int h = tile * 16 + m;
         return (int64_t)e * j.hidden + (h < j.hidden ? h : j.hidden - 1);
     };
     MxStream<1, G, KS, WK, true> stream;
-    const int n = list_tokens(s.chosen, j.tokens * j.top, e, list, &count);
     for (int i0 = 0; i0 < n; i0 += 16) {
         const uint16_t *row = i0 + l16 < n ? s.act + (int64_t)list[i0 + l16] * s.ld_act : nullptr;
         for (int s0 = 0; s0 < w.slabs; s0 += WK * KS) {
@@ -406,7 +425,7 @@ hipError_t launch_up(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     const hipError_t e = allow_lds((const void *)up_kernel<TYPE, KS, WK, FEW>, bytes);
     if (e != hipSuccess) return e;
     return hipLaunchKernel((const void *)up_kernel<TYPE, KS, WK, FEW>,
-                           dim3((unsigned)((tiles + per - 1) / per), (unsigned)(FEW ? all : j.experts)), dim3(kThinThreads), params,
+                           dim3((unsigned)((tiles + per - 1) / per), (unsigned)(FEW ? all : expert_rows(j))), dim3(kThinThreads), params,
                            bytes, stream);
 }
 
@@ -439,7 +458,7 @@ hipError_t launch_down(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     void *params[] = {&j, &s, &w, &per};
     const hipError_t e = allow_lds((const void *)down_kernel<P, KS, WK>, bytes);
     if (e != hipSuccess) return e;
-    return hipLaunchKernel((const void *)down_kernel<P, KS, WK>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)j.experts),
+    return hipLaunchKernel((const void *)down_kernel<P, KS, WK>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)expert_rows(j)),
                            dim3(kThinThreads), params, bytes, stream);
 }
 

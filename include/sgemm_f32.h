@@ -455,8 +455,8 @@ int sgemm_f32_mx4_train_scratch(int M, int N, int K, long long *forward_bytes,
  * Y = X * W^T for float rows X (M x K) and 4-bit weights W (N x K), Y (M x N)
  * in X's type: the product of one token or a few with a layer whose weights
  * alone are in 4 bits.  X is not rounded: every product is exact, the sums
- * are in fp32.  (Of fp32 values, what lies below 2^-133 is cut where a larger
- * one than 2^-60 stands within the same thousand columns of the row.)  W is
+ * are in fp32.  (Of an fp32 value, what lies below 2^-133 is cut where a value
+ * above 2^-60 stands within the same 256 columns of its row.)  W is
  * read once for up to 64 rows of X (32 in fp32); longer X run 64 rows at a
  * time (sgemm_f32_mx4_gemm, on quantised X, is the call for those).  scratch:
  * device memory of at least the bytes that sgemm_f32_mx4_linear_scratch
@@ -484,7 +484,8 @@ int sgemm_f32_mx4_linear_scratch(int M, int N, int K, int type, long long *bytes
  * 4-bit matrix of experts * 2 * inner rows and hidden columns: expert after
  * expert, first the inner rows of G_e, then those of U_e.  `down`: experts *
  * hidden rows, inner columns.  The choice is made on sums in 64 bits.  The
- * inner activations are held to 24 bits for fp32, to 16 for 16-bit types.
+ * inner activations are held to 24 bits for fp32, to 16 for 16-bit types (and
+ * to multiples of 2^-133).
  * tokens <= 64, 1 <= top <= min(experts, 16), experts <= 1024; hidden and
  * inner at least 1.  scratch: device memory of at least the bytes that
  * sgemm_f32_mx4_moe_scratch gives, 256-byte aligned, overlapping nothing;
