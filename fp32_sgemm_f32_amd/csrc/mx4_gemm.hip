@@ -414,8 +414,6 @@ hipError_t launch_tile(const MxGemmJob &j, hipStream_t s) {
     Args g = arguments<TL>(j);
     const void *k = (const void *)mx4_gemm_kernel<TL, TYPE>;
     const int bytes = TL::S * TL::STAGE;
-    hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return e;
     void *params[] = {&g};
     return hipLaunchKernel(k, dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(TL::NT), params, bytes, s);
 }
@@ -425,8 +423,6 @@ hipError_t launch_two(const MxGemmJob &first, const MxGemmJob &second, hipStream
     Args g = arguments<TL>(first), h = arguments<TL>(second);
     const void *k = (const void *)mx4_gemm_two_kernel<TL, TYPE>;
     const int bytes = TL::S * TL::STAGE;
-    hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != hipSuccess) return e;
     int tiles0 = g.tiles_m * g.tiles_n;
     void *params[] = {&g, &h, &tiles0};
     return hipLaunchKernel(k, dim3((unsigned)(tiles0 + h.tiles_m * h.tiles_n)), dim3(TL::NT), params, bytes, s);
@@ -437,11 +433,15 @@ int64_t tiles_of(const MxGemmJob &j, int b) { return (((int64_t)j.M + b - 1) / b
 template <int TYPE>
 hipError_t launch_type(const MxGemmJob &j, int num_cus, hipStream_t s) {
     const auto tiles = [&](int b) { return tiles_of(j, b); };
-    // The largest tile that gives every CU one.  A row of an even number of
-    // slabs is whole 128-byte lines, which chunks of two slabs read at once
-    // (16384^3: 1957 us, in chunks of one 2109); rows of an odd number split
-    // every line between two such chunks (16000^3: 2042 against 1974).
-    if (tiles(256) >= num_cus)
+    // The largest tile that gives every CU one and whose rounds leave at most
+    // a fifth of the CUs' time unused (272 tiles of 256 x 256, 4352 x 4096 x
+    // 4096: 70 us, 60 in tiles of 128 x 128, two to a CU; 448 in two rounds,
+    // 7000 x 4096 x 4096: 76 against 82).  A row of an even number of slabs is
+    // whole 128-byte lines, which chunks of two slabs read at once (16384^3:
+    // 1957 us, in chunks of one 2109); rows of an odd number split every line
+    // between two such chunks (16000^3: 2042 against 1974).
+    const int64_t rounds = (tiles(256) + num_cus - 1) / num_cus;
+    if (tiles(256) >= num_cus && 4 * rounds * num_cus <= 5 * tiles(256))
         return mx_slabs(j.K) % 2 == 0 ? launch_tile<T256, TYPE>(j, s) : launch_tile<T256Odd, TYPE>(j, s);
     if (tiles(128) >= num_cus) return launch_tile<T128, TYPE>(j, s);
     // With one tile for a CU at most, a deep ring hides the memory's latency

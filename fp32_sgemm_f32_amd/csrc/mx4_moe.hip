@@ -407,11 +407,6 @@ int groups_of(int tiles, int unit, int slots, int fill, int most) {
 // comes in several pieces (their sums stay in LDS).
 constexpr int kCarryTiles = 32;
 
-// More than 64 KiB of LDS has to be asked for.
-hipError_t allow_lds(const void *kernel, int bytes) {
-    return bytes > 48 * 1024 ? hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) : hipSuccess;
-}
-
 template <int TYPE, int KS, int WK, bool FEW>
 hipError_t launch_up(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     constexpr int G = group_of(mx_pieces(TYPE), KS, FEW);
@@ -422,8 +417,6 @@ hipError_t launch_up(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     int per = mx_share(tiles, groups_of(tiles, 2, slots, fill, pieces ? kCarryTiles : tiles), 2);
     const int bytes = (kThinSums<G, 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
     void *params[] = {&j, &s, &w, &per};
-    const hipError_t e = allow_lds((const void *)up_kernel<TYPE, KS, WK, FEW>, bytes);
-    if (e != hipSuccess) return e;
     return hipLaunchKernel((const void *)up_kernel<TYPE, KS, WK, FEW>,
                            dim3((unsigned)((tiles + per - 1) / per), (unsigned)(FEW ? all : expert_rows(j))), dim3(kThinThreads), params,
                            bytes, stream);
@@ -456,8 +449,6 @@ hipError_t launch_down(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     int per = mx_share(tiles, groups_of(tiles, 1, slots, 512, pieces ? kCarryTiles : tiles), 1);
     const int bytes = (kThinSums<group_of(P, KS, false), 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
     void *params[] = {&j, &s, &w, &per};
-    const hipError_t e = allow_lds((const void *)down_kernel<P, KS, WK>, bytes);
-    if (e != hipSuccess) return e;
     return hipLaunchKernel((const void *)down_kernel<P, KS, WK>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)expert_rows(j)),
                            dim3(kThinThreads), params, bytes, stream);
 }

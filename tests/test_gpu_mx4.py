@@ -202,7 +202,7 @@ def test_dequantize_every_code_and_scale(dev, dtype):
 # ---- the product ------------------------------------------------------------------------------------------------
 
 GEMMS = [(1, 1, 1), (1, 17, 32), (33, 1, 31), (31, 65, 127), (64, 64, 128), (65, 63, 129), (100, 300, 257), (257, 255, 640),
-         (130, 520, 1000), (1111, 500, 333), (1, 2000, 4096), (3000, 5, 100), (2100, 2050, 384), (4097, 4200, 65)]
+         (130, 520, 1000), (1111, 500, 333), (1, 2000, 4096), (3000, 5, 100), (2100, 2050, 384), (4097, 4200, 65), (4200, 4097, 130), (4096, 4096, 128)]
 
 
 @typed
@@ -508,6 +508,7 @@ def test_moe_nan_token_stays_alone(dev, t):
     rng = np.random.default_rng(19)
     x, router, up, down = moe_case(rng, t, 8, 128, 64, torch.bfloat16, dev)
     clean = sg.mx4_moe(x, router, up, down, 2)
+    assert sg.mx4_moe(x[:0], router, up, down, 2).shape == (0, 128)
     x[1, 5] = float("nan")
     got = sg.mx4_moe(x, router, up, down, 2)
     assert bool(got[1].isnan().all())
