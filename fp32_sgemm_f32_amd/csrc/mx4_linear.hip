@@ -18,6 +18,10 @@ constexpr bool two_on_a_cu(int pieces, int ks, int mt) { return pieces == 1 ? mt
 // Row tiles that a wave adds up at a time.
 constexpr int group_of(int ks, int mt) { return mt > 1 ? 2 : ks == 4 ? 1 : 4; }
 
+// Pieces by what they take of the registers while they are made: folded ones
+// count as one, but an fp32 token is held whole first.
+constexpr int register_pieces(int type, bool fold) { return fold && type != SGEMM_TYPE_F32 ? 1 : mx_pieces(type); }
+
 struct Args {
     const void *x;
     int64_t ldx;
@@ -29,8 +33,8 @@ struct Args {
     int64_t pitch;
 };
 
-template <int TYPE, int KS, int MT, int G>
-__global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, MT) ? 4 : 2) void linear_kernel(Args a) {
+template <int TYPE, int KS, int MT, int G, bool FOLD>
+__global__ __launch_bounds__(kThinThreads, two_on_a_cu(register_pieces(TYPE, FOLD), KS, MT) ? 4 : 2) void linear_kernel(Args a) {
     typedef typename MxType<TYPE>::T T;
     __shared__ __attribute__((aligned(16))) f32v4 red[kThinSums<G, MT>];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -41,13 +45,13 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, MT) 
         const int n = tile * 16 + m;
         return n < a.N ? n : a.N - 1;   // rows past N: computed, not stored
     };
+    MxTokens<TYPE, mx_pieces(TYPE), KS, kThinWaves, MT, FOLD> x;
     const T *row[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        const int t = m0 + mt * 16 + (lane & 15);
-        row[mt] = t < a.M ? (const T *)a.x + t * a.ldx : nullptr;
+        const int t = m0 + mt * 16 + x.token();
+        row[mt] = x.token() >= 0 && t < a.M ? (const T *)a.x + t * a.ldx : nullptr;
     }
-    MxTokens<TYPE, mx_pieces(TYPE), KS, kThinWaves, MT> x;
     x.load(row, slab0, a.K, lane >> 4);
     MxStream<1, G, KS, kThinWaves, false> stream;
     stream.begin(a.w, slab0, first, end, row_of);
@@ -78,38 +82,37 @@ __global__ __launch_bounds__(256) void join_kernel(Args a) {
     ((typename MxType<TYPE>::T *)a.y)[t * a.ldy + n] = MxType<TYPE>::from(sum);
 }
 
-// Slabs that a wave keeps: as many as hold K, up to `most` (the registers).
-int kept_slabs(int K, int most) {
+// How a pass of up to 64 tokens runs.
+struct Shape {
+    int mt, ks, parts;   // token tiles of a workgroup, slabs of a wave, workgroups along K
+    bool fold;
+};
+Shape shape_of(int M, int K, int type) {
+    Shape s;
+    s.fold = type == SGEMM_TYPE_F16 ? M <= 8 : type == SGEMM_TYPE_F32 && M <= 5;
+    s.mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    if (type == SGEMM_TYPE_F32 && s.mt > 2) s.mt = 2;   // (four tiles would take 192 registers)
+    // As many slabs as hold K, up to what the registers hold.
+    const int most = type == SGEMM_TYPE_F32                ? (s.mt == 1 ? 2 : 1)
+                     : type == SGEMM_TYPE_BF16 || s.fold ? (s.mt == 1 ? 4 : 2)
+                                                         : (s.mt < 4 ? 2 : 1);
     const int need = (mx_slabs(K) + kThinWaves - 1) / kThinWaves;
-    return need >= most ? most : need > 2 ? 4 : need > 1 ? 2 : 1;
-}
-// That most, for 16 mt tokens.
-int most_slabs(int type, int mt) {
-    if (type == SGEMM_TYPE_BF16) return mt == 1 ? 4 : 2;
-    if (type == SGEMM_TYPE_F16) return mt < 4 ? 2 : 1;
-    return mt == 1 ? 2 : 1;
-}
-// Token tiles of a workgroup; fp32 stops at 2 (four would take 192 registers).
-int token_tiles(int M, int type) {
-    const int mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-    return type == SGEMM_TYPE_F32 && mt > 2 ? 2 : mt;
-}
-int k_parts(int M, int K, int type) {
-    const int ks = kept_slabs(K, most_slabs(type, token_tiles(M, type)));
-    const int parts = (mx_slabs(K) + kThinWaves * ks - 1) / (kThinWaves * ks);
-    return parts > 0 ? parts : 1;
+    s.ks = need >= most ? most : need > 2 ? 4 : need > 1 ? 2 : 1;
+    s.parts = (mx_slabs(K) + kThinWaves * s.ks - 1) / (kThinWaves * s.ks);
+    if (s.parts < 1) s.parts = 1;
+    return s;
 }
 
-template <int TYPE, int KS, int MT>
+template <int TYPE, int KS, int MT, bool FOLD>
 hipError_t launch_shape(Args a, hipStream_t s) {
     constexpr int G = group_of(KS, MT);
     // Workgroups: as many as the CUs hold at once.
-    constexpr int kWant = two_on_a_cu(mx_pieces(TYPE), KS, MT) ? 512 : 256;
+    constexpr int kWant = two_on_a_cu(register_pieces(TYPE, FOLD), KS, MT) ? 512 : 256;
     const int tiles = (a.N + 15) / 16, groups = kWant / a.parts > 0 ? kWant / a.parts : 1;
     a.per = mx_share(tiles, groups < tiles ? groups : tiles, 1);
     const int row_groups = (tiles + a.per - 1) / a.per;
     void *params[] = {&a};
-    hipError_t e = hipLaunchKernel((const void *)linear_kernel<TYPE, KS, MT, G>,
+    hipError_t e = hipLaunchKernel((const void *)linear_kernel<TYPE, KS, MT, G, FOLD>,
                                    dim3((unsigned)(row_groups * a.parts), (unsigned)((a.M + 16 * MT - 1) / (16 * MT))),
                                    dim3(kThinThreads), params, 0, s);
     if (e != hipSuccess || a.parts == 1) return e;
@@ -117,14 +120,14 @@ hipError_t launch_shape(Args a, hipStream_t s) {
                            0, s);
 }
 
-template <int TYPE, int MT>
-hipError_t launch_tokens(const Args &a, hipStream_t s) {
-    const int ks = kept_slabs(a.K, most_slabs(TYPE, MT));
-    if constexpr (TYPE == SGEMM_TYPE_BF16 && MT == 1)
-        if (ks == 4) return launch_shape<TYPE, 4, MT>(a, s);
-    if constexpr (!(TYPE == SGEMM_TYPE_F16 && MT == 4) && !(TYPE == SGEMM_TYPE_F32 && MT > 1))
-        if (ks == 2) return launch_shape<TYPE, 2, MT>(a, s);
-    return launch_shape<TYPE, 1, MT>(a, s);
+template <int TYPE, int MT, bool FOLD>
+hipError_t launch_tokens(const Args &a, int ks, hipStream_t s) {
+    constexpr int P = register_pieces(TYPE, FOLD);
+    if constexpr (P == 1 && MT == 1)
+        if (ks == 4) return launch_shape<TYPE, 4, MT, FOLD>(a, s);
+    if constexpr (P == 1 || (P == 2 && MT < 4) || (P == 3 && MT == 1))
+        if (ks == 2) return launch_shape<TYPE, 2, MT, FOLD>(a, s);
+    return launch_shape<TYPE, 1, MT, FOLD>(a, s);
 }
 
 template <int TYPE>
@@ -140,15 +143,20 @@ hipError_t launch_type(const MxLinearJob &j, hipStream_t s) {
         a.K = j.K;
         a.y = (char *)j.y + m * j.ldy * esize;
         a.ldy = j.ldy;
-        a.parts = k_parts(a.M, a.K, TYPE);
+        const Shape shape = shape_of(a.M, a.K, TYPE);
+        a.parts = shape.parts;
         a.partial = j.scratch;
         a.pitch = ((int64_t)j.N + 15) / 16 * 16;
-        const int mt = token_tiles(a.M, TYPE);
-        hipError_t e;
-        if (mt == 1) e = launch_tokens<TYPE, 1>(a, s);
-        else if (mt == 2) e = launch_tokens<TYPE, 2>(a, s);
-        else if constexpr (TYPE != SGEMM_TYPE_F32) e = launch_tokens<TYPE, 4>(a, s);
-        else e = hipErrorInvalidValue;
+        hipError_t e = hipErrorInvalidValue;
+        if (shape.fold) {
+            if constexpr (TYPE != SGEMM_TYPE_BF16) e = launch_tokens<TYPE, 1, true>(a, shape.ks, s);
+        } else if (shape.mt == 1) {
+            e = launch_tokens<TYPE, 1, false>(a, shape.ks, s);
+        } else if (shape.mt == 2) {
+            e = launch_tokens<TYPE, 2, false>(a, shape.ks, s);
+        } else {
+            if constexpr (TYPE != SGEMM_TYPE_F32) e = launch_tokens<TYPE, 4, false>(a, shape.ks, s);
+        }
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -162,7 +170,7 @@ int64_t mx4_linear_scratch(int M, int N, int K, int type) {
     const int sizes[] = {M < kMostTokens ? M : kMostTokens, M % kMostTokens};
     for (int m : sizes) {
         if (m == 0) continue;
-        const int64_t parts = k_parts(m, K, type);
+        const int64_t parts = shape_of(m, K, type).parts;
         const int64_t bytes = parts > 1 ? parts * m * (((int64_t)N + 15) / 16 * 16) * 4 : 0;
         most = bytes > most ? bytes : most;
     }

@@ -24,8 +24,8 @@
 //   down_few  a workgroup takes 16 rows of the output and all choices: its
 //             waves share the (choice, slab) list evenly and add p_e times
 //             their part into sums of their own, added in wave order
-// (2 tokens, 8 of 64 experts of 2048 x 768: 28.8 us so, 32.6 by the five below;
-// 4 tokens 45 against 36.)
+// (2 tokens, 8 of 64 experts of 2048 x 768: 25.0 us so, 32.6 by the five below;
+// 4 tokens, before folding, 45 against 36.)
 // More: five.
 //   logits, choose
 //   up        a workgroup takes an expert and a run of inner columns, for all
@@ -44,7 +44,10 @@ constexpr int kFew = 16;
 // beginnings and meetings (`down` of 128 experts x 4096 x 1536: 105 us so, 112
 // with one of twice the loads in flight), and the row tiles that a wave adds
 // up at a time: as many loads in flight as the registers hold.
-constexpr bool two_on_a_cu(int pieces, int ks, bool few) { return ks <= 2 && pieces * ks <= (few ? 2 : 4); }
+constexpr bool two_on_a_cu(int pieces, int ks, bool few) { return ks <= 2 && pieces < 3 && pieces * ks <= (few ? 2 : 4); }
+// Pieces by what they take of the registers while they are made: folded ones
+// count as one, but an fp32 token is held whole first.
+constexpr int register_pieces(int type, bool fold) { return fold && type != SGEMM_TYPE_F32 ? 1 : mx_pieces(type); }
 constexpr int group_of(int pieces, int ks, bool few) {
     return few ? 2 : two_on_a_cu(pieces, ks, few) ? (ks == 1 && pieces <= 2 ? 4 : 2) : pieces == 1 ? 4 : 2;
 }
@@ -223,17 +226,17 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
 // ---- up ----
 
-template <int TYPE, int KS, int WK, bool FEW>
-__global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, FEW) ? 4 : 2) void up_kernel(MxMoeJob j, Scratch s,
+template <int TYPE, int KS, int WK, bool FEW, bool FOLD>
+__global__ __launch_bounds__(kThinThreads, two_on_a_cu(register_pieces(TYPE, FOLD), KS, FEW) ? 4 : 2) void up_kernel(MxMoeJob j, Scratch s,
                                                                                                       MxWeights w, int per) {
     typedef typename MxType<TYPE>::T T;
-    constexpr int G = group_of(mx_pieces(TYPE), KS, FEW), PA = act_pieces(TYPE);
+    constexpr int G = group_of(register_pieces(TYPE, FOLD), KS, FEW), PA = act_pieces(TYPE);
     const int all = j.tokens * j.top;
     // red, then the sums kept from one piece of K to the next.
     extern __shared__ __attribute__((aligned(16))) f32v4 red[];
     __shared__ std::conditional_t<FEW, Choice, Listed> choice;
     const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK, l16 = lane & 15;
-    MxTokens<TYPE, mx_pieces(TYPE), KS, WK, 1> x;
+    MxTokens<TYPE, mx_pieces(TYPE), KS, WK, 1, FOLD> x;
     MxStream<2, G, KS, WK, true> stream;
     // Row tiles come in pairs: 16 rows of the gate, the same 16 of U.
     const int tiles = 2 * ((j.inner + 15) / 16), first = blockIdx.x * per, end = first + per < tiles ? first + per : tiles;
@@ -245,18 +248,18 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, FEW)
     if constexpr (FEW) {
         // blockIdx.y: a choice.  Its token is known before its expert.
         const int t = blockIdx.y / j.top;
-        const T *row[1] = {l16 == 0 ? (const T *)j.x + (int64_t)t * j.ldx : nullptr};
+        const T *row[1] = {x.token() == 0 ? (const T *)j.x + (int64_t)t * j.ldx : nullptr};
         x.load(row, kw * KS, j.hidden, lane >> 4);
         rank_experts(j, s.logits + (int64_t)t * j.experts, choice);
         e = choice.expert[blockIdx.y % j.top];
     } else {
         n = list_tokens(j, s.chosen, e, choice);
     }
-    for (int i0 = 0; i0 < n; i0 += 16) {
+    for (int i0 = 0; i0 < n; i0 += x.kTokens) {
         const T *row[1] = {nullptr};
-        if (i0 + l16 < n) {
+        if (x.token() >= 0 && i0 + x.token() < n) {
             int a = blockIdx.y;
-            if constexpr (!FEW) a = choice.list[i0 + l16];
+            if constexpr (!FEW) a = choice.list[i0 + x.token()];
             row[0] = (const T *)j.x + (int64_t)(a / j.top) * j.ldx;
         }
         for (int s0 = 0; s0 < w.slabs; s0 += WK * KS) {
@@ -289,13 +292,14 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(mx_pieces(TYPE), KS, FEW)
 
 // ---- down ----
 
-template <int P, int KS, int WK>
-__global__ __launch_bounds__(kThinThreads, two_on_a_cu(P, KS, false) ? 4 : 2) void down_kernel(MxMoeJob j, Scratch s, MxWeights w,
-                                                                                             int per) {
-    constexpr int G = group_of(P, KS, false);
+template <int P, int KS, int WK, bool FOLD>
+__global__ __launch_bounds__(kThinThreads, two_on_a_cu(FOLD ? 1 : P, KS, false) ? 4 : 2) void down_kernel(MxMoeJob j, Scratch s,
+                                                                                                       MxWeights w, int per) {
+    constexpr int G = group_of(FOLD ? 1 : P, KS, false);
+    MxTokens<SGEMM_TYPE_BF16, P, KS, WK, 1, FOLD> x;
     extern __shared__ __attribute__((aligned(16))) f32v4 red[];
     __shared__ Listed choice;
-    const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK, l16 = lane & 15;
+    const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK;
     int e;
     const int n = list_tokens(j, s.chosen, e, choice);
     const int *list = choice.list;
@@ -305,10 +309,10 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(P, KS, false) ? 4 : 2) vo
         return (int64_t)e * j.hidden + (h < j.hidden ? h : j.hidden - 1);
     };
     MxStream<1, G, KS, WK, true> stream;
-    for (int i0 = 0; i0 < n; i0 += 16) {
-        const uint16_t *row = i0 + l16 < n ? s.act + (int64_t)list[i0 + l16] * s.ld_act : nullptr;
+    for (int i0 = 0; i0 < n; i0 += x.kTokens) {
+        const int t = x.token();
+        const uint16_t *row = t >= 0 && i0 + t < n ? s.act + (int64_t)list[i0 + t] * s.ld_act : nullptr;
         for (int s0 = 0; s0 < w.slabs; s0 += WK * KS) {
-            MxTokens<SGEMM_TYPE_BF16, P, KS, WK, 1> x;
             x.load_pieces(row, (int64_t)j.tokens * j.top * s.ld_act, s0 + kw * KS, (int)s.ld_act, lane >> 4);
             stream.begin(w, s0 + kw * KS, first, end, row_of);
             stream.run(
@@ -334,7 +338,7 @@ __global__ __launch_bounds__(256) void join_kernel(MxMoeJob j, Scratch s) {
 template <int TYPE>
 __global__ __launch_bounds__(kThinThreads) void down_few_kernel(MxMoeJob j, Scratch s, MxWeights w) {
     typedef typename MxType<TYPE>::T T;
-    constexpr int P = act_pieces(TYPE), U = 4;
+    constexpr int P = act_pieces(TYPE), U = 6;
     __shared__ float ys[kThinWaves][kFew][16];   // a wave's sums: token, row
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
     const int all = j.tokens * j.top, h0 = blockIdx.x * 16;
@@ -354,33 +358,32 @@ __global__ __launch_bounds__(kThinThreads) void down_few_kernel(MxMoeJob j, Scra
         f32v4 acc{0.0f, 0.0f, 0.0f, 0.0f};
         for (int s0 = s_begin; s0 < s_end; s0 += U) {
             MxBlock b[U];
-            uint4 x[U][4][P];
+            uint4 x[U][4];
 #pragma unroll
             for (int u = 0; u < U; ++u) b[u] = s0 + u < s_end ? w.load(r, s0 + u, q) : MxBlock{uint4{0, 0, 0, 0}, 0};
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {   // one token: the operand's first column
-                        const int c = (s0 + u) * kMxSlab + 32 * q + 8 * k;
-                        x[u][k][p] = l16 == 0 && s0 + u < s_end && c < s.ld_act ? *(const uint4 *)(act + p * all * s.ld_act + c)
-                                                                                : uint4{0, 0, 0, 0};
-                    }
+                for (int k = 0; k < 4; ++k) {   // one token, folded: piece p in column p
+                    const int c = (s0 + u) * kMxSlab + 32 * q + 8 * k;
+                    x[u][k] = l16 < P && s0 + u < s_end && c < s.ld_act ? *(const uint4 *)(act + l16 * all * s.ld_act + c)
+                                                                        : uint4{0, 0, 0, 0};
+                }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint32_t c[4] = {b[u].codes.x, b[u].codes.y, b[u].codes.z, b[u].codes.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const bf16v8 m = mx_bf16x8(c[k], mx_scale(b[u], q));
-#pragma unroll
-                    for (int p = 0; p < P; ++p) acc = mx_mfma(m, x[u][k][p], acc);
-                }
+                for (int k = 0; k < 4; ++k) acc = mx_mfma(mx_bf16x8(c[k], mx_scale(b[u], q)), x[u][k], acc);
             }
         }
+        f32v4 sum = acc;
+#pragma unroll
+        for (int p = 1; p < P; ++p)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sum[k] += __shfl(acc[k], (lane & 48) + p, 64);
         if (l16 == 0) {
             f32v4 *y = (f32v4 *)&ys[wave][a / j.top][4 * q];
-            *y += weight * acc;
+            *y += weight * sum;
         }
     }
     __syncthreads();
@@ -407,63 +410,72 @@ int groups_of(int tiles, int unit, int slots, int fill, int most) {
 // comes in several pieces (their sums stay in LDS).
 constexpr int kCarryTiles = 32;
 
-template <int TYPE, int KS, int WK, bool FEW>
+template <int TYPE, int KS, int WK, bool FEW, bool FOLD>
 hipError_t launch_up(MxMoeJob &j, Scratch &s, hipStream_t stream) {
-    constexpr int G = group_of(mx_pieces(TYPE), KS, FEW);
+    constexpr int P = register_pieces(TYPE, FOLD), G = group_of(P, KS, FEW);
     MxWeights w = mx_weights(j.up, j.sup, (int64_t)2 * j.experts * j.inner, j.hidden);
-    const int tiles = 2 * ((j.inner + 15) / 16), all = j.tokens * j.top, slots = FEW ? all : all < j.experts ? all : j.experts;
+    const int tiles = 2 * ((j.inner + 15) / 16), all = j.tokens * j.top, slots = FEW ? all : expert_rows(j);
     const bool pieces = w.slabs > WK * KS;
-    const int fill = FEW && !two_on_a_cu(mx_pieces(TYPE), KS, FEW) ? 256 : 512;
+    const int fill = FEW && !two_on_a_cu(P, KS, FEW) ? 256 : 512;
     int per = mx_share(tiles, groups_of(tiles, 2, slots, fill, pieces ? kCarryTiles : tiles), 2);
     const int bytes = (kThinSums<G, 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
     void *params[] = {&j, &s, &w, &per};
-    return hipLaunchKernel((const void *)up_kernel<TYPE, KS, WK, FEW>,
-                           dim3((unsigned)((tiles + per - 1) / per), (unsigned)(FEW ? all : expert_rows(j))), dim3(kThinThreads), params,
-                           bytes, stream);
+    return hipLaunchKernel((const void *)up_kernel<TYPE, KS, WK, FEW, FOLD>,
+                           dim3((unsigned)((tiles + per - 1) / per), (unsigned)slots), dim3(kThinThreads), params, bytes, stream);
 }
 
 // (slabs a wave keeps, waves along K) for a number of slabs: few idle places,
 // and no more slabs than the pieces leave registers for.
-template <int TYPE, bool FEW>
+template <int TYPE, bool FEW, bool FOLD>
 hipError_t launch_up_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
+    constexpr int P = register_pieces(TYPE, FOLD);
     const int n = mx_slabs(j.hidden);
     if constexpr (!FEW) {   // (few choices: latency counts, all waves along K)
-        if (n <= 2) return launch_up<TYPE, 1, 2, FEW>(j, s, stream);
-        if (n <= 4) return launch_up<TYPE, 1, 4, FEW>(j, s, stream);
-        if (n <= 8) return launch_up<TYPE, 2, 4, FEW>(j, s, stream);
-        if constexpr (TYPE == SGEMM_TYPE_BF16) {
-            if (n <= 12) return launch_up<TYPE, 3, 4, FEW>(j, s, stream);
-            if (n > 16 && n <= 24) return launch_up<TYPE, 3, 8, FEW>(j, s, stream);
+        if (n <= 2) return launch_up<TYPE, 1, 2, FEW, FOLD>(j, s, stream);
+        if (n <= 4) return launch_up<TYPE, 1, 4, FEW, FOLD>(j, s, stream);
+        if (n <= 8) return launch_up<TYPE, 2, 4, FEW, FOLD>(j, s, stream);
+        if constexpr (P == 1) {
+            if (n <= 12) return launch_up<TYPE, 3, 4, FEW, FOLD>(j, s, stream);
+            if (n > 16 && n <= 24) return launch_up<TYPE, 3, 8, FEW, FOLD>(j, s, stream);
         }
     }
-    if constexpr (TYPE == SGEMM_TYPE_BF16)
-        if (n > 16) return launch_up<TYPE, 4, 8, FEW>(j, s, stream);
-    return n > 8 ? launch_up<TYPE, 2, 8, FEW>(j, s, stream) : launch_up<TYPE, 1, 8, FEW>(j, s, stream);
+    if constexpr (P == 1)
+        if (n > 16) return launch_up<TYPE, 4, 8, FEW, FOLD>(j, s, stream);
+    return n > 8 ? launch_up<TYPE, 2, 8, FEW, FOLD>(j, s, stream) : launch_up<TYPE, 1, 8, FEW, FOLD>(j, s, stream);
 }
 
-template <int P, int KS, int WK>
+template <int P, int KS, int WK, bool FOLD>
 hipError_t launch_down(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     MxWeights w = mx_weights(j.down, j.sdown, (int64_t)j.experts * j.hidden, j.inner);
-    const int tiles = (j.hidden + 15) / 16, all = j.tokens * j.top, slots = all < j.experts ? all : j.experts;
+    const int tiles = (j.hidden + 15) / 16, slots = expert_rows(j);
     const bool pieces = w.slabs > WK * KS;
     int per = mx_share(tiles, groups_of(tiles, 1, slots, 512, pieces ? kCarryTiles : tiles), 1);
-    const int bytes = (kThinSums<group_of(P, KS, false), 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
+    const int bytes = (kThinSums<group_of(FOLD ? 1 : P, KS, false), 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
     void *params[] = {&j, &s, &w, &per};
-    return hipLaunchKernel((const void *)down_kernel<P, KS, WK>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)expert_rows(j)),
+    return hipLaunchKernel((const void *)down_kernel<P, KS, WK, FOLD>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)slots),
                            dim3(kThinThreads), params, bytes, stream);
 }
 
-template <int P>
+template <int P, bool FOLD>
 hipError_t launch_down_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     const int n = mx_slabs(j.inner);
-    if (n <= 1) return launch_down<P, 1, 1>(j, s, stream);
-    if (n <= 2) return launch_down<P, 1, 2>(j, s, stream);
-    if (n <= 4) return launch_down<P, 2, 2>(j, s, stream);
-    if (n <= 6) return launch_down<P, 3, 2>(j, s, stream);
-    if (n <= 8) return launch_down<P, 2, 4>(j, s, stream);
-    if (n <= 16) return launch_down<P, 2, 8>(j, s, stream);
-    return launch_down<P, 3, 8>(j, s, stream);
+    if (n <= 1) return launch_down<P, 1, 1, FOLD>(j, s, stream);
+    if (n <= 2) return launch_down<P, 1, 2, FOLD>(j, s, stream);
+    if (n <= 4) return launch_down<P, 2, 2, FOLD>(j, s, stream);
+    if (n <= 6) return launch_down<P, 3, 2, FOLD>(j, s, stream);
+    if (n <= 8) return launch_down<P, 2, 4, FOLD>(j, s, stream);
+    if constexpr (FOLD) {
+        if (n > 8 && n <= 16) return launch_down<P, 4, 4, FOLD>(j, s, stream);
+        if (n > 24) return launch_down<P, 4, 8, FOLD>(j, s, stream);
+    }
+    if (n <= 16) return launch_down<P, 2, 8, FOLD>(j, s, stream);
+    return launch_down<P, 3, 8, FOLD>(j, s, stream);
 }
+
+// Whether an expert's tokens always fit a folded tile.  (Where only most do, the
+// few workgroups that stream their weights twice are what the kernel waits for:
+// 48 tokens, 8 of 128 experts, 4096 x 1536: 124 us, unfolded 104.)
+bool folds(const MxMoeJob &j, int pieces) { return j.tokens <= 16 / pieces; }
 
 template <int TYPE>
 hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
@@ -477,7 +489,7 @@ hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
                                                   dim3(256), params, 0, stream);
     if (e != hipSuccess) return e;
     if (j.tokens * j.top <= kFew) {
-        e = launch_up_slabs<TYPE, true>(j, s, stream);
+        e = launch_up_slabs<TYPE, true, (mx_pieces(TYPE) > 1)>(j, s, stream);
         if (e != hipSuccess) return e;
         MxWeights w = mx_weights(j.down, j.sdown, (int64_t)j.experts * j.hidden, j.inner);
         void *down[] = {&j, &s, &w};
@@ -486,9 +498,11 @@ hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
     }
     e = hipLaunchKernel((const void *)choose_kernel, dim3((unsigned)j.tokens), dim3(kThinThreads), params, 0, stream);
     if (e != hipSuccess) return e;
-    e = launch_up_slabs<TYPE, false>(j, s, stream);
+    constexpr int PX = mx_pieces(TYPE), PA = act_pieces(TYPE);
+    if (PX > 1 && folds(j, PX)) e = launch_up_slabs<TYPE, false, (PX > 1)>(j, s, stream);
+    else e = launch_up_slabs<TYPE, false, false>(j, s, stream);
     if (e != hipSuccess) return e;
-    e = launch_down_slabs<act_pieces(TYPE)>(j, s, stream);
+    e = folds(j, PA) ? launch_down_slabs<PA, true>(j, s, stream) : launch_down_slabs<PA, false>(j, s, stream);
     if (e != hipSuccess) return e;
     return hipLaunchKernel((const void *)join_kernel<TYPE>, dim3((unsigned)((j.hidden + 255) / 256), (unsigned)j.tokens), dim3(256),
                            params, 0, stream);

@@ -20,7 +20,9 @@
 // (two bits of significand; the conversion instruction applies the scale).  A
 // token value is cut into P bf16 pieces that add up to it: one for bf16, two
 // for fp16 (11 bits), three for fp32 (24 bits); each piece costs one more
-// matrix step, which the loads of the weights hide.  bf16 ends at 2^-133, so
+// matrix step and as many registers.  With at most 8 (two pieces) or 5 (three)
+// tokens they are folded: the pieces take the other columns of the same step,
+// and their sums are added with the waves'.  bf16 ends at 2^-133, so
 // where all of a wave's values of an fp32 token lie below 2^-60 they are
 // taken 2^32 times larger and the wave's sum 2^32 times smaller: both exact,
 // and far from overflow with the largest weight.
@@ -107,12 +109,35 @@ __device__ __forceinline__ uint4 mx_bf16_edge8(const uint16_t *row, int c, int c
 // What fp32 values whose largest magnitude has these bits are multiplied by.
 __device__ __forceinline__ float mx_lift(uint32_t largest) { return largest < 0x21800000u ? 0x1p32f : 1.0f; }
 
-// A wave's tokens: MT tiles of 16, KS slabs, P pieces; WK waves share K.
-template <int TYPE, int P, int KS, int WK, int MT>
+// A wave's tokens: MT tiles, KS slabs, P pieces; WK waves share K.  FOLD: the
+// pieces of a token stand in different columns.
+template <int TYPE, int P, int KS, int WK, int MT, bool FOLD = false>
 struct MxTokens {
     typedef typename MxType<TYPE>::T T;
-    uint4 x[KS][MT][4][P];
+    static constexpr int Q = FOLD ? 1 : P;              // matrix steps for a product
+    static constexpr int kFold = FOLD ? P : 1, kTokens = 16 / kFold;   // columns of a token, tokens of a tile
+    uint4 x[KS][MT][4][Q];
     float back[MT];   // what sums of a token are multiplied by
+
+    // The token of the lane's column (-1: none) and the piece that stands there.
+    static __device__ __forceinline__ int token() {
+        const int c = threadIdx.x & 15;
+        return c < kFold * kTokens ? c % kTokens : -1;
+    }
+    static __device__ __forceinline__ int piece() { return (threadIdx.x & 15) / kTokens; }
+    // One operand of the pieces of eight values.
+    static __device__ __forceinline__ void take(const uint4 (&all)[P], uint4 (&to)[Q]) {
+        if constexpr (FOLD) {
+            const int p = piece();
+            to[0] = all[0];
+#pragma unroll
+            for (int k = 1; k < P; ++k)
+                if (p == k) to[0] = all[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < P; ++k) to[k] = all[k];
+        }
+    }
 
     // The lane's tokens are in row[mt] (NULL: none, zeros), its columns in
     // slabs slab0 + i.
@@ -128,6 +153,17 @@ struct MxTokens {
                         const int c = (slab0 + i) * kMxSlab + 32 * q + 8 * s;
                         x[i][mt][s][0] = row[mt] ? mx_bf16_edge8(row[mt], c, cols) : uint4{0, 0, 0, 0};
                     }
+            } else if constexpr (TYPE != SGEMM_TYPE_F32) {
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        float v[8];
+                        uint4 all[P];
+                        mx_load_edge8<TYPE>(row[mt], (slab0 + i) * kMxSlab + 32 * q + 8 * s, row[mt] ? cols : 0, v);
+                        mx_split8<P>(v, all);
+                        take(all, x[i][mt][s]);
+                    }
             } else {
                 float v[KS][4][8];
                 uint32_t m = 0;
@@ -135,44 +171,31 @@ struct MxTokens {
                 for (int i = 0; i < KS; ++i)
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
-                        const int c = (slab0 + i) * kMxSlab + 32 * q + 8 * s;
-                        mx_load_edge8<TYPE>(row[mt], c, row[mt] ? cols : 0, v[i][s]);
+                        mx_load_edge8<TYPE>(row[mt], (slab0 + i) * kMxSlab + 32 * q + 8 * s, row[mt] ? cols : 0, v[i][s]);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t b = __float_as_uint(v[i][s][k]) & 0x7fffffffu;
+                            m = m > b ? m : b;
+                        }
                     }
-                if constexpr (TYPE == SGEMM_TYPE_F32) {
+                // The token's other blocks lie with lanes l ^ 16, l ^ 32, l ^ 48.
+                uint32_t o = __shfl_xor(m, 16, 64);
+                m = m > o ? m : o;
+                o = __shfl_xor(m, 32, 64);
+                m = m > o ? m : o;
+                const float lift = mx_lift(m);
+                back[mt] = lift == 1.0f ? 1.0f : 0x1p-32f;
 #pragma unroll
-                    for (int i = 0; i < KS; ++i)
+                for (int i = 0; i < KS; ++i)
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
+                    for (int s = 0; s < 4; ++s) {
+                        uint4 all[P];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const uint32_t b = __float_as_uint(v[i][s][k]) & 0x7fffffffu;
-                                m = m > b ? m : b;
-                            }
-                    // The token's other blocks lie with lanes l ^ 16, l ^ 32, l ^ 48.
-                    uint32_t o = __shfl_xor(m, 16, 64);
-                    m = m > o ? m : o;
-                    o = __shfl_xor(m, 32, 64);
-                    m = m > o ? m : o;
-                    const float lift = mx_lift(m);
-                    back[mt] = lift == 1.0f ? 1.0f : 0x1p-32f;
-#pragma unroll
-                    for (int i = 0; i < KS; ++i)
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) v[i][s][k] *= lift;
-                }
-                if (TYPE == SGEMM_TYPE_F32 && P > 1 && m < 0x7f800000u) {
-#pragma unroll
-                    for (int i = 0; i < KS; ++i)
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) mx_split8_finite<P>(v[i][s], x[i][mt][s]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < KS; ++i)
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) mx_split8<P>(v[i][s], x[i][mt][s]);
-                }
+                        for (int k = 0; k < 8; ++k) v[i][s][k] *= lift;
+                        if (m < 0x7f800000u) mx_split8_finite<P>(v[i][s], all);
+                        else mx_split8<P>(v[i][s], all);
+                        take(all, x[i][mt][s]);
+                    }
             }
         }
     }
@@ -187,9 +210,9 @@ struct MxTokens {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
+                for (int p = 0; p < Q; ++p) {
                     const int c = (slab0 + i) * kMxSlab + 32 * q + 8 * s;
-                    x[i][0][s][p] = row && c < cols ? *(const uint4 *)(row + p * stride + c) : uint4{0, 0, 0, 0};
+                    x[i][0][s][p] = row && c < cols ? *(const uint4 *)(row + (FOLD ? piece() : p) * stride + c) : uint4{0, 0, 0, 0};
                 }
     }
 };
@@ -306,8 +329,8 @@ struct MxStream {
     // With K in several pieces, carry (LDS, (end - first) * MT * 64 sums)
     // holds them from the first piece to the last.  Every thread of the
     // workgroup calls this.
-    template <int TYPE, int P, int MT, class Row, class Emit>
-    __device__ __forceinline__ void run(const MxTokens<TYPE, P, KS, WK, MT> &x, const MxWeights &w, int slab0, int first, int end,
+    template <int TYPE, int P, int MT, bool FOLD, class Row, class Emit>
+    __device__ __forceinline__ void run(const MxTokens<TYPE, P, KS, WK, MT, FOLD> &x, const MxWeights &w, int slab0, int first, int end,
                                         f32v4 *red, f32v4 *carry, bool first_piece, bool last_piece, Row row, Emit emit) {
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4;
         for (int t0 = first; t0 < end; t0 += G * WR) {
@@ -330,7 +353,7 @@ struct MxStream {
                         const uint4 c = b[g][i].codes;
                         const bf16v8 v = mx_bf16x8(s == 0 ? c.x : s == 1 ? c.y : s == 2 ? c.z : c.w, mx_scale(b[g][i], q));
 #pragma unroll
-                        for (int p = 0; p < P; ++p)
+                        for (int p = 0; p < (FOLD ? 1 : P); ++p)
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt) acc[g][mt] = mx_mfma(v, x.x[i][mt][s][p], acc[g][mt]);
                     }
@@ -349,6 +372,7 @@ struct MxStream {
             for (int i = tid; i < G / U * WR * MT * 64; i += kThinThreads) {
                 const int l = i & 63, mt = (i >> 6) % MT, unit = (i >> 6) / MT, set = unit % WR, g = unit / WR * U;
                 if (t0 + unit * U >= end) break;
+                if (FOLD && (l & 15) >= x.kTokens) continue;
                 f32v4 v[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -356,6 +380,12 @@ struct MxStream {
                     v[u] = *from;
 #pragma unroll
                     for (int k = 1; k < WK; ++k) v[u] += from[k * G * MT * 64];
+                    if constexpr (FOLD) {
+#pragma unroll
+                        for (int f = 1; f < P; ++f)
+#pragma unroll
+                            for (int k = 0; k < WK; ++k) v[u] += from[k * G * MT * 64 + f * x.kTokens];
+                    }
                     f32v4 *kept = carry + ((t0 - first + unit * U + u) * MT + mt) * 64 + l;
                     if (!first_piece) v[u] = *kept + v[u];
                     if (!last_piece) *kept = v[u];
