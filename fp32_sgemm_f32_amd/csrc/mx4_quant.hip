@@ -12,7 +12,9 @@
 // instruction's (checked against the definition at every code border and for
 // every scale byte).
 //
-// Bound by HBM: 4 (2) bytes read and 0.53 written per value and direction.
+// Bound by HBM: 4 (2) bytes read and 0.53 written per value and direction.  8191
+// x 16388 floats: along the rows 109 us (5.6 TB/s), both ways 143 (4.7); 8192 x
+// 4096 bf16: 14.6 (5.8) and 23.7 (4.3).
 #include "mx4.h"
 
 namespace sgemm {
