@@ -14,6 +14,7 @@ PyTorch for as little as it can: one allocation for the two arrays of a result
 handle, no module looked up twice.
 """
 import ctypes
+import functools
 import operator
 
 SCALE_FLOOR = 0
@@ -245,13 +246,25 @@ class _Run:
             raise h.error(st, fn.__name__)
 
 
-def _size(fn, *args):
-    """A call that gives a number of bytes."""
+@functools.lru_cache(maxsize=1024)
+def _scratch(name, *sizes):
+    """Bytes of scratch memory of a call with these sizes (a function of them alone)."""
+    fn = getattr(_host, name)
     n = ctypes.c_longlong()
-    st = fn(*args, ctypes.byref(n))
+    st = fn(*sizes, ctypes.byref(n))
     if st != _host.ok:
         raise _host.error(st, fn.__name__)
     return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _train_scratch(M, N, K):
+    """The same of the forward and the backward call of a training step."""
+    f, b = ctypes.c_longlong(), ctypes.c_longlong()
+    st = _host.train_scratch(M, N, K, ctypes.byref(f), ctypes.byref(b))
+    if st != _host.ok:
+        raise _host.error(st, "sgemm_f32_mx4_train_scratch")
+    return f.value, b.value
 
 
 def _out(run, out, shape, dtype, name="out"):
@@ -363,12 +376,11 @@ def mx4_train_forward(X, W, rule="floor", stream=None):
     at_w = (of_x + 255) // 256 * 256
     kept = run.bytes(at_w + of_w)
     xt, wt = Mx4._of(kept, 0, K, M), Mx4._of(kept, at_w, K, N)
-    n = ctypes.c_longlong()
-    h.train_scratch(M, N, K, ctypes.byref(n), None)
-    scratch = run.bytes(n.value)
+    need = _train_scratch(M, N, K)[0]
+    scratch = run.bytes(need)
     Y = run.empty((M, N), X.dtype)
     run.call(h.train_forward, (X, W), M, N, K, tx, X.data_ptr(), ldx, tw, W.data_ptr(), ldw, code, Y.data_ptr(), N,
-             *xt._pointers(), *wt._pointers(), scratch.data_ptr(), n.value)
+             *xt._pointers(), *wt._pointers(), scratch.data_ptr(), need)
     return Y, (xt, wt, rule)
 
 
@@ -391,14 +403,13 @@ def mx4_train_backward(dY, saved, dW=None, stream=None):
         raise ValueError(f"dY {(M, N)} does not fit what the forward pass saved of {M2} x {K} and {N2} x {K2} matrices")
     h = _host
     run = _Run(device, stream)
-    n = ctypes.c_longlong()
-    h.train_scratch(M, N, K, None, ctypes.byref(n))
-    scratch = run.bytes(n.value)
+    need = _train_scratch(M, N, K)[1]
+    scratch = run.bytes(need)
     dX = run.empty((M, K), dY.dtype)
     beta = 0.0 if dW is None else 1.0
     dW, _, ldw = _out(run, dW, (N, K), h.float32, "dW")
     run.call(h.train_backward, (dY, xt, wt, dW), M, N, K, ty, dY.data_ptr(), ld, code, *xt._pointers(), *wt._pointers(),
-             dX.data_ptr(), K, beta, dW.data_ptr(), ldw, scratch.data_ptr(), n.value)
+             dX.data_ptr(), K, beta, dW.data_ptr(), ldw, scratch.data_ptr(), need)
     return dX, dW
 
 
@@ -417,7 +428,7 @@ def mx4_linear(X, W, out=None, stream=None):
     h = _host
     run = _Run(device, stream)
     out, _, ldy = _out(run, out, (M, N), X.dtype)
-    need = _size(h.linear_scratch, M, N, K, ty)
+    need = _scratch("linear_scratch", M, N, K, ty)
     scratch = run.bytes(need) if need else None
     run.call(h.linear, (X, W, out), M, N, K, ty, X.data_ptr(), ldx, *W._pointers(), out.data_ptr(), ldy,
              scratch.data_ptr() if need else None, need)
@@ -447,7 +458,7 @@ def mx4_moe(X, router, gate_up, down, top, norm=True, out=None, stream=None):
                          f"together with {H} columns of X")
     top = max(0, min(operator.index(top), _INT_MAX))    # the library says which are too few or too many
     h = _host
-    need = _size(h.moe_scratch, T, H, F, E, top, ty)
+    need = _scratch("moe_scratch", T, H, F, E, top, ty)
     run = _Run(device, stream)
     out, _, ldy = _out(run, out, (T, H), X.dtype)
     scratch = run.bytes(need)
