@@ -176,7 +176,7 @@ def _floats(t, name, device=None):
         ld, unit = t.stride()
         if unit != 1 and cols > 1:
             raise ValueError(f"{name} must be row-major (unit column stride)")
-        if rows == 1 and ld < cols:
+        if rows == 1:
             ld = cols
     if rows > _INT_MAX or ld > _INT_MAX:
         raise ValueError(f"{name} is too large")

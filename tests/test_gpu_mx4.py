@@ -321,6 +321,26 @@ def test_train(dev, dtype, m, n, k):
     close(both, host(start) + r(D.T) @ r(X.T).T, product_bound(r(D.T), r(X.T)) + 2.0 ** -22 * (np.abs(host(start)) + np.abs(host(dw))))
 
 
+@typed
+@pytest.mark.parametrize("m, n, k", [(300, 520, 700), (2100, 2050, 2060), (2048, 4096, 1000), (4096, 4100, 4090), (4096, 4096, 4100),
+                                     (250, 254, 65500)])
+def test_train_equals_its_parts(dev, dtype, m, n, k):
+    """The calls of a training step give bit for bit what quantising and multiplying one after the other gives, for all tiles
+    and for products in one launch and in two."""
+    rng = np.random.default_rng(31)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(int(rng.integers(1 << 30)))
+    x, w, dy = (torch.randn(s, generator=gen, device=dev).to(dtype) for s in ((m, k), (n, k), (m, n)))
+    y, saved = sg.mx4_train_forward(x, w)
+    start = torch.randn(n, k, generator=gen, device=dev)
+    dw = start.clone()
+    dx, _ = sg.mx4_train_backward(dy, saved, dW=dw)
+    quant = sg.mx4_quantize
+    assert torch.equal(y, sg.mx4_gemm(quant(x), quant(w), dtype=dtype))
+    assert torch.equal(dx, sg.mx4_gemm(quant(dy), quant(w.t()), dtype=dtype))
+    assert torch.equal(dw, sg.mx4_gemm(quant(dy.t()), quant(x.t()), out=start, beta=1.0))
+
+
 def test_train_of_two_types_and_of_views(dev):
     """X and W of different types, column-major, strided: the same results as of the plain copies."""
     rng = np.random.default_rng(29)
