@@ -2,15 +2,18 @@
 // the thin product and the expert layer.
 //
 // A workgroup of 8 waves owns a piece of K and streams rows of weights past
-// it; where K is short, sets of WK < 8 waves own it and share the rows.  A wave keeps its tokens' part of KS slabs (128 columns each) in operand
-// registers for as long as it lives and takes 16 rows of weights and those
-// slabs at a time: lane l loads the 16 bytes (one block, 32 codes) of row
-// l % 16 and block q = l / 16, so a wave reads 64 bytes of each row and
-// neighbouring waves the 64 bytes beside them.  On v_mfma_f32_16x16x32_bf16,
-// the weights as the first operand, step j = 0..3 takes codes 8 j .. 8 j + 7
-// of every lane; the sum's order along K does not matter as long as the
-// tokens follow it, so they are taken at column 32 q + 8 j.  The eight waves'
-// sums meet in LDS and are added in wave order, G tiles of rows at a time.
+// it; where K is short, sets of WK < 8 waves own it and share the rows.  A
+// wave keeps its tokens' part of KS adjacent slabs (128 columns each) in
+// operand registers for as long as it lives and takes 16 rows of weights and
+// those slabs at a time, on v_mfma_f32_16x16x32_bf16 with the weights as the
+// first operand: lane l holds the 16 bytes (one block, 32 codes) of row l % 16
+// and block q = l / 16 of a slab, and step j = 0..3 takes codes 8 j .. 8 j + 7
+// of every lane.  The sum's order along K does not matter as long as the
+// tokens follow it, so they are taken at column 32 q + 8 j.  Two slabs are
+// loaded as 8 rows x 128 bytes, whole lines of memory, and exchanged between
+// lanes l and l ^ 8 (`up` of 128 experts x 4096 x 1536: 160 us, by 16 rows x
+// 64 bytes 180).  The waves' sums meet in LDS and are added in wave order, G
+// tiles of rows at a time.
 //
 // (A wave that took the tokens anew for every 16 rows read four to twelve
 // bytes of them for each byte of weights and split them again each time: 13
@@ -22,10 +25,10 @@
 // for fp16 (11 bits), three for fp32 (24 bits); each piece costs one more
 // matrix step and as many registers.  With at most 8 (two pieces) or 5 (three)
 // tokens they are folded: the pieces take the other columns of the same step,
-// and their sums are added with the waves'.  bf16 ends at 2^-133, so
-// where all of a wave's values of an fp32 token lie below 2^-60 they are
-// taken 2^32 times larger and the wave's sum 2^32 times smaller: both exact,
-// and far from overflow with the largest weight.
+// and their sums are added with the waves'.  bf16 ends at 2^-133, so where all
+// of a wave's values of an fp32 token lie below 2^-60 they are taken 2^32 times
+// larger and the wave's sum 2^32 times smaller: both exact, and far from
+// overflow with the largest weight.
 #pragma once
 
 #include "mx4.h"

@@ -456,12 +456,12 @@ int sgemm_f32_mx4_train_scratch(int M, int N, int K, long long *forward_bytes,
  * in X's type: the product of one token or a few with a layer whose weights
  * alone are in 4 bits.  X is not rounded: every product is exact, the sums
  * are in fp32.  (Of an fp32 value, what lies below 2^-133 is cut where a value
- * above 2^-60 stands within the same 256 columns of its row.)  W is
- * read once for up to 64 rows of X (32 in fp32); longer X run 64 rows at a
- * time (sgemm_f32_mx4_gemm, on quantised X, is the call for those).  scratch:
- * device memory of at least the bytes that sgemm_f32_mx4_linear_scratch
- * gives (for short K none), 256-byte aligned, overlapping nothing; its
- * contents do not matter before or after.
+ * above 2^-60 stands within the same 256 columns of its row.)  W is read once
+ * for up to 64 rows of X (32 in fp32); longer X run 64 rows at a time
+ * (sgemm_f32_mx4_gemm, on quantised X, is the call for those).  scratch: device
+ * memory of at least the bytes that sgemm_f32_mx4_linear_scratch gives (for
+ * short K none), 256-byte aligned, overlapping nothing; its contents do not
+ * matter before or after.
  */
 int sgemm_f32_mx4_linear(int M, int N, int K, int type, const void *X, int ldx,
                          const void *codes, const void *scales,
@@ -485,11 +485,10 @@ int sgemm_f32_mx4_linear_scratch(int M, int N, int K, int type, long long *bytes
  * expert, first the inner rows of G_e, then those of U_e.  `down`: experts *
  * hidden rows, inner columns.  The choice is made on sums in 64 bits.  The
  * inner activations are held to 24 bits for fp32, to 16 for 16-bit types (and
- * to multiples of 2^-133).
- * tokens <= 64, 1 <= top <= min(experts, 16), experts <= 1024; hidden and
- * inner at least 1.  scratch: device memory of at least the bytes that
- * sgemm_f32_mx4_moe_scratch gives, 256-byte aligned, overlapping nothing;
- * its contents do not matter before or after.
+ * to multiples of 2^-133).  tokens <= 64, 1 <= top <= min(experts, 16),
+ * experts <= 1024; hidden and inner at least 1.  scratch: device memory of at
+ * least the bytes that sgemm_f32_mx4_moe_scratch gives, 256-byte aligned,
+ * overlapping nothing; its contents do not matter before or after.
  */
 #define SGEMM_MX4_MAX_TOKENS   64
 #define SGEMM_MX4_MAX_TOP      16
