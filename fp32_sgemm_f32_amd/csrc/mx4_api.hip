@@ -266,7 +266,7 @@ SGEMM_API int sgemm_f32_mx4_moe_scratch(int tokens, int hidden, int inner, int e
     const int status = moe_sizes(tokens, hidden, inner, experts, top, type);
     if (status != SGEMM_OK) return status;
     if (!bytes) return SGEMM_ERR_NULL;
-    *bytes = mx4_moe_scratch(tokens, hidden, inner, experts, top, type);
+    *bytes = mx4_moe_scratch(tokens, hidden, inner, experts, top);
     return SGEMM_OK;
 }
 
@@ -279,7 +279,7 @@ SGEMM_API int sgemm_f32_mx4_moe(int tokens, int hidden, int inner, int experts, 
     if (norm != 0 && norm != 1) return SGEMM_ERR_CONFIG;
     if (tokens == 0) return SGEMM_OK;
     if (ldx < hidden || ldr < hidden || ldy < hidden) return SGEMM_ERR_LD;
-    const int64_t need = mx4_moe_scratch(tokens, hidden, inner, experts, top, type);
+    const int64_t need = mx4_moe_scratch(tokens, hidden, inner, experts, top);
     const int ur = experts * 2 * inner, dr = experts * hidden;
     const Span spans[] = {floats(X, tokens, hidden, ldx, type, false), floats(router, experts, hidden, ldr, type, false),
                           codes(up, ur, hidden, false), scales(sup, ur, hidden, false),

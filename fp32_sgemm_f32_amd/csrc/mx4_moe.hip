@@ -9,14 +9,14 @@
 // `up` (2 E F x H), D_e rows [e H, e H + H) of `down` (E H x F).
 //
 // Bound by reading the chosen experts once: 3 F H 0.53 bytes each.  48 tokens, 8
-// of 128 experts of 4096 x 1536, bf16: 242 us; `up` reads 816 MB in 140 (5.8
-// TB/s), `down` 408 MB in 98 (4.2).  One token, 8 of 64 experts of 2048 x 768:
+// of 128 experts of 4096 x 1536, bf16: 265 us; `up` reads 816 MB in 140 (5.8
+// TB/s), `down` 408 MB in 115 (3.5).  One token, 8 of 64 experts of 2048 x 768:
 // 16.7 us in a graph, latencies one after another.
 //
 // Logits are summed in 64 bits: which expert is chosen must not hang on the
-// order of a sum.  The inner activations enter the second product as bf16
-// pieces: three (24 bits) for fp32 outputs, two (16 bits) for 16-bit ones,
-// whose own rounding is at least 32 times coarser.  Every sum has a fixed order:
+// order of a sum.  The inner activations enter the second product as three
+// bf16 pieces, 24 bits, whatever the type of the tokens: nothing is rounded
+// between a token and its result but fp32 sums.  Every sum has a fixed order:
 // results repeat bit for bit.
 //
 // Few choices (tokens * top <= kFew): three kernels.
@@ -44,29 +44,28 @@ namespace {
 
 constexpr int kFew = 16;
 // Whether the registers let a CU hold two workgroups, which hide each other's
-// beginnings and meetings (`down` of 128 experts x 4096 x 1536: 105 us so, 112
-// with one of twice the loads in flight), and the row tiles that a wave adds
-// up at a time: as many loads in flight as the registers hold.
-constexpr bool two_on_a_cu(int pieces, int ks, bool few) { return ks <= 2 && pieces < 3 && pieces * ks <= (few ? 2 : 4); }
+// beginnings and meetings, and the row tiles that a wave adds up at a time: as
+// many loads in flight as the registers hold.
+constexpr bool two_on_a_cu(int pieces, int ks, bool few) { return ks <= 2 && pieces * ks <= (few ? 2 : 4); }
 // Pieces by what they take of the registers while they are made: folded ones
 // count as one, but an fp32 token is held whole first.
 constexpr int register_pieces(int type, bool fold) { return fold && type != SGEMM_TYPE_F32 ? 1 : mx_pieces(type); }
 constexpr int group_of(int pieces, int ks, bool few) {
     return few ? 2 : two_on_a_cu(pieces, ks, few) ? (ks == 1 && pieces <= 2 ? 4 : 2) : pieces == 1 ? 4 : 2;
 }
-constexpr int act_pieces(int type) { return type == SGEMM_TYPE_F32 ? 3 : 2; }
+constexpr int kActPieces = 3;   // of an inner activation
 
 // Scratch memory, every part 256-byte aligned.
 struct Scratch {
     double *logits;   // tokens x experts
     int *chosen;      // tokens x top
     float *weight;    // tokens x top
-    uint16_t *act;    // pieces x (tokens * top) x ld_act (inner rounded up to 16), zeros beyond inner
+    uint16_t *act;    // kActPieces x (tokens * top) x ld_act (inner rounded up to 16), zeros beyond inner
     float *part;      // (tokens * top) x ld_part; not with few choices
     int64_t ld_act, ld_part, bytes;
 };
 
-Scratch layout(char *p, int tokens, int hidden, int inner, int experts, int top, int type) {
+Scratch layout(char *p, int tokens, int hidden, int inner, int experts, int top) {
     Scratch s;
     int64_t at = 0;
     const auto take = [&](int64_t n) { const int64_t here = at; at += (n + 255) & ~(int64_t)255; return p + here; };
@@ -76,7 +75,7 @@ Scratch layout(char *p, int tokens, int hidden, int inner, int experts, int top,
     s.logits = (double *)take((int64_t)tokens * experts * 8);
     s.chosen = (int *)take(all * 4);
     s.weight = (float *)take(all * 4);
-    s.act = (uint16_t *)take(act_pieces(type) * all * s.ld_act * 2);
+    s.act = (uint16_t *)take(kActPieces * all * s.ld_act * 2);
     s.part = (float *)take(all > kFew ? all * s.ld_part * 4 : 0);
     s.bytes = at;
     return s;
@@ -233,7 +232,7 @@ template <int TYPE, int KS, int WK, bool FEW, bool FOLD>
 __global__ __launch_bounds__(kThinThreads, two_on_a_cu(register_pieces(TYPE, FOLD), KS, FEW) ? 4 : 2) void up_kernel(MxMoeJob j, Scratch s,
                                                                                                       MxWeights w, int per) {
     typedef typename MxType<TYPE>::T T;
-    constexpr int G = group_of(register_pieces(TYPE, FOLD), KS, FEW), PA = act_pieces(TYPE);
+    constexpr int G = group_of(register_pieces(TYPE, FOLD), KS, FEW), PA = kActPieces;
     const int all = j.tokens * j.top;
     // red, then the sums kept from one piece of K to the next.
     extern __shared__ __attribute__((aligned(16))) f32v4 red[];
@@ -295,11 +294,11 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(register_pieces(TYPE, FOL
 
 // ---- down ----
 
-template <int P, int KS, int WK, bool FOLD>
-__global__ __launch_bounds__(kThinThreads, two_on_a_cu(FOLD ? 1 : P, KS, false) ? 4 : 2) void down_kernel(MxMoeJob j, Scratch s,
+template <int KS, int WK, bool FOLD>
+__global__ __launch_bounds__(kThinThreads, two_on_a_cu(FOLD ? 1 : kActPieces, KS, false) ? 4 : 2) void down_kernel(MxMoeJob j, Scratch s,
                                                                                                        MxWeights w, int per) {
-    constexpr int G = group_of(FOLD ? 1 : P, KS, false);
-    MxTokens<SGEMM_TYPE_BF16, P, KS, WK, 1, FOLD> x;
+    constexpr int G = group_of(FOLD ? 1 : kActPieces, KS, false);
+    MxTokens<SGEMM_TYPE_BF16, kActPieces, KS, WK, 1, FOLD> x;
     extern __shared__ __attribute__((aligned(16))) f32v4 red[];
     __shared__ Listed choice;
     const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK;
@@ -341,7 +340,7 @@ __global__ __launch_bounds__(256) void join_kernel(MxMoeJob j, Scratch s) {
 template <int TYPE>
 __global__ __launch_bounds__(kThinThreads) void down_few_kernel(MxMoeJob j, Scratch s, MxWeights w) {
     typedef typename MxType<TYPE>::T T;
-    constexpr int P = act_pieces(TYPE), U = 6;
+    constexpr int P = kActPieces, U = 6;
     __shared__ float ys[kThinWaves][kFew][16];   // a wave's sums: token, row
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
     const int all = j.tokens * j.top, h0 = blockIdx.x * 16;
@@ -447,43 +446,47 @@ hipError_t launch_up_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     return n > 8 ? launch_up<TYPE, 2, 8, FEW, FOLD>(j, s, stream) : launch_up<TYPE, 1, 8, FEW, FOLD>(j, s, stream);
 }
 
-template <int P, int KS, int WK, bool FOLD>
+template <int KS, int WK, bool FOLD>
 hipError_t launch_down(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     MxWeights w = mx_weights(j.down, j.sdown, (int64_t)j.experts * j.hidden, j.inner);
     const int tiles = (j.hidden + 15) / 16, slots = expert_rows(j);
     const bool pieces = w.slabs > WK * KS;
     int per = mx_share(tiles, groups_of(tiles, 1, slots, 512, pieces ? kCarryTiles : tiles), 1);
-    const int bytes = (kThinSums<group_of(FOLD ? 1 : P, KS, false), 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
+    const int bytes = (kThinSums<group_of(FOLD ? 1 : kActPieces, KS, false), 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
     void *params[] = {&j, &s, &w, &per};
-    return hipLaunchKernel((const void *)down_kernel<P, KS, WK, FOLD>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)slots),
+    return hipLaunchKernel((const void *)down_kernel<KS, WK, FOLD>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)slots),
                            dim3(kThinThreads), params, bytes, stream);
 }
 
-template <int P, bool FOLD>
+// Unfolded, three pieces of more than one slab take a CU to themselves: beyond
+// four slabs K goes in runs of eight past two workgroups on a CU (the layer for 48
+// tokens, 8 of 128 experts, 4096 x 1536, takes 265 us so, 278 with two slabs a wave; 20 tokens, 2 of 16, 4096 x 4096: 106 against 114; 24 tokens, 4 of
+// 16, 2048 x 2560: 55.6 against 58.3).
+template <bool FOLD>
 hipError_t launch_down_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     const int n = mx_slabs(j.inner);
-    if (n <= 1) return launch_down<P, 1, 1, FOLD>(j, s, stream);
-    if (n <= 2) return launch_down<P, 1, 2, FOLD>(j, s, stream);
-    if (n <= 4) return launch_down<P, 2, 2, FOLD>(j, s, stream);
-    if (n <= 6) return launch_down<P, 3, 2, FOLD>(j, s, stream);
-    if (n <= 8) return launch_down<P, 2, 4, FOLD>(j, s, stream);
+    if (n <= 1) return launch_down<1, 1, FOLD>(j, s, stream);
+    if (n <= 2) return launch_down<1, 2, FOLD>(j, s, stream);
+    if (n <= 4) return launch_down<2, 2, FOLD>(j, s, stream);
     if constexpr (FOLD) {
-        if (n > 8 && n <= 16) return launch_down<P, 4, 4, FOLD>(j, s, stream);
-        if (n > 24) return launch_down<P, 4, 8, FOLD>(j, s, stream);
+        if (n <= 6) return launch_down<3, 2, FOLD>(j, s, stream);
+        if (n <= 8) return launch_down<2, 4, FOLD>(j, s, stream);
+        if (n <= 16) return launch_down<4, 4, FOLD>(j, s, stream);
+        return n > 24 ? launch_down<4, 8, FOLD>(j, s, stream) : launch_down<3, 8, FOLD>(j, s, stream);
+    } else {
+        return launch_down<1, 8, FOLD>(j, s, stream);
     }
-    if (n <= 16) return launch_down<P, 2, 8, FOLD>(j, s, stream);
-    return launch_down<P, 3, 8, FOLD>(j, s, stream);
 }
 
 // Whether an expert's tokens always fit a folded tile.  (Where only most do, the
 // few workgroups that stream their weights twice are what the kernel waits for:
-// 48 tokens, 8 of 128 experts, 4096 x 1536: 124 us, unfolded 104.)
+// `down` of two pieces, 48 tokens, 8 of 128 experts, 4096 x 1536: 124 us, unfolded 104.)
 bool folds(const MxMoeJob &j, int pieces) { return j.tokens <= 16 / pieces; }
 
 template <int TYPE>
 hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
     MxMoeJob j = job;
-    Scratch s = layout(j.scratch, j.tokens, j.hidden, j.inner, j.experts, j.top, TYPE);
+    Scratch s = layout(j.scratch, j.tokens, j.hidden, j.inner, j.experts, j.top);
     void *params[] = {&j, &s};
     const unsigned ge = (unsigned)((j.experts + 3) / 4);
     hipError_t e = j.tokens < 4 ? hipLaunchKernel((const void *)logits_kernel<TYPE, 1>, dim3(ge, (unsigned)j.tokens), dim3(256),
@@ -501,11 +504,11 @@ hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
     }
     e = hipLaunchKernel((const void *)choose_kernel, dim3((unsigned)j.tokens), dim3(kThinThreads), params, 0, stream);
     if (e != hipSuccess) return e;
-    constexpr int PX = mx_pieces(TYPE), PA = act_pieces(TYPE);
+    constexpr int PX = mx_pieces(TYPE);
     if (PX > 1 && folds(j, PX)) e = launch_up_slabs<TYPE, false, (PX > 1)>(j, s, stream);
     else e = launch_up_slabs<TYPE, false, false>(j, s, stream);
     if (e != hipSuccess) return e;
-    e = folds(j, PA) ? launch_down_slabs<PA, true>(j, s, stream) : launch_down_slabs<PA, false>(j, s, stream);
+    e = folds(j, kActPieces) ? launch_down_slabs<true>(j, s, stream) : launch_down_slabs<false>(j, s, stream);
     if (e != hipSuccess) return e;
     return hipLaunchKernel((const void *)join_kernel<TYPE>, dim3((unsigned)((j.hidden + 255) / 256), (unsigned)j.tokens), dim3(256),
                            params, 0, stream);
@@ -513,8 +516,8 @@ hipError_t launch_type(const MxMoeJob &job, hipStream_t stream) {
 
 }  // namespace
 
-int64_t mx4_moe_scratch(int tokens, int hidden, int inner, int experts, int top, int type) {
-    return layout(nullptr, tokens, hidden, inner, experts, top, type).bytes;
+int64_t mx4_moe_scratch(int tokens, int hidden, int inner, int experts, int top) {
+    return layout(nullptr, tokens, hidden, inner, experts, top).bytes;
 }
 
 hipError_t launch_mx4_moe(const MxMoeJob &j, hipStream_t s) {

@@ -429,6 +429,6 @@ struct MxMoeJob {
 hipError_t launch_mx4_linear(const MxLinearJob &j, hipStream_t s);
 int64_t mx4_linear_scratch(int M, int N, int K, int type);
 hipError_t launch_mx4_moe(const MxMoeJob &j, hipStream_t s);
-int64_t mx4_moe_scratch(int tokens, int hidden, int inner, int experts, int top, int type);
+int64_t mx4_moe_scratch(int tokens, int hidden, int inner, int experts, int top);
 
 }  // namespace sgemm

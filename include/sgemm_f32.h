@@ -484,8 +484,8 @@ int sgemm_f32_mx4_linear_scratch(int M, int N, int K, int type, long long *bytes
  * 4-bit matrix of experts * 2 * inner rows and hidden columns: expert after
  * expert, first the inner rows of G_e, then those of U_e.  `down`: experts *
  * hidden rows, inner columns.  The choice is made on sums in 64 bits.  The
- * inner activations are held to 24 bits for fp32, to 16 for 16-bit types (and
- * to multiples of 2^-133).  tokens <= 64, 1 <= top <= min(experts, 16),
+ * inner activations are held to 24 bits (and to multiples of 2^-133) for
+ * every type.  tokens <= 64, 1 <= top <= min(experts, 16),
  * experts <= 1024; hidden and inner at least 1.  scratch: device memory of at
  * least the bytes that sgemm_f32_mx4_moe_scratch gives, 256-byte aligned,
  * overlapping nothing; its contents do not matter before or after.
