@@ -43,10 +43,12 @@ namespace sgemm {
 namespace {
 
 constexpr int kFew = 16;
-// Whether the registers let a CU hold two workgroups, which hide each other's
-// beginnings and meetings, and the row tiles that a wave adds up at a time: as
-// many loads in flight as the registers hold.
-constexpr bool two_on_a_cu(int pieces, int ks, bool few) { return ks <= 2 && pieces * ks <= (few ? 2 : 4); }
+// Whether the registers (128 a lane, without spills) let a CU hold two
+// workgroups, which hide each other's beginnings and meetings, and the row
+// tiles that a wave adds up at a time: as many loads in flight as the registers
+// hold.  (Two pieces of two slabs spilled at two workgroups: `up` of fp16, the
+// layer for 48 tokens, 8 of 128 experts, 4096 x 1536: 365 us so, 336 with one.)
+constexpr bool two_on_a_cu(int pieces, int ks, bool few) { return ks <= 2 && pieces * ks <= (few ? 2 : 3); }
 // Pieces by what they take of the registers while they are made: folded ones
 // count as one, but an fp32 token is held whole first.
 constexpr int register_pieces(int type, bool fold) { return fold && type != SGEMM_TYPE_F32 ? 1 : mx_pieces(type); }
@@ -435,7 +437,9 @@ hipError_t launch_up_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     if constexpr (!FEW) {   // (few choices: latency counts, all waves along K)
         if (n <= 2) return launch_up<TYPE, 1, 2, FEW, FOLD>(j, s, stream);
         if (n <= 4) return launch_up<TYPE, 1, 4, FEW, FOLD>(j, s, stream);
-        if (n <= 8) return launch_up<TYPE, 2, 4, FEW, FOLD>(j, s, stream);
+        // (two pieces of two slabs have a CU to themselves: fp16, 32 tokens, 8 of 64
+        // experts, 768 x 512: 43.2 us with two slabs, 36.2 with one)
+        if (n <= 8) return launch_up<TYPE, P == 2 ? 1 : 2, P == 2 ? 8 : 4, FEW, FOLD>(j, s, stream);
         if constexpr (P == 1) {
             if (n <= 12) return launch_up<TYPE, 3, 4, FEW, FOLD>(j, s, stream);
             if (n > 16 && n <= 24) return launch_up<TYPE, 3, 8, FEW, FOLD>(j, s, stream);

@@ -52,3 +52,14 @@ def test_loop_of_the_large_product(asm):
         assert len(waits) == 1, m.group(1)          # the one before the barrier
         found += 1
     assert found == 6                               # two chunk lengths, three result types
+
+
+@pytest.mark.parametrize("source", ["mx4_linear.hip", "mx4_moe.hip"])
+def test_streaming_kernels_hold_their_registers(source, tmp_path):
+    """The kernels that stream weights past tokens in registers: each bound on the registers of a lane is one that
+    the kernel fits without spilling."""
+    text = assembly(source, tmp_path)
+    kernels = re.findall(r"\.name:\s*(_Z\S+)\n.*?\.private_segment_fixed_size:\s*(\d+).*?\.vgpr_spill_count:\s*(\d+)", text, re.S)
+    assert len(kernels) == text.count(".vgpr_spill_count:") and len(kernels) > 20
+    assert [k for k in kernels if k[1:] != ("0", "0")] == []
+    assert not re.search(r"v_pk_(add|mul|fma)_f32", text)
