@@ -37,19 +37,39 @@ struct Args {
     int64_t pitch;
 };
 
+__device__ __forceinline__ int64_t weight_row(const Args &a, int tile, int m) {
+    const int n = tile * 16 + m;
+    return n < a.N ? n : a.N - 1;   // rows past N: computed, not stored
+}
+
+// Sums of token t, rows 16 tile + 4 quad + c where bit c of `rows` is set.
+template <int TYPE>
+__device__ __forceinline__ void store_sums(const Args &a, int part, int t, int tile, int quad, f32v4 v, int rows) {
+    typedef typename MxType<TYPE>::T T;
+    const int n = tile * 16 + 4 * quad;
+    if (t >= a.M) return;
+    if (a.parts > 1) {
+        mx_store_rows(a.partial + ((int64_t)part * a.M + t) * a.pitch + n, v, rows);
+        return;
+    }
+    T *y = (T *)a.y + t * a.ldy + n;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (n + c < a.N && (rows >> c & 1)) y[c] = MxType<TYPE>::from(v[c]);
+}
+
 template <int TYPE, int KS, int MT, int G, bool FOLD>
 __global__ __launch_bounds__(kThinThreads, two_on_a_cu(register_pieces(TYPE, FOLD), KS, MT) ? 4 : 2) void linear_kernel(Args a) {
     typedef typename MxType<TYPE>::T T;
+    typedef MxTokens<TYPE, mx_pieces(TYPE), KS, kThinWaves, MT, FOLD> Tokens;
+    typedef MxStream<1, G, KS, kThinWaves, false> Stream;
     __shared__ __attribute__((aligned(16))) f32v4 red[kThinSums<G, MT>];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int part = blockIdx.x % a.parts, first = blockIdx.x / a.parts * a.per, m0 = blockIdx.y * 16 * MT;
     const int tiles = (a.N + 15) / 16, end = first + a.per < tiles ? first + a.per : tiles;
     const int slab0 = (part * kThinWaves + wave) * KS;
-    const auto row_of = [&](int tile, int m) -> int64_t {
-        const int n = tile * 16 + m;
-        return n < a.N ? n : a.N - 1;   // rows past N: computed, not stored
-    };
-    MxTokens<TYPE, mx_pieces(TYPE), KS, kThinWaves, MT, FOLD> x;
+    const auto row_of = [&](int tile, int m) { return weight_row(a, tile, m); };
+    Tokens x;
     const T *row[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -57,22 +77,26 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(register_pieces(TYPE, FOL
         row[mt] = x.token() >= 0 && t < a.M ? (const T *)a.x + t * a.ldx : nullptr;
     }
     x.load(row, slab0, a.K, lane >> 4);
-    MxStream<1, G, KS, kThinWaves, false> stream;
+    Stream stream;
     stream.begin(a.w, slab0, first, end, row_of);
-    stream.run(
-        x, a.w, slab0, first, end, red, nullptr, true, true, row_of,
-        [&](int tile, int mt, int l, const f32v4(&v)[1]) {
-            const int t = m0 + mt * 16 + (l & 15), n = tile * 16 + 4 * (l >> 4);
-            if (t >= a.M) return;
-            if (a.parts > 1) {
-                *(f32v4 *)(a.partial + ((int64_t)part * a.M + t) * a.pitch + n) = v[0];
-                return;
-            }
-            T *y = (T *)a.y + t * a.ldy + n;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (n + c < a.N) y[c] = MxType<TYPE>::from(v[0][c]);
-        });
+    bool odd = false;
+    stream.run(x, a.w, slab0, first, end, red, nullptr, true, true, odd, row_of, [&](int tile, int mt, int l, const f32v4(&v)[1], int rows) {
+        store_sums<TYPE>(a, part, m0 + mt * 16 + (l & 15), tile, l >> 4, v[0], rows);
+    });
+    if (__builtin_expect(odd, 0)) {   // weights beyond the largest float?
+        const Args b = mx_arguments<Args>();
+        const int part = blockIdx.x % b.parts, first = blockIdx.x / b.parts * b.per, m0 = blockIdx.y * 16 * MT;
+        const int tiles = (b.N + 15) / 16, end = first + b.per < tiles ? first + b.per : tiles;
+        Stream::template mend<MT, Tokens::kTokens>(
+            b.w, part * kThinWaves * KS, (part + 1) * kThinWaves * KS, first, end, [&](int tile, int m) { return weight_row(b, tile, m); },
+            [&](int mt, int t16, int column) {
+                const int t = m0 + mt * 16 + t16;
+                return t < b.M && column < b.K ? MxType<TYPE>::load((const T *)b.x + t * b.ldx + column) : 0.0f;
+            },
+            [&](int tile, int mt, int l, const f32v4(&v)[1], int rows) {
+                store_sums<TYPE>(b, part, m0 + mt * 16 + (l & 15), tile, l >> 4, v[0], rows);
+            });
+    }
 }
 
 // Adds the parts; a thread takes one value.

@@ -208,17 +208,18 @@ __global__ __launch_bounds__(kThinThreads) void choose_kernel(MxMoeJob j, Scratc
 // it does (4 tokens, 8 of 64 experts of 2048 x 768: 35.1 us, 35.9 with a row of
 // workgroups for every expert).
 struct Listed {
-    int list[SGEMM_MX4_MAX_TOKENS], count, earlier;
+    int list[SGEMM_MX4_MAX_TOKENS], token[SGEMM_MX4_MAX_TOKENS], count, earlier, expert;
 };
 __device__ __forceinline__ int list_tokens(const MxMoeJob &j, const int *chosen, int &e, Listed &l) {
     const int all = j.tokens * j.top;
     const bool by_choice = all < j.experts;
     e = by_choice ? chosen[blockIdx.y] : (int)blockIdx.y;
-    if (threadIdx.x == 0) l.count = 0, l.earlier = 0;
+    if (threadIdx.x == 0) l.count = 0, l.earlier = 0, l.expert = e;
     __syncthreads();
     for (int a = threadIdx.x; a < all; a += kThinThreads)
         if (chosen[a] == e) {
-            l.list[atomicAdd(&l.count, 1)] = a;
+            const int i = atomicAdd(&l.count, 1);
+            l.list[i] = a, l.token[i] = a / j.top;
             if (by_choice && a < (int)blockIdx.y) l.earlier = 1;
         }
     __syncthreads();
@@ -226,29 +227,61 @@ __device__ __forceinline__ int list_tokens(const MxMoeJob &j, const int *chosen,
 }
 int expert_rows(const MxMoeJob &j) { return j.tokens * j.top < j.experts ? j.tokens * j.top : j.experts; }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+// Arguments of the kernels that stream weights.
+struct StreamArgs {
+    MxMoeJob j;
+    Scratch s;
+    MxWeights w;
+    int per;   // row tiles of a workgroup
+};
 
 // ---- up ----
 
+// Row tiles come in pairs: 16 rows of the gate, the same 16 of U.
+inline __host__ __device__ int up_tiles(const MxMoeJob &j) { return 2 * ((j.inner + 15) / 16); }
+__device__ __forceinline__ int64_t up_row(const MxMoeJob &j, int e, int tile, int m) {
+    const int f = (tile >> 1) * 16 + m;
+    return (int64_t)2 * e * j.inner + (f < j.inner ? f : j.inner - 1) + (tile & 1 ? j.inner : 0);
+}
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
+// Inner activations f .. f + 3 of choice a, those whose bits are set in `rows`.
+__device__ __forceinline__ void store_activations(const MxMoeJob &j, const Scratch &s, int a, int f, f32v4 g, f32v4 u, int rows) {
+    uint16_t p[4][kActPieces];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) mx_split<kActPieces>(f + c < j.inner ? silu(g[c]) * u[c] : 0.0f, p[c]);
+#pragma unroll
+    for (int k = 0; k < kActPieces; ++k) {
+        uint16_t *to = s.act + ((int64_t)k * (j.tokens * j.top) + a) * s.ld_act + f;
+        if (rows == 15) {
+            *(uint2 *)to = uint2{(uint32_t)p[0][k] | (uint32_t)p[1][k] << 16, (uint32_t)p[2][k] | (uint32_t)p[3][k] << 16};
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (rows >> c & 1) to[c] = p[c][k];
+        }
+    }
+}
+
 template <int TYPE, int KS, int WK, bool FEW, bool FOLD>
-__global__ __launch_bounds__(kThinThreads, two_on_a_cu(register_pieces(TYPE, FOLD), KS, FEW) ? 4 : 2) void up_kernel(MxMoeJob j, Scratch s,
-                                                                                                      MxWeights w, int per) {
+__global__ __launch_bounds__(kThinThreads, two_on_a_cu(register_pieces(TYPE, FOLD), KS, FEW) ? 4 : 2) void up_kernel(StreamArgs args) {
     typedef typename MxType<TYPE>::T T;
-    constexpr int G = group_of(register_pieces(TYPE, FOLD), KS, FEW), PA = kActPieces;
-    const int all = j.tokens * j.top;
+    constexpr int G = group_of(register_pieces(TYPE, FOLD), KS, FEW);
+    typedef MxTokens<TYPE, mx_pieces(TYPE), KS, WK, 1, FOLD> Tokens;
+    typedef MxStream<2, G, KS, WK, true> Stream;
+    const MxMoeJob &j = args.j;
+    const Scratch &s = args.s;
+    const MxWeights &w = args.w;
     // red, then the sums kept from one piece of K to the next.
     extern __shared__ __attribute__((aligned(16))) f32v4 red[];
     __shared__ std::conditional_t<FEW, Choice, Listed> choice;
     const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK;
-    MxTokens<TYPE, mx_pieces(TYPE), KS, WK, 1, FOLD> x;
-    MxStream<2, G, KS, WK, true> stream;
-    // Row tiles come in pairs: 16 rows of the gate, the same 16 of U.
-    const int tiles = 2 * ((j.inner + 15) / 16), first = blockIdx.x * per, end = first + per < tiles ? first + per : tiles;
+    Tokens x;
+    Stream stream;
+    const int tiles = up_tiles(j), first = blockIdx.x * args.per, end = first + args.per < tiles ? first + args.per : tiles;
     int e = blockIdx.y, n = 1;
-    const auto row_of = [&](int tile, int m) -> int64_t {
-        const int f = (tile >> 1) * 16 + m;
-        return (int64_t)2 * e * j.inner + (f < j.inner ? f : j.inner - 1) + (tile & 1 ? j.inner : 0);
-    };
+    const auto row_of = [&](int tile, int m) { return up_row(j, e, tile, m); };
     if constexpr (FEW) {
         // blockIdx.y: a choice.  Its token is known before its expert.
         const int t = blockIdx.y / j.top;
@@ -259,32 +292,26 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(register_pieces(TYPE, FOL
     } else {
         n = list_tokens(j, s.chosen, e, choice);
     }
+    bool odd = false;
     for (int i0 = 0; i0 < n; i0 += x.kTokens) {
         const T *row[1] = {nullptr};
         if (x.token() >= 0 && i0 + x.token() < n) {
-            int a = blockIdx.y;
-            if constexpr (!FEW) a = choice.list[i0 + x.token()];
-            row[0] = (const T *)j.x + (int64_t)(a / j.top) * j.ldx;
+            int t;
+            if constexpr (FEW) t = blockIdx.y / j.top;
+            else t = choice.token[i0 + x.token()];
+            row[0] = (const T *)j.x + (int64_t)t * j.ldx;
         }
         for (int s0 = 0; s0 < w.slabs; s0 += WK * KS) {
             if (!FEW || s0 > 0) x.load(row, s0 + kw * KS, j.hidden, lane >> 4);
             stream.begin(w, s0 + kw * KS, first, end, row_of);
-            stream.run(x, w, s0 + kw * KS, first, end, red, red + kThinSums<G, 1>, s0 == 0, s0 + WK * KS >= w.slabs, row_of,
-                       [&](int tile, int, int l, const f32v4(&v)[2]) {
-                                const int i = i0 + (l & 15), f = (tile >> 1) * 16 + 4 * (l >> 4);
-                                if (i >= n) return;
-                                int a = blockIdx.y;
-                                if constexpr (!FEW) a = choice.list[i];
-                                uint16_t p[4][PA];
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    mx_split<PA>(f + c < j.inner ? silu(v[0][c]) * v[1][c] : 0.0f, p[c]);
-#pragma unroll
-                                for (int k = 0; k < PA; ++k)
-                                    *(uint2 *)(s.act + ((int64_t)k * all + a) * s.ld_act + f) =
-                                        uint2{(uint32_t)p[0][k] | (uint32_t)p[1][k] << 16,
-                                              (uint32_t)p[2][k] | (uint32_t)p[3][k] << 16};
-                            });
+            stream.run(x, w, s0 + kw * KS, first, end, red, red + kThinSums<G, 1>, s0 == 0, s0 + WK * KS >= w.slabs, odd, row_of,
+                       [&](int tile, int, int l, const f32v4(&v)[2], int rows) {
+                           const int i = i0 + (l & 15);
+                           if (i >= n) return;
+                           int a = blockIdx.y;
+                           if constexpr (!FEW) a = choice.list[i];
+                           store_activations(j, s, a, (tile >> 1) * 16 + 4 * (l >> 4), v[0], v[1], rows);
+                       });
         }
     }
     if constexpr (FEW)
@@ -292,40 +319,99 @@ __global__ __launch_bounds__(kThinThreads, two_on_a_cu(register_pieces(TYPE, FOL
             const int t = blockIdx.y / j.top;
             write_choice(j, s, t, s.logits + (int64_t)t * j.experts, choice);
         }
+    if (__builtin_expect(odd, 0)) {   // weights beyond the largest float?
+        const StreamArgs b = mx_arguments<StreamArgs>();
+        const int tiles = up_tiles(b.j), first = blockIdx.x * b.per, end = first + b.per < tiles ? first + b.per : tiles;
+        int count = 1;
+        if constexpr (!FEW) count = choice.count;
+        const auto choice_of = [&](int i) {
+            if constexpr (FEW) return (int)blockIdx.y;
+            else return choice.list[i];
+        };
+        const auto token_of = [&](int i) {
+            if constexpr (FEW) return (int)blockIdx.y / b.j.top;
+            else return choice.token[i];
+        };
+        int e;
+        if constexpr (FEW) e = choice.expert[blockIdx.y % b.j.top];
+        else e = choice.expert;
+#pragma nounroll
+        for (int i0 = 0; i0 < count; i0 += Tokens::kTokens)
+            Stream::template mend<1, Tokens::kTokens>(
+                b.w, 0, b.w.slabs, first, end, [&](int tile, int m) { return up_row(b.j, e, tile, m); },
+                [&](int, int t, int column) {
+                    if (i0 + t >= count || column >= b.j.hidden) return 0.0f;
+                    return MxType<TYPE>::load((const T *)b.j.x + (int64_t)token_of(i0 + t) * b.j.ldx + column);
+                },
+                [&](int tile, int, int l, const f32v4(&v)[2], int rows) {
+                    const int i = i0 + (l & 15);
+                    if (i < count) store_activations(b.j, b.s, choice_of(i), (tile >> 1) * 16 + 4 * (l >> 4), v[0], v[1], rows);
+                });
+    }
 }
 
 // ---- down ----
 
+// An inner activation of choice a from its pieces, zero beyond the last.
+__device__ __forceinline__ float activation(const MxMoeJob &j, const Scratch &s, int a, int column) {
+    if (column >= j.inner) return 0.0f;
+    float v = 0.0f;
+#pragma unroll
+    for (int p = 0; p < kActPieces; ++p)
+        v += MxType<SGEMM_TYPE_BF16>::load(s.act + ((int64_t)p * (j.tokens * j.top) + a) * s.ld_act + column);
+    return v;
+}
+
+__device__ __forceinline__ int64_t down_row(const MxMoeJob &j, int e, int tile, int m) {
+    const int h = tile * 16 + m;
+    return (int64_t)e * j.hidden + (h < j.hidden ? h : j.hidden - 1);
+}
+
 template <int KS, int WK, bool FOLD>
-__global__ __launch_bounds__(kThinThreads, two_on_a_cu(FOLD ? 1 : kActPieces, KS, false) ? 4 : 2) void down_kernel(MxMoeJob j, Scratch s,
-                                                                                                       MxWeights w, int per) {
+__global__ __launch_bounds__(kThinThreads, two_on_a_cu(FOLD ? 1 : kActPieces, KS, false) ? 4 : 2) void down_kernel(StreamArgs args) {
     constexpr int G = group_of(FOLD ? 1 : kActPieces, KS, false);
-    MxTokens<SGEMM_TYPE_BF16, kActPieces, KS, WK, 1, FOLD> x;
+    typedef MxTokens<SGEMM_TYPE_BF16, kActPieces, KS, WK, 1, FOLD> Tokens;
+    typedef MxStream<1, G, KS, WK, true> Stream;
+    const MxMoeJob &j = args.j;
+    const Scratch &s = args.s;
+    const MxWeights &w = args.w;
+    Tokens x;
     extern __shared__ __attribute__((aligned(16))) f32v4 red[];
     __shared__ Listed choice;
     const int lane = threadIdx.x & 63, kw = (threadIdx.x >> 6) % WK;
     int e;
     const int n = list_tokens(j, s.chosen, e, choice);
     const int *list = choice.list;
-    const int tiles = (j.hidden + 15) / 16, first = blockIdx.x * per, end = first + per < tiles ? first + per : tiles;
-    const auto row_of = [&](int tile, int m) -> int64_t {
-        const int h = tile * 16 + m;
-        return (int64_t)e * j.hidden + (h < j.hidden ? h : j.hidden - 1);
-    };
-    MxStream<1, G, KS, WK, true> stream;
+    const int tiles = (j.hidden + 15) / 16, first = blockIdx.x * args.per, end = first + args.per < tiles ? first + args.per : tiles;
+    const auto row_of = [&](int tile, int m) { return down_row(j, e, tile, m); };
+    Stream stream;
+    bool odd = false;
     for (int i0 = 0; i0 < n; i0 += x.kTokens) {
         const int t = x.token();
         const uint16_t *row = t >= 0 && i0 + t < n ? s.act + (int64_t)list[i0 + t] * s.ld_act : nullptr;
         for (int s0 = 0; s0 < w.slabs; s0 += WK * KS) {
             x.load_pieces(row, (int64_t)j.tokens * j.top * s.ld_act, s0 + kw * KS, (int)s.ld_act, lane >> 4);
             stream.begin(w, s0 + kw * KS, first, end, row_of);
-            stream.run(
-                x, w, s0 + kw * KS, first, end, red, red + kThinSums<G, 1>, s0 == 0, s0 + WK * KS >= w.slabs, row_of,
-                [&](int tile, int, int l, const f32v4(&v)[1]) {
-                    const int i = i0 + (l & 15);
-                    if (i < n) *(f32v4 *)(s.part + (int64_t)list[i] * s.ld_part + tile * 16 + 4 * (l >> 4)) = v[0];
-                });
+            stream.run(x, w, s0 + kw * KS, first, end, red, red + kThinSums<G, 1>, s0 == 0, s0 + WK * KS >= w.slabs, odd, row_of,
+                       [&](int tile, int, int l, const f32v4(&v)[1], int rows) {
+                           const int i = i0 + (l & 15);
+                           if (i < n) mx_store_rows(s.part + (int64_t)list[i] * s.ld_part + tile * 16 + 4 * (l >> 4), v[0], rows);
+                       });
         }
+    }
+    if (__builtin_expect(odd, 0)) {   // weights beyond the largest float?
+        const StreamArgs b = mx_arguments<StreamArgs>();
+        const int tiles = (b.j.hidden + 15) / 16, first = blockIdx.x * b.per, end = first + b.per < tiles ? first + b.per : tiles;
+#pragma nounroll
+        for (int i0 = 0; i0 < choice.count; i0 += Tokens::kTokens)
+            Stream::template mend<1, Tokens::kTokens>(
+                b.w, 0, b.w.slabs, first, end, [&](int tile, int m) { return down_row(b.j, choice.expert, tile, m); },
+                [&](int, int t, int column) { return i0 + t < choice.count ? activation(b.j, b.s, choice.list[i0 + t], column) : 0.0f; },
+                [&](int tile, int, int l, const f32v4(&v)[1], int rows) {
+                    const int i = i0 + (l & 15);
+                    if (i < choice.count)
+                        mx_store_rows(b.s.part + (int64_t)choice.list[i] * b.s.ld_part + tile * 16 + 4 * (l >> 4), v[0], rows);
+                });
     }
 }
 
@@ -391,12 +477,30 @@ __global__ __launch_bounds__(kThinThreads) void down_few_kernel(MxMoeJob j, Scra
         }
     }
     __syncthreads();
-    for (int i = tid; i < j.tokens * 16; i += kThinThreads) {
-        const int t = i >> 4, r = i & 15;
-        float sum = ys[0][t][r];
+    static_assert(kFew * 16 <= kThinThreads, "a thread takes one result");
+    const int t = tid >> 4, r = tid & 15;
+    const bool mine = t < j.tokens && h0 + r < j.hidden;
+    float sum = 0.0f;
+    if (mine) {
+        sum = ys[0][t][r];
 #pragma unroll
         for (int k = 1; k < kThinWaves; ++k) sum += ys[k][t][r];
-        if (h0 + r < j.hidden) ((T *)j.y)[t * j.ldy + h0 + r] = MxType<TYPE>::from(sum);
+        ((T *)j.y)[t * j.ldy + h0 + r] = MxType<TYPE>::from(sum);
+    }
+    // Once more those to which a weight beyond the largest float adds.
+    for (uint64_t odd = __ballot(mine && !mx_finite(sum)); __builtin_expect(odd != 0, 0); odd &= odd - 1) {
+        const int l = __ffsll((unsigned long long)odd) - 1, i = __builtin_amdgcn_readfirstlane(wave) * 64 + l;
+        const int begin = (i >> 4) * j.top, end = begin + j.top;
+        const auto row = [&](int a) { return (int64_t)s.chosen[a] * j.hidden + h0 + (i & 15); };
+        bool beyond = false;
+#pragma nounroll
+        for (int a = begin; a < end; ++a) beyond |= mx_beyond(w, row(a), 0, w.slabs);
+        if (!beyond) continue;
+        sum = 0.0f;
+#pragma nounroll
+        for (int a = begin; a < end; ++a)
+            sum = fmaf(s.weight[a], mx_plain_sum(w, row(a), 0, w.slabs, [&](int column) { return activation(j, s, a, column); }), sum);
+        if (lane == l) ((T *)j.y)[t * j.ldy + h0 + r] = MxType<TYPE>::from(sum);
     }
 }
 
@@ -417,13 +521,13 @@ constexpr int kCarryTiles = 32;
 template <int TYPE, int KS, int WK, bool FEW, bool FOLD>
 hipError_t launch_up(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     constexpr int P = register_pieces(TYPE, FOLD), G = group_of(P, KS, FEW);
-    MxWeights w = mx_weights(j.up, j.sup, (int64_t)2 * j.experts * j.inner, j.hidden);
-    const int tiles = 2 * ((j.inner + 15) / 16), all = j.tokens * j.top, slots = FEW ? all : expert_rows(j);
-    const bool pieces = w.slabs > WK * KS;
+    StreamArgs args{j, s, mx_weights(j.up, j.sup, (int64_t)2 * j.experts * j.inner, j.hidden), 0};
+    const int tiles = up_tiles(j), all = j.tokens * j.top, slots = FEW ? all : expert_rows(j);
+    const bool pieces = args.w.slabs > WK * KS;
     const int fill = FEW && !two_on_a_cu(P, KS, FEW) ? 256 : 512;
-    int per = mx_share(tiles, groups_of(tiles, 2, slots, fill, pieces ? kCarryTiles : tiles), 2);
+    const int per = args.per = mx_share(tiles, groups_of(tiles, 2, slots, fill, pieces ? kCarryTiles : tiles), 2);
     const int bytes = (kThinSums<G, 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
-    void *params[] = {&j, &s, &w, &per};
+    void *params[] = {&args};
     return hipLaunchKernel((const void *)up_kernel<TYPE, KS, WK, FEW, FOLD>,
                            dim3((unsigned)((tiles + per - 1) / per), (unsigned)slots), dim3(kThinThreads), params, bytes, stream);
 }
@@ -452,12 +556,12 @@ hipError_t launch_up_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
 
 template <int KS, int WK, bool FOLD>
 hipError_t launch_down(MxMoeJob &j, Scratch &s, hipStream_t stream) {
-    MxWeights w = mx_weights(j.down, j.sdown, (int64_t)j.experts * j.hidden, j.inner);
+    StreamArgs args{j, s, mx_weights(j.down, j.sdown, (int64_t)j.experts * j.hidden, j.inner), 0};
     const int tiles = (j.hidden + 15) / 16, slots = expert_rows(j);
-    const bool pieces = w.slabs > WK * KS;
-    int per = mx_share(tiles, groups_of(tiles, 1, slots, 512, pieces ? kCarryTiles : tiles), 1);
+    const bool pieces = args.w.slabs > WK * KS;
+    const int per = args.per = mx_share(tiles, groups_of(tiles, 1, slots, 512, pieces ? kCarryTiles : tiles), 1);
     const int bytes = (kThinSums<group_of(FOLD ? 1 : kActPieces, KS, false), 1> + (pieces ? kCarryTiles * 64 : 0)) * 16;
-    void *params[] = {&j, &s, &w, &per};
+    void *params[] = {&args};
     return hipLaunchKernel((const void *)down_kernel<KS, WK, FOLD>, dim3((unsigned)((tiles + per - 1) / per), (unsigned)slots),
                            dim3(kThinThreads), params, bytes, stream);
 }

@@ -29,6 +29,12 @@
 // of a wave's values of an fp32 token lie below 2^-60 they are taken 2^32 times
 // larger and the wave's sum 2^32 times smaller: both exact, and far from
 // overflow with the largest weight.
+//
+// A code under a scale byte of 253 or 254 can exceed the largest float, though
+// its products need not.  As bf16 it is infinite, and its product with a zero
+// piece of a token NaN: it always shows in the sum.  So a wave that met an
+// infinite sum or NaN looks its rows over at the end and computes those that
+// hold such a weight anew, in plain floats from memory.
 #pragma once
 
 #include "mx4.h"
@@ -258,6 +264,62 @@ struct MxWeights {
     }
 };
 
+__device__ __forceinline__ bool mx_finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
+
+// The four floats of v whose bits are set in `rows`.
+__device__ __forceinline__ void mx_store_rows(float *p, f32v4 v, int rows) {
+    if (rows == 15) {
+        *(f32v4 *)p = v;
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (rows >> c & 1) p[c] = v[c];
+}
+
+// Whether row r holds a weight beyond the largest float in slabs [from, to):
+// from 2 on under scale byte 254, from 4 on under 253.  For a whole wave.
+__device__ __forceinline__ bool mx_beyond(const MxWeights &w, int64_t r, int from, int to) {
+    const int lane = threadIdx.x & 63;
+    uint32_t hit = 0;
+#pragma nounroll
+    for (int b0 = 4 * from; b0 < 4 * to; b0 += 64) {
+        const int block = b0 + lane;
+        const uint32_t s = block < 4 * to ? w.word(r, block >> 2) >> (8 * (block & 3)) & 255u : 0;
+        if (s - 253u < 2u) {
+            const uint4 c = *(const uint4 *)(w.codes + r * w.rowb + (int64_t)block * 16);
+            hit |= s == 254 ? (c.x | c.y | c.z | c.w) & 0x44444444u
+                            : ((c.x & c.x >> 1) | (c.y & c.y >> 1) | (c.z & c.z >> 1) | (c.w & c.w >> 1)) & 0x22222222u;
+        }
+    }
+    return __any(hit != 0);
+}
+
+// The sum over slabs [from, to) of row r times a token, whose value at a column
+// (zero beyond the last one) is value(column).  In plain floats, of a quarter of
+// the weights: those are exact from 2^-130 to 1.5 2^127.  For a whole wave.
+template <class Value>
+__device__ __forceinline__ float mx_plain_sum(const MxWeights &w, int64_t r, int from, int to, Value value) {
+    const int lane = threadIdx.x & 63;
+    float quarter = 0.0f;
+#pragma nounroll
+    for (int b0 = 4 * from; b0 < 4 * to; b0 += 64) {
+        const int block = b0 + lane;
+        if (block >= 4 * to) break;
+        const uint32_t s = w.word(r, block >> 2) >> (8 * (block & 3)) & 255u;
+        const float f = s == 255 ? __uint_as_float(0x7fc00000u) : ldexpf(1.0f, (int)s - 129);
+#pragma nounroll
+        for (int k = 0; k < 16; ++k) {
+            const auto two = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.codes[r * w.rowb + (int64_t)block * 16 + k], 1.0f, 0);
+            quarter = fmaf(value(block * 32 + 2 * k), two[0] * f, quarter);
+            quarter = fmaf(value(block * 32 + 2 * k + 1), two[1] * f, quarter);
+        }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) quarter += __shfl_xor(quarter, off, 64);
+    return 4.0f * quarter;
+}
+
 inline __host__ __device__ MxWeights mx_weights(const uint8_t *codes, const uint8_t *scales, int64_t rows, int cols) {
     return MxWeights{codes, (const uint32_t *)scales, (int64_t)mx_slabs(cols) * kMxSlabBytes, mx_plane_rows(rows), mx_slabs(cols)};
 }
@@ -326,15 +388,17 @@ struct MxStream {
         for (int i = 0; i < KS; i += pair(i) ? 2 : 1) fetch(w, slab0, i, first, end, row);
     }
 
-    // After begin with the same arguments.  emit(tile, mt, l, sums) takes the
-    // sums of U tiles (tile .. tile + U - 1) for token l % 16 of tile mt, rows
-    // 4 (l / 16) .. + 3 of each.  red: LDS for kThinSums<G, MT> sums.
+    // After begin with the same arguments.  emit(tile, mt, l, sums, rows) takes
+    // the sums of U tiles (tile .. tile + U - 1) for token l % 16 of tile mt, rows
+    // 4 (l / 16) + c of each where bit c of `rows` is set.  red: LDS for kThinSums<G, MT> sums.
+    // odd is set, for the whole wave, where a sum of the last piece is infinite
+    // or NaN.
     // With K in several pieces, carry (LDS, (end - first) * MT * 64 sums)
     // holds them from the first piece to the last.  Every thread of the
     // workgroup calls this.
     template <int TYPE, int P, int MT, bool FOLD, class Row, class Emit>
     __device__ __forceinline__ void run(const MxTokens<TYPE, P, KS, WK, MT, FOLD> &x, const MxWeights &w, int slab0, int first, int end,
-                                        f32v4 *red, f32v4 *carry, bool first_piece, bool last_piece, Row row, Emit emit) {
+                                        f32v4 *red, f32v4 *carry, bool first_piece, bool last_piece, bool &odd, Row row, Emit emit) {
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4;
         for (int t0 = first; t0 < end; t0 += G * WR) {
             f32v4 acc[G][MT];
@@ -372,6 +436,7 @@ struct MxStream {
                     half[((wave * G + g) * MT + mt) * 64 + lane] = acc[g][mt];
                 }
             __syncthreads();
+            bool here = false;
             for (int i = tid; i < G / U * WR * MT * 64; i += kThinThreads) {
                 const int l = i & 63, mt = (i >> 6) % MT, unit = (i >> 6) / MT, set = unit % WR, g = unit / WR * U;
                 if (t0 + unit * U >= end) break;
@@ -393,12 +458,66 @@ struct MxStream {
                     if (!first_piece) v[u] = *kept + v[u];
                     if (!last_piece) *kept = v[u];
                 }
-                if (last_piece) emit(t0 + unit * U, mt, l, v);
+                if (last_piece) {
+                    f32v4 all = v[0];
+#pragma unroll
+                    for (int u = 1; u < U; ++u) all += v[u];
+                    here |= !mx_finite(all[0] + all[1] + (all[2] + all[3]));
+                    emit(t0 + unit * U, mt, l, v, 15);
+                }
             }
+            odd |= __builtin_amdgcn_readfirstlane(__any(here)) != 0;
         }
         __syncthreads();   // red is free
     }
+
+    // Gives emit this wave's sums of slabs [from, to) once more for the rows that
+    // hold a weight beyond the largest float; value(mt, t, column): token t of
+    // tile mt, zero beyond the last column.
+    template <int MT, int TOKENS, class Row, class Value, class Emit>
+    static __device__ __forceinline__ void mend(const MxWeights &w, int from, int to, int first, int end, Row row, Value value, Emit emit) {
+        if (to > w.slabs) to = w.slabs;
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+#pragma nounroll
+        for (int t0 = first; t0 < end; t0 += G * WR)
+#pragma nounroll
+            for (int i = wave; i < G / U * WR * MT; i += kThinWaves) {
+                const int mt = i % MT, tile = t0 + i / MT * U;
+                if (tile >= end) break;
+#pragma nounroll
+                for (int m = 0; m < 16; ++m) {
+                    bool beyond = false;
+#pragma nounroll
+                    for (int u = 0; u < U; ++u) beyond |= mx_beyond(w, row(tile + u, m), from, to);
+                    if (!beyond) continue;
+#pragma nounroll
+                    for (int t = 0; t < TOKENS; ++t) {
+                        f32v4 v[U];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const float sum = mx_plain_sum(w, row(tile + u, m), from, to, [&](int column) { return value(mt, t, column); });
+                            v[u] = f32v4{sum, sum, sum, sum};
+                        }
+                        if (lane == (m >> 2) * 16 + t) emit(tile, mt, lane, v, 1 << (m & 3));
+                    }
+                }
+            }
+    }
 };
+
+// The kernel's arguments (one struct), read again: what rare code at a kernel's
+// end needs of them is kept in no register until then.
+template <class A>
+__device__ __forceinline__ A mx_arguments() {
+    typedef const __attribute__((address_space(4))) A Argument;
+    uint64_t p = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    A a;
+    __builtin_memcpy(&a, (const void *)(Argument *)p, sizeof(A));
+    return a;
+}
 
 // The number of row tiles each workgroup of `groups` takes.
 inline int mx_share(int tiles, int groups, int unit) {

@@ -372,8 +372,10 @@ int sgemm_f32_release(void);
  *           ((b / 4) * rp + r) * 4 + b % 4; zeros beyond rows and cols
  * codes must be 16-byte aligned, scales 4-byte aligned.  The products rely on
  * the zeros beyond cols (sgemm_f32_mx4_quantize writes them).  A value is
- * code * 2^(s - 127); where that exceeds the largest float (s above 252) it
- * is infinite.  rows and cols are at most SGEMM_MX4_MAX_DIM.
+ * code * 2^(s - 127).  Where that exceeds the largest float (s above 252),
+ * sgemm_f32_mx4_dequantize gives infinity; the products take the value
+ * itself, so that a result is infinite only where it is too large.  rows and
+ * cols are at most SGEMM_MX4_MAX_DIM.
  *
  * Common to the calls below: float matrices are row-major, of one of the
  * types SGEMM_TYPE_*, with a leading dimension in elements; they need the
