@@ -551,7 +551,9 @@ hipError_t launch_up_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     }
     if constexpr (P == 1)
         if (n > 16) return launch_up<TYPE, 4, 8, FEW, FOLD>(j, s, stream);
-    return n > 8 ? launch_up<TYPE, 2, 8, FEW, FOLD>(j, s, stream) : launch_up<TYPE, 1, 8, FEW, FOLD>(j, s, stream);
+    if constexpr (FEW)
+        if (n <= 8) return launch_up<TYPE, 1, 8, FEW, FOLD>(j, s, stream);
+    return launch_up<TYPE, 2, 8, FEW, FOLD>(j, s, stream);
 }
 
 template <int KS, int WK, bool FOLD>
