@@ -532,27 +532,34 @@ hipError_t launch_up(MxMoeJob &j, Scratch &s, hipStream_t stream) {
                            dim3((unsigned)((tiles + per - 1) / per), (unsigned)slots), dim3(kThinThreads), params, bytes, stream);
 }
 
-// (slabs a wave keeps, waves along K) for a number of slabs: few idle places,
-// and no more slabs than the pieces leave registers for.
+// (slabs a wave keeps, waves along K) for a number of slabs.  Where K is short,
+// so few waves share it that none idles; else eight waves take two slabs each,
+// several runs of them if need be.  The layer for 32 tokens, 8 of 64 experts, in
+// us, against eight waves of two slabs for every length:
+//   hidden (inner 768)    256         512         1024
+//   bf16                  24.8 / 34.5 29.7 / 36.9 36.5 / 41.1
+//   fp16                  27.7 / 49.6 31.9 / 52.9 40.2 / 57.4
+//   fp32                  27.7 / 49.1 31.8 / 53.6 46.5 / 57.4
+// (Two pieces of two slabs have a CU to themselves: fp16, 768 x 512: 43.2 with
+// two slabs, 36.2 with one.)  bf16 beyond 24 slabs goes by whole runs of four
+// (24 tokens, 8 of 128 experts, 4096 x 1536: 250 against 271 us; 8 tokens, 6144 x
+// 1024: 143 against 129; 64 tokens, 4096 x 1024: the same).  Few choices: latency
+// counts, all waves along K.
 template <int TYPE, bool FEW, bool FOLD>
 hipError_t launch_up_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     constexpr int P = register_pieces(TYPE, FOLD);
     const int n = mx_slabs(j.hidden);
-    if constexpr (!FEW) {   // (few choices: latency counts, all waves along K)
+    if constexpr (FEW) {
+        if (n <= 8) return launch_up<TYPE, 1, 8, FEW, FOLD>(j, s, stream);
+        if constexpr (P == 1)
+            if (n > 16) return launch_up<TYPE, 4, 8, FEW, FOLD>(j, s, stream);
+    } else {
         if (n <= 2) return launch_up<TYPE, 1, 2, FEW, FOLD>(j, s, stream);
         if (n <= 4) return launch_up<TYPE, 1, 4, FEW, FOLD>(j, s, stream);
-        // (two pieces of two slabs have a CU to themselves: fp16, 32 tokens, 8 of 64
-        // experts, 768 x 512: 43.2 us with two slabs, 36.2 with one)
         if (n <= 8) return launch_up<TYPE, P == 2 ? 1 : 2, P == 2 ? 8 : 4, FEW, FOLD>(j, s, stream);
-        if constexpr (P == 1) {
-            if (n <= 12) return launch_up<TYPE, 3, 4, FEW, FOLD>(j, s, stream);
-            if (n > 16 && n <= 24) return launch_up<TYPE, 3, 8, FEW, FOLD>(j, s, stream);
-        }
+        if constexpr (P == 1 && !FOLD)
+            if (n > 24) return launch_up<TYPE, 4, 8, FEW, FOLD>(j, s, stream);
     }
-    if constexpr (P == 1)
-        if (n > 16) return launch_up<TYPE, 4, 8, FEW, FOLD>(j, s, stream);
-    if constexpr (FEW)
-        if (n <= 8) return launch_up<TYPE, 1, 8, FEW, FOLD>(j, s, stream);
     return launch_up<TYPE, 2, 8, FEW, FOLD>(j, s, stream);
 }
 
@@ -568,17 +575,20 @@ hipError_t launch_down(MxMoeJob &j, Scratch &s, hipStream_t stream) {
                            dim3(kThinThreads), params, bytes, stream);
 }
 
-// Unfolded, three pieces of more than one slab take a CU to themselves: beyond
-// four slabs K goes in runs of eight past two workgroups on a CU (the layer for 48
-// tokens, 8 of 128 experts, 4096 x 1536, takes 265 us so, 278 with two slabs a wave; 20 tokens, 2 of 16, 4096 x 4096: 106 against 114; 24 tokens, 4 of
-// 16, 2048 x 2560: 55.6 against 58.3).
+// The same.  Unfolded, three pieces of more than one slab take a CU to themselves:
+// beyond two slabs K goes in runs of eight past two workgroups on a CU (48 tokens, 8
+// of 128 experts, 4096 x 1536 bf16: 265 us so, 278 with two slabs a wave; 20 tokens,
+// 2 of 16, 4096 x 4096: 106 against 114; 32 tokens, 8 of 64, 2048 x 512: 43.5 against
+// 45.7).  Folded, against eight waves of three slabs for every length, 4 tokens, 8 of
+// 64 experts of hidden 2048: inner 128 19.6 / 30.7 us, 256 21.8 / 32.2, 512 25.9 /
+// 35.6, 768 35.4 / 38.5, 1024 34.9 / 41.2, 2048 56.0 / 59.6, 4096 90.9 / 100.8.
 template <bool FOLD>
 hipError_t launch_down_slabs(MxMoeJob &j, Scratch &s, hipStream_t stream) {
     const int n = mx_slabs(j.inner);
     if (n <= 1) return launch_down<1, 1, FOLD>(j, s, stream);
     if (n <= 2) return launch_down<1, 2, FOLD>(j, s, stream);
-    if (n <= 4) return launch_down<2, 2, FOLD>(j, s, stream);
     if constexpr (FOLD) {
+        if (n <= 4) return launch_down<2, 2, FOLD>(j, s, stream);
         if (n <= 6) return launch_down<3, 2, FOLD>(j, s, stream);
         if (n <= 8) return launch_down<2, 4, FOLD>(j, s, stream);
         if (n <= 16) return launch_down<4, 4, FOLD>(j, s, stream);

@@ -101,20 +101,13 @@ def up_instance(type, tokens, top, hidden):
     n = slabs(hidden)
 
     def shape():
-        if not few:
-            if n <= 2:
-                return 1, 2
-            if n <= 4:
-                return 1, 4
-            if n <= 8:
-                return (1, 8) if p == 2 else (2, 4)
-            if p == 1 and n <= 12:
-                return 3, 4
-            if p == 1 and 16 < n <= 24:
-                return 3, 8
-        if p == 1 and n > 16:
-            return 4, 8
-        return (2, 8) if n > 8 else (1, 8)
+        if few:
+            return (1, 8) if n <= 8 else (4, 8) if p == 1 and n > 16 else (2, 8)
+        if n <= 4:
+            return (1, 2) if n <= 2 else (1, 4)
+        if n <= 8:
+            return (1, 8) if p == 2 else (2, 4)
+        return (4, 8) if type == BF16 and n > 24 else (2, 8)
 
     return (type, *shape(), int(few), int(fold))
 
@@ -128,10 +121,10 @@ def down_instance(tokens, top, inner):
         return 1, 1, int(fold)
     if n <= 2:
         return 1, 2, int(fold)
-    if n <= 4:
-        return 2, 2, int(fold)
     if not fold:
         return 1, 8, 0
+    if n <= 4:
+        return 2, 2, 1
     return (3, 2, 1) if n <= 6 else (2, 4, 1) if n <= 8 else (4, 4, 1) if n <= 16 else (4, 8, 1) if n > 24 else (3, 8, 1)
 
 
