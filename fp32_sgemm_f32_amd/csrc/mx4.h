@@ -119,7 +119,7 @@ hipError_t launch_mx4_quantize(const MxQuantJob &j, hipStream_t s);
 hipError_t launch_mx4_quantize_two(const MxQuantJob &j, const MxQuantJob &k, hipStream_t s);
 hipError_t launch_mx4_dequantize(const MxDequantJob &j, hipStream_t s);
 hipError_t launch_mx4_gemm(const MxGemmJob &j, int num_cus, hipStream_t s);
-// Two products, the second with a result in fp32; in one launch if both are small.
+// Two products, the second with a result in fp32; in one launch where both take the same tiles.
 hipError_t launch_mx4_gemm_two(const MxGemmJob &j, const MxGemmJob &k, int num_cus, hipStream_t s);
 
 }  // namespace sgemm

@@ -449,9 +449,13 @@ Kind kind_of(const MxGemmJob &j, int num_cus) {
         return mx_slabs(j.K) % 2 == 0 ? k256 : k256Odd;
     if (tiles(128) >= num_cus) return k128;
     // With one tile for a CU at most, a deep ring hides the memory's latency
-    // (64 x 8192 x 8192: 13.0 us against 21.5); with more, further workgroups
-    // do (1111 x 4097 x 2050: 19.9 against 18.5).
-    return tiles(64) <= num_cus ? k64Deep : k64;
+    // (64 x 8192 x 8192: 13.0 us against 21.5).  Two deep rings fit on a CU: up to
+    // as many tiles they pay for long K (300 x 4096 x 16384: 25.9 against 38.4, 1111
+    // x 1500 x 4096: 10.5 against 12.9, 512 x 4096 x 4096: the same; but 300 x 4096 x
+    // 1024: 6.3 against 6.1).  With more, further workgroups hide it (333 x 6000 x
+    // 1536: 10.2 against 8.2).
+    const bool deep = tiles(64) <= num_cus || (tiles(64) <= 2 * num_cus && mx_slabs(j.K) >= 32);
+    return deep ? k64Deep : k64;
 }
 
 template <int TYPE>

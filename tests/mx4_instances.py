@@ -39,7 +39,8 @@ def gemm_tile(m, n, k, cus=CUS):
         return T256 if slabs(k) % 2 == 0 else T256_ODD
     if tiles(m, n, 128) >= cus:
         return T128
-    return T64_DEEP if tiles(m, n, 64) <= cus else T64
+    small = tiles(m, n, 64)
+    return T64_DEEP if small <= cus or small <= 2 * cus and slabs(k) >= 32 else T64
 
 
 def gemm_pair(m, n, k, cus=CUS):
@@ -56,7 +57,7 @@ GEMMS = {
     (4090, 4093, 1000): T256, (4090, 4093, 1100): T256_ODD, (4090, 4093, 1536): T256, (4090, 4093, 640): T256_ODD,
     (2100, 2050, 1000): T128, (2100, 2050, 1100): T128,
     (1111, 1500, 1000): T64, (1111, 1500, 1100): T64,
-    (130, 520, 1536): T64_DEEP, (130, 520, 1700): T64_DEEP,
+    (130, 520, 1536): T64_DEEP, (130, 520, 1700): T64_DEEP, (300, 4093, 4200): T64_DEEP,
 }
 ADDING = [(4090, 4093, 1000), (4090, 4093, 1100), (2100, 2050, 1100), (1111, 1500, 1000), (130, 520, 1700)]
 # (m, n, k) of training steps, by the launch of the backward products.
