@@ -28,7 +28,7 @@
 // the stage of chunk c.
 //
 // Bound, on random codes, by the power the chip may draw: 16384^3 runs at
-// 4.5 PFLOP/s, on zeros at 5.5, and the matrix instructions and barriers of
+// 4.3 to 4.6 PFLOP/s on different chips, on zeros at 5.5, and the matrix instructions and barriers of
 // the loop alone, without loads and LDS reads, at 5.7 and 7.8.
 #include <type_traits>
 

@@ -9,9 +9,9 @@
 // `up` (2 E F x H), D_e rows [e H, e H + H) of `down` (E H x F).
 //
 // Bound by reading the chosen experts once: 3 F H 0.53 bytes each.  48 tokens, 8
-// of 128 experts of 4096 x 1536, bf16: 265 us; `up` reads 816 MB in 140 (5.8
-// TB/s), `down` 408 MB in 115 (3.5).  One token, 8 of 64 experts of 2048 x 768:
-// 16.7 us in a graph, latencies one after another.
+// of 128 experts of 4096 x 1536, bf16: 266 us; `up` reads 816 MB in 146 (5.6
+// TB/s), `down` 408 MB in 113 (3.6).  One token, 8 of 64 experts of 2048 x 768:
+// 17.5 us in a graph, latencies one after another.
 //
 // Logits are summed in 64 bits: which expert is chosen must not hang on the
 // order of a sum.  The inner activations enter the second product as three
@@ -27,7 +27,7 @@
 //   down_few  a workgroup takes 16 rows of the output and all choices: its
 //             waves share the (choice, slab) list evenly and add p_e times
 //             their part into sums of their own, added in wave order
-// (2 tokens, 8 of 64 experts of 2048 x 768: 25.0 us so, 32.6 by the five below;
+// (2 tokens, 8 of 64 experts of 2048 x 768: 25.1 us so, 29.1 by the five below;
 // 4 tokens, before folding, 45 against 36.)
 // More: five.
 //   logits, choose

@@ -175,8 +175,10 @@ __global__ __launch_bounds__(512) void quant_tile_kernel(MxQuantJob j0, MxQuantJ
 // Back to floats.  A workgroup takes one run of a row, a lane 16 bytes of it,
 // stored past the caches.  Workgroups side by side run on different XCDs, and
 // a line that two of them write part of costs memory a read: the fewer, longer
-// runs, the better (8191 x 16388 and 16388 x 8191 floats: 104 and 89 us, with
-// runs of 1 KiB over 8 rows 143 and 139; a fill of as many bytes takes 81).
+// runs, the better (8191 x 16388 and 16388 x 8191 floats, each called over and
+// over: 108 and 99 us, with runs of 1 KiB over 8 rows 143 and 139; a fill of as
+// many bytes takes 80.  Behind the quantisation, whose results and input fill the
+// caches: 125 and 134).
 template <int TYPE>
 __global__ __launch_bounds__(kDequantLanes) void dequant_kernel(MxDequantJob j) {
     typedef typename MxType<TYPE>::T T;
