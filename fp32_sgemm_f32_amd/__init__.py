@@ -8,7 +8,10 @@ hold device memory and to name the current HIP stream.
 import ctypes
 import os
 
+from . import i8 as _i8
 from . import mx4 as _mx4
+from .i8 import I8, i8_dequantize, i8_gemm, i8_linear, i8_quantize  # noqa: F401
+from .i8 import i8_swiglu_backward, i8_swiglu_forward, i8_train_backward, i8_train_forward  # noqa: F401
 from .mx4 import Mx4, mx4_dequantize, mx4_gemm, mx4_quantize, mx4_quantize_both  # noqa: F401
 from .mx4 import mx4_linear, mx4_moe, mx4_train_backward, mx4_train_forward  # noqa: F401
 
@@ -166,6 +169,7 @@ def library():
     lib.sgemm_f32_release.restype = i
     lib.sgemm_f32_release.argtypes = []
     _mx4._bind(lib)
+    _i8._bind(lib)
     _lib = lib
     return lib
 

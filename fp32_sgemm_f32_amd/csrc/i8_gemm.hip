@@ -1,0 +1,338 @@
+// C = alpha A B^T + beta C for two matrices in the 8-bit integer format (A: M x
+// K, B: N x K, a scale for each row), and C = alpha A B for B stored K x N
+// (`down`), on v_mfma_i32_32x32x32_i8: exact 32-bit sums, scales in the
+// epilogue.
+//
+// A workgroup computes a BM x BN tile.  Chunks of 128 along K go from global
+// memory straight into LDS, through a ring of S stages; the buffer resources
+// end where the matrix does, so what lies beyond reads as zeros and nothing is
+// masked (A's rows are padded with zeros in the format itself; down B's rows
+// beyond K meet those).
+//
+// LDS of a stage: A's rows (128 bytes), then B's rows (128 bytes of a column of
+// C), or, down, 128 rows of BN bytes.  A lane's operand is 16 bytes along K.
+// - Rows along K: quad q (16 bytes) of a row is kept at q ^ swz(row), so that
+//   the 32 rows of an operand read fall on different banks.  B's rows are kept
+//   in the order that gives a lane FN adjacent columns of C (fragment f holds
+//   columns FN l + f): stores are FN values wide.
+// - Down: ds_read_b64_tr_b8 reads 8 rows x 16 bytes across 16 lanes and gives
+//   each of them a column's 8 bytes; two make an operand.  Quad q of row k is
+//   kept at q ^ swz_down(k): the 8 rows x 32 columns that half a wave reads lie
+//   in different banks.  A lane's columns are 32 apart.
+//
+// pieces = 2 (down): A's fragments come in pairs, the high and the low bytes of
+// 16-bit whole numbers; a pair's sums are joined as 256 high + low.
+//
+// Ring: before the last step of chunk c, whose operands are in registers by
+// then, the waves meet once (loads of chunk c + 1 landed, LDS reads of chunk c
+// done), read the first operands of chunk c + 1, and load chunk c + S into the
+// stage of chunk c.
+#include "i8.h"
+#include "lds_dma.h"
+
+namespace sgemm {
+namespace {
+
+typedef int i32v2 __attribute__((ext_vector_type(2)));
+typedef int i32v16 __attribute__((ext_vector_type(16)));
+
+constexpr int kChunk = 128;   // of K
+
+struct Args {
+    const int8_t *a;
+    const float *sa;
+    const int8_t *b;
+    const float *sb;
+    void *c;
+    int64_t ldc;
+    int M, N, K;        // M: rows of C
+    int rows_a;         // rows of A (with two pieces more than M)
+    int tiles_m, tiles_n;
+    float alpha, beta;
+};
+
+template <int BM_, int BN_, int WM_, int WN_, int S_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+    static constexpr int NW = WM * WN, NT = 64 * NW;
+    static constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
+    static constexpr int STEPS = kChunk / 32;
+    static constexpr int A_BYTES = BM * kChunk, B_BYTES = BN * kChunk, STAGE = A_BYTES + B_BYTES;
+    static constexpr int A_PW = A_BYTES / 1024 / NW, B_PW = B_BYTES / 1024 / NW, L = A_PW + B_PW;   // loads of a wave per chunk
+    static_assert(A_PW * NW * 1024 == A_BYTES && B_PW * NW * 1024 == B_BYTES, "a chunk's loads split evenly over the waves");
+    static_assert(S * STAGE <= 160 * 1024 && (S - 2) * L < 64 && S >= 2, "LDS and vmcnt budget");
+
+    __device__ __forceinline__ static int swz(int r) { return (r ^ (r >> 3)) & 7; }
+    // Column of the tile that B's LDS row r holds.
+    __device__ __forceinline__ static int b_col(int r) { return r / WTN * WTN + FN * (r % 32) + r % WTN / 32; }
+    // Rows of BN bytes: 256 / BN of them to all banks.
+    __device__ __forceinline__ static int swz_down(int k) { return 2 * ((k / (256 / BN)) & (BN / 32 - 1)); }
+};
+
+// A sum times its row's and its column's scale: the smaller first, which
+// neither overflows nor underflows where the result does not.
+__device__ __forceinline__ float scaled(float sum, float x, float y) {
+    const bool less = x < y;   // (where one is NaN, it comes second)
+    return sum * (less ? x : y) * (less ? y : x);
+}
+
+// The tile of workgroup `block` of the product g.
+template <class TL, int TYPE, bool DOWN, int PIECES>
+__device__ __forceinline__ void compute_tile(const Args &g, int block) {
+    typedef typename MxType<TYPE>::T T;
+    extern __shared__ __attribute__((aligned(1024))) int8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / TL::WN, wn = wave % TL::WN;
+
+    // Workgroup -> tile: each XCD (workgroups w, w + 8, ...) takes a
+    // contiguous run of tiles, which go down columns of 8-row groups.
+    int tm, tn;
+    {
+        const int tiles = g.tiles_m * g.tiles_n, per = tiles >> 3, rest = tiles & 7;
+        const int x = block & 7, y = block >> 3;
+        const int t = x * per + (x < rest ? x : rest) + y;
+        const int group = 8 * g.tiles_n, gi = t / group, first = gi * 8;
+        const int rows = g.tiles_m - first < 8 ? g.tiles_m - first : 8;
+        tm = first + (t - gi * group) % rows;
+        tn = (t - gi * group) / rows;
+    }
+    const int m0 = tm * TL::BM, n0 = tn * TL::BN;
+    const int chunks = (g.K + kChunk - 1) / kChunk;
+    const int64_t rowb = (int64_t)chunks * kChunk;   // bytes of a row along K
+    const int64_t downb = i8_ld(g.N);                // of a row down K
+
+    // Sources of this wave's loads.  The resources end with the tile's last
+    // real row along K; down, with the chunk's last real row.
+    const int am = g.rows_a - m0 < TL::BM ? g.rows_a - m0 : TL::BM, bn = g.N - n0 < TL::BN ? g.N - n0 : TL::BN;
+    i32v4 ra = resource(g.a + m0 * rowb, 0), rb = DOWN ? resource(g.b, 0) : resource(g.b + n0 * rowb, 0);
+    uint32_t va[TL::A_PW], vb[TL::B_PW];
+#pragma unroll
+    for (int i = 0; i < TL::A_PW; ++i) {
+        const int r = (wave * TL::A_PW + i) * 8 + lane / 8;
+        va[i] = (uint32_t)(r * rowb) + 16 * ((lane % 8) ^ TL::swz(r));
+    }
+#pragma unroll
+    for (int i = 0; i < TL::B_PW; ++i) {
+        if constexpr (DOWN) {
+            constexpr int QUADS = TL::BN / 16;
+            const int at = (wave * TL::B_PW + i) * 64 + lane, k = at / QUADS;
+            vb[i] = (uint32_t)(k * downb) + n0 + 16 * ((at % QUADS) ^ TL::swz_down(k));
+        } else {
+            const int r = (wave * TL::B_PW + i) * 8 + lane / 8;
+            vb[i] = (uint32_t)(TL::b_col(r) * rowb) + 16 * ((lane % 8) ^ TL::swz(r));
+        }
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)lds;
+
+    // Loads i = 0 .. L-1 of a chunk, A's first; `next_chunk` moves the
+    // resources on by one chunk.  From the last chunk on they are empty.
+    int lc = 0;   // the chunk that the resources stand at
+    auto limits = [&] {
+        const bool in = lc < chunks;
+        ra[2] = in ? (int)(am * rowb - lc * kChunk) : 0;
+        if constexpr (DOWN) rb[2] = in ? (int)((g.K - lc * kChunk < kChunk ? g.K - lc * kChunk : kChunk) * downb) : 0;
+        else rb[2] = in ? (int)(bn * rowb - lc * kChunk) : 0;
+    };
+    limits();
+    auto load_one = [&](auto ic, int stage) {
+        constexpr int i = decltype(ic)::value;
+        const uint32_t base = lds0 + stage * TL::STAGE;
+        if constexpr (i < TL::A_PW) dma16(ra, va[i], base + (wave * TL::A_PW + i) * 1024);
+        else if constexpr (i < TL::L) dma16(rb, vb[i - TL::A_PW], base + TL::A_BYTES + (wave * TL::B_PW + i - TL::A_PW) * 1024);
+    };
+    auto next_chunk = [&] {
+        ++lc;
+        advance(ra, kChunk);
+        advance(rb, DOWN ? kChunk * downb : kChunk);
+        limits();
+    };
+    auto load_chunk = [&](int stage) {
+        each<0, TL::L>([&](auto i) { load_one(i, stage); });
+        next_chunk();
+    };
+
+    i32v16 acc[TL::FM][TL::FN];
+#pragma unroll
+    for (int i = 0; i < TL::FM; ++i)
+#pragma unroll
+        for (int k = 0; k < TL::FN; ++k)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][k][r] = 0;
+
+    // Operand reads: lane l takes row (down: column) l % 32 of a fragment,
+    // bytes 32 j + 16 (l / 32) + 0 .. 15 of the chunk.
+    const int fr = lane & 31, h = lane >> 5;
+    const int tr_row = 16 * h + ((lane & 15) >> 1);   // down: the row of step 0 that this lane names
+    const int tr_at = tr_row * TL::BN + 8 * (lane & 1);
+    struct Ops {
+        i32v4 a[TL::FM], b[TL::FN];
+    };
+    auto read_ops = [&](Ops &o, int stage, int j) {
+        const int8_t *st = lds + stage * TL::STAGE;
+#pragma unroll
+        for (int i = 0; i < TL::FM; ++i) {
+            const int r = wm * TL::WTM + 32 * i + fr;
+            o.a[i] = *(const i32v4 *)(st + r * kChunk + 16 * ((2 * j + h) ^ TL::swz(r)));
+        }
+#pragma unroll
+        for (int i = 0; i < TL::FN; ++i) {
+            if constexpr (DOWN) {
+                const int quad = (wn * TL::WTN + 32 * i) / 16 + (fr >> 4);
+                typedef __attribute__((address_space(3))) i32v2 *Tr;
+                const int8_t *p = st + TL::A_BYTES + 32 * j * TL::BN + tr_at + 16 * (quad ^ TL::swz_down(tr_row));
+                const i32v2 lo = __builtin_amdgcn_ds_read_tr8_b64_v2i32((Tr)p);
+                const i32v2 hi = __builtin_amdgcn_ds_read_tr8_b64_v2i32((Tr)(p + 8 * TL::BN));
+                o.b[i] = i32v4{lo[0], lo[1], hi[0], hi[1]};
+            } else {
+                const int r = wn * TL::WTN + 32 * i + fr;
+                o.b[i] = *(const i32v4 *)(st + TL::A_BYTES + r * kChunk + 16 * ((2 * j + h) ^ TL::swz(r)));
+            }
+        }
+    };
+    // Products p = 0 .. FM FN - 1 of a matrix step, row by row.
+    auto multiply = [&](const Ops &o, auto pc) {
+        constexpr int i = decltype(pc)::value / TL::FN, k = decltype(pc)::value % TL::FN;
+        acc[i][k] = __builtin_amdgcn_mfma_i32_32x32x32_i8(o.a[i], o.b[k], acc[i][k], 0, 0, 0);
+    };
+    constexpr int NP = TL::FM * TL::FN;
+
+    // Chunks 0 .. S-1 go out, the last of them only in part; from then on
+    // every iteration adds one.  A chunk's loads are spread over the products
+    // of a last step (the first EARLY of them) and of the next chunk's first:
+    // a wave that issues loads back to back waits for the address unit with
+    // its products behind it.  Past the last chunk nothing is in range, but
+    // the loads are issued all the same (they leave zeros): the waits count
+    // them.
+    constexpr int HEAD = NP / 4 > 0 ? NP / 4 : 1;
+    constexpr int EARLY = TL::L * (NP - HEAD) / (2 * NP - HEAD);
+    for (int c = 0; c < TL::S - 1; ++c) load_chunk(c);
+    each<0, EARLY>([&](auto i) { load_one(i, TL::S - 1); });
+    meet<(TL::S - 2) * TL::L + EARLY>();
+    Ops o[2];
+    read_ops(o[0], 0, 0);
+    int stage = 0, freed = TL::S - 1;
+    for (int c = 0; c < chunks; ++c) {
+        const int next = stage + 1 == TL::S ? 0 : stage + 1;
+        each<0, TL::STEPS - 1>([&](auto jc) {
+            constexpr int j = decltype(jc)::value;
+            read_ops(o[(j + 1) & 1], stage, j + 1);
+            fence_order();
+            each<0, NP>([&](auto p) {
+                multiply(o[j & 1], p);
+                if constexpr (j == 0) {
+                    constexpr int first = EARLY + p * (TL::L - EARLY) / NP, end = EARLY + (p + 1) * (TL::L - EARLY) / NP;
+                    each<first, end>([&](auto i) { load_one(i, freed); });
+                    fence_order();
+                }
+            });
+            if constexpr (j == 0) next_chunk();
+            fence_order();
+        });
+        // The last step's operands are in registers once this wave has met
+        // the others; behind its products go the next chunk's first operands
+        // and the first loads into the stage that is free now.
+        meet<(TL::S - 2) * TL::L>();
+        constexpr int j = TL::STEPS - 1;
+        each<0, HEAD>([&](auto p) { multiply(o[j & 1], p); });
+        fence_order();
+        read_ops(o[0], next, 0);
+        fence_order();
+        each<HEAD, NP>([&](auto p) {
+            multiply(o[j & 1], p);
+            constexpr int first = (p - HEAD) * EARLY / (NP - HEAD), end = (p - HEAD + 1) * EARLY / (NP - HEAD);
+            each<first, end>([&](auto i) { load_one(i, stage); });
+            fence_order();
+        });
+        freed = stage;
+        stage = next;
+    }
+    // Loads still in flight write this workgroup's LDS: let them land.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+
+    // Lane l holds columns FN (l % 32) + 0 .. FN-1 of its wave's tile (down:
+    // l % 32 + 32 k), rows 8 (r / 4) + 4 (l / 32) + r % 4 of each fragment.
+    constexpr int APART = DOWN ? 32 : 1;   // columns between a lane's
+    const int col = n0 + wn * TL::WTN + (DOWN ? 1 : TL::FN) * fr;
+    const bool wide = !DOWN && col + TL::FN <= g.N;
+    float sb[TL::FN];
+#pragma unroll
+    for (int k = 0; k < TL::FN; ++k) sb[k] = g.sb && col + APART * k < g.N ? g.sb[col + APART * k] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < TL::FM; i += PIECES)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = (m0 + wm * TL::WTM + 32 * i) / PIECES + 8 * (r / 4) + 4 * h + r % 4;
+            if (row >= g.M) continue;
+            const float sa = g.sa ? g.sa[row] : 1.0f;
+            float v[TL::FN];
+#pragma unroll
+            for (int k = 0; k < TL::FN; ++k) {
+                float sum = (float)acc[i][k][r];
+                if constexpr (PIECES == 2) sum = fmaf(256.0f, sum, (float)acc[i + 1][k][r]);
+                v[k] = g.alpha * scaled(sum, sa, sb[k]);
+            }
+            T *p = (T *)g.c + row * g.ldc + col;
+            if (wide) {
+                Vec<TL::FN, T> out;
+                if (g.beta != 0.0f) {
+                    const Vec<TL::FN, T> old = *(const Vec<TL::FN, T> *)p;
+#pragma unroll
+                    for (int k = 0; k < TL::FN; ++k) v[k] += g.beta * MxType<TYPE>::load(&old.v[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < TL::FN; ++k) out.v[k] = MxType<TYPE>::from(v[k]);
+                store<TL::BM >= 256>((Vec<TL::FN, T> *)p, out);
+            } else {
+#pragma unroll
+                for (int k = 0; k < TL::FN; ++k)
+                    if (col + APART * k < g.N) {
+                        if (g.beta != 0.0f) v[k] += g.beta * MxType<TYPE>::load(p + APART * k);
+                        p[APART * k] = MxType<TYPE>::from(v[k]);
+                    }
+            }
+        }
+}
+
+template <class TL, int TYPE, bool DOWN, int PIECES>
+__global__ __launch_bounds__(TL::NT, 1) void i8_gemm_kernel(Args g) {
+    compute_tile<TL, TYPE, DOWN, PIECES>(g, blockIdx.x);
+}
+
+typedef Tile<256, 256, 2, 4, 2> T256;
+typedef Tile<128, 128, 2, 4, 2> T128;
+typedef Tile<64, 64, 1, 4, 2> T64;
+
+template <class TL>
+Args arguments(const I8GemmJob &j) {
+    const int rows_a = j.pieces == 2 ? (int)i8_piece_rows(j.M) : j.M;
+    return Args{j.a, j.sa, j.b, j.sb, j.c, j.ldc, j.M, j.N, j.K, rows_a, (int)(((int64_t)rows_a + TL::BM - 1) / TL::BM),
+                (int)(((int64_t)j.N + TL::BN - 1) / TL::BN), j.alpha, j.beta};
+}
+
+template <class TL, int TYPE, bool DOWN, int PIECES>
+hipError_t launch_tile(const I8GemmJob &j, hipStream_t s) {
+    Args g = arguments<TL>(j);
+    void *params[] = {&g};
+    return hipLaunchKernel((const void *)i8_gemm_kernel<TL, TYPE, DOWN, PIECES>, dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(TL::NT), params,
+                           TL::S * TL::STAGE, s);
+}
+
+template <int TYPE, bool DOWN, int PIECES>
+hipError_t launch_form(const I8GemmJob &j, int num_cus, hipStream_t s) {
+    return launch_tile<T128, TYPE, DOWN, PIECES>(j, s);
+}
+
+}  // namespace
+
+hipError_t launch_i8_gemm(const I8GemmJob &j, int num_cus, hipStream_t s) {
+    if (j.pieces == 2) return launch_form<SGEMM_TYPE_F32, true, 2>(j, num_cus, s);
+    switch (j.type) {
+    case SGEMM_TYPE_F32: return j.down ? launch_form<SGEMM_TYPE_F32, true, 1>(j, num_cus, s) : launch_form<SGEMM_TYPE_F32, false, 1>(j, num_cus, s);
+    case SGEMM_TYPE_BF16: return j.down ? launch_form<SGEMM_TYPE_BF16, true, 1>(j, num_cus, s) : launch_form<SGEMM_TYPE_BF16, false, 1>(j, num_cus, s);
+    case SGEMM_TYPE_F16: return j.down ? launch_form<SGEMM_TYPE_F16, true, 1>(j, num_cus, s) : launch_form<SGEMM_TYPE_F16, false, 1>(j, num_cus, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace sgemm

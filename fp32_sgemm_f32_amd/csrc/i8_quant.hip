@@ -1,0 +1,288 @@
+// Quantisation to 8-bit integers, by rows, by columns (transposed on the way)
+// and by groups of 128 columns, and back.
+//
+// A row's scale follows from its largest magnitude m: s = max(m / 127, 2^-126),
+// and x is held as the whole number nearest to x / s.  m is taken on the bits
+// below the sign, so that one integer maximum finds NaN and infinities too.
+//
+// Gradients that go into an integer product are first multiplied by the scales
+// that stand along the product's sum (fold).  By columns they are held in 16
+// bits: n = 256 h + l with h and l signed bytes, the two rows of a column 32
+// apart in a matrix of twice the rows (rows 64 b + i hold h, 64 b + 32 + i l of
+// column 32 b + i), which is how a fragment of a matrix instruction takes them.
+//
+// Bound by HBM.
+#include "i8.h"
+
+namespace sgemm {
+namespace {
+
+constexpr int kKeep = 4;   // eights of a row that a lane keeps in registers between the two passes
+
+// WAVES waves take a row; four rows a workgroup where that is one.
+template <int TYPE, int WAVES>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void i8_rows_kernel(I8RowsJob j0, I8RowsJob j1, int64_t blocks0) {
+    constexpr int T = 64 * WAVES, ROWS = WAVES == 1 ? 4 : 1;
+    typedef typename MxType<TYPE>::T E;
+    const bool second = blockIdx.x >= blocks0;
+    const I8RowsJob &j = second ? j1 : j0;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, t = WAVES == 1 ? lane : (int)threadIdx.x;
+    const int64_t row = (blockIdx.x - (second ? blocks0 : 0)) * ROWS + (WAVES == 1 ? wave : 0);
+    if (row >= j.rows) return;
+    const E *x = (const E *)j.x + row * j.ldx;
+    const int ld = (int)i8_ld(j.cols);
+    const auto load = [&](int c, float (&v)[8]) {
+        mx_load_edge8<TYPE>(x, c, j.cols, v);
+        if (j.fold) {
+            float w[8];
+            mx_load_edge8<SGEMM_TYPE_F32>(j.fold, c, j.cols, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= w[i];
+        }
+    };
+    float v[kKeep][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) load(8 * (t + T * i), v[i]);
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) m = i8_max(m, i8_max8(v[i]));
+    for (int c = 8 * (t + T * kKeep); c < j.cols; c += 8 * T) {
+        float w[8];
+        load(c, w);
+        m = i8_max(m, i8_max8(w));
+    }
+    m = i8_max16(m);
+    m = i8_max(m, __shfl_xor(m, 16, 64));
+    m = i8_max(m, __shfl_xor(m, 32, 64));
+    if constexpr (WAVES > 1) {
+        __shared__ uint32_t part[WAVES];
+        if (lane == 0) part[wave] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) m = i8_max(m, part[i]);
+    }
+    const float s = i8_scale(m, kI8Levels), inv = 1.0f / s;
+    int8_t *q = j.q + row * ld;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+        const int c = 8 * (t + T * i);
+        if (c < ld) *(uint2 *)(q + c) = i8_nearest8(v[i], s, inv);
+    }
+    for (int c = 8 * (t + T * kKeep); c < ld; c += 8 * T) {
+        float w[8];
+        load(c, w);
+        *(uint2 *)(q + c) = i8_nearest8(w, s, inv);
+    }
+    if (t == 0) j.s[row] = s;
+}
+
+// ---- by columns ----
+
+constexpr int kMostParts = 64;
+inline __host__ __device__ int rows_of_part(int rows) {
+    const int per = (rows + kMostParts - 1) / kMostParts;
+    return per > 64 ? per : 64;
+}
+inline __host__ __device__ int parts_of(int rows) { return (rows + rows_of_part(rows) - 1) / rows_of_part(rows); }
+
+// The largest magnitudes of 128 columns in a part of the rows.
+template <int TYPE>
+__global__ __launch_bounds__(256) void i8_part_kernel(I8ColsJob j) {
+    typedef typename MxType<TYPE>::T E;
+    __shared__ uint32_t most[16][128];
+    const int c = 8 * (threadIdx.x & 15), r = threadIdx.x >> 4, c0 = blockIdx.x * 128;
+    const int per = rows_of_part(j.rows), begin = blockIdx.y * per, end = begin + per < j.rows ? begin + per : j.rows;
+    uint32_t m[8] = {};
+#pragma unroll 4
+    for (int row = begin + r; row < end; row += 16) {
+        float v[8];
+        mx_load_edge8<TYPE>((const E *)j.x + row * j.ldx, c0 + c, j.cols, v);
+        const float f = j.fold ? j.fold[row] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = i8_max(m[i], i8_magnitude(v[i] * f));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most[r][c + i] = m[i];
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        uint32_t all = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) all = i8_max(all, most[i][threadIdx.x]);
+        j.part[(int64_t)blockIdx.y * i8_ld(j.cols) + c0 + threadIdx.x] = all;
+    }
+}
+
+// 128 columns x 128 rows, written as rows.
+template <int TYPE, int PIECES>
+__global__ __launch_bounds__(256) void i8_cols_kernel(I8ColsJob j) {
+    typedef typename MxType<TYPE>::T E;
+    __shared__ uint32_t tile[PIECES][128][33];   // 128 bytes of a column; one word more, so that columns start on other banks
+    __shared__ uint32_t most[128];
+    __shared__ float scale[128], inverse[128];
+    const int tid = threadIdx.x, c0 = blockIdx.x * 128, r0 = blockIdx.y * 128, ld = (int)i8_ld(j.rows);
+    {
+        const int c = tid & 127, parts = parts_of(j.rows);
+        uint32_t m = 0;
+#pragma unroll 8
+        for (int p = tid >> 7; p < parts; p += 2) m = i8_max(m, j.part[p * i8_ld(j.cols) + c0 + c]);
+        if (tid < 128) most[c] = m;
+        __syncthreads();
+        if (tid >= 128) {
+            const float s = i8_scale(i8_max(m, most[c]), PIECES == 2 ? kI8Levels16 : kI8Levels);
+            scale[c] = s;
+            inverse[c] = 1.0f / s;
+            if (blockIdx.y == 0 && c0 + c < j.cols) j.s[c0 + c] = s;
+        }
+        __syncthreads();
+    }
+    const int c = 8 * (tid & 15);
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+        const int four = (tid >> 4) + 16 * it;   // four rows, one word of a column
+        float v[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = r0 + 4 * four + k;
+            const bool real = row < j.rows;
+            mx_load_edge8<TYPE>((const E *)j.x + (real ? row : 0) * j.ldx, c0 + c, real ? j.cols : 0, v[k]);
+            const float f = j.fold && real ? j.fold[row] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[k][i] *= f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t high = 0, low = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int n = i8_nearest(v[k][i], scale[c + i], inverse[c + i]);
+                if constexpr (PIECES == 2) high |= ((uint32_t)((n + 128) >> 8) & 255u) << (8 * k);
+                low |= ((uint32_t)n & 255u) << (8 * k);
+            }
+            if constexpr (PIECES == 2) tile[0][c + i][four] = high;
+            tile[PIECES - 1][c + i][four] = low;
+        }
+    }
+    __syncthreads();
+    for (int i = tid >> 5; i < PIECES * 128; i += 8) {
+        const int piece = i >> 7, n = c0 + (i & 127);
+        if (n >= j.cols) continue;
+        const int64_t row = PIECES == 2 ? (int64_t)(n >> 5) * 64 + piece * 32 + (n & 31) : n;
+        *(uint32_t *)(j.q + row * ld + r0 + 4 * (tid & 31)) = tile[piece][i & 127][tid & 31];
+    }
+}
+
+// ---- by groups, and back ----
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void i8_groups_kernel(I8GroupsJob j) {
+    const int chunks = (int)(i8_ld(j.cols) / 8);
+    const I8Place at = i8_place(chunks, 256);
+    const bool real = at.row < j.rows;
+    float v[8];
+    mx_load_edge8<TYPE>((const typename MxType<TYPE>::T *)j.x + (real ? at.row : 0) * j.ldx, at.c, real ? j.cols : 0, v);
+    const float s = i8_scale(i8_max16(i8_max8(v)), kI8Levels), inv = 1.0f / s;
+    if (!real) return;
+    *(uint2 *)(j.q + (at.row * chunks) * 8 + at.c) = i8_nearest8(v, s, inv);
+    if ((threadIdx.x & 15) == 0) j.s[at.row * (chunks / 16) + at.c / 128] = s;
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void i8_back_kernel(I8BackJob j) {
+    const int chunks = (j.cols + 7) / 8;
+    const I8Place at = i8_place(chunks, 256);
+    if (at.row >= j.rows) return;
+    const int64_t ld = i8_ld(j.cols);
+    float v[8];
+    i8_values8(*(const uint2 *)(j.q + at.row * ld + at.c), j.s[j.group ? at.row * (ld / 128) + at.c / 128 : at.row], v);
+    i8_store8<TYPE>((typename MxType<TYPE>::T *)j.y + at.row * j.ldy, at.c, j.cols, v);
+}
+
+// ---- launches ----
+
+template <int TYPE, int WAVES>
+hipError_t rows(const I8RowsJob &first, const I8RowsJob &second, hipStream_t s) {
+    constexpr int ROWS = WAVES == 1 ? 4 : 1;
+    I8RowsJob j = first, k = second;
+    int64_t head = ((int64_t)j.rows + ROWS - 1) / ROWS;
+    const int64_t all = head + ((int64_t)k.rows + ROWS - 1) / ROWS;
+    void *params[] = {&j, &k, &head};
+    return hipLaunchKernel((const void *)i8_rows_kernel<TYPE, WAVES>, dim3((unsigned)all), dim3(WAVES == 1 ? 256 : 64 * WAVES), params, 0, s);
+}
+
+// Few enough waves that a lane keeps its part of a row.
+template <int TYPE>
+hipError_t rows_type(const I8RowsJob &j, const I8RowsJob &k, hipStream_t s) {
+    const int cols = j.cols > k.cols ? j.cols : k.cols;
+    if (cols <= 64 * 8 * kKeep) return rows<TYPE, 1>(j, k, s);
+    if (cols <= 256 * 8 * kKeep) return rows<TYPE, 4>(j, k, s);
+    return rows<TYPE, 16>(j, k, s);
+}
+
+template <int TYPE>
+hipError_t cols_type(const I8ColsJob &job, hipStream_t s) {
+    I8ColsJob j = job;
+    void *params[] = {&j};
+    const unsigned across = (unsigned)(i8_ld(j.cols) / 128), down = (unsigned)(i8_ld(j.rows) / 128);
+    const hipError_t e = hipLaunchKernel((const void *)i8_part_kernel<TYPE>, dim3(across, (unsigned)parts_of(j.rows)), dim3(256), params, 0, s);
+    if (e != hipSuccess) return e;
+    return hipLaunchKernel(j.pieces == 2 ? (const void *)i8_cols_kernel<TYPE, 2> : (const void *)i8_cols_kernel<TYPE, 1>, dim3(across, down),
+                           dim3(256), params, 0, s);
+}
+
+template <int TYPE>
+hipError_t groups_type(const I8GroupsJob &job, hipStream_t s) {
+    I8GroupsJob j = job;
+    void *params[] = {&j};
+    return hipLaunchKernel((const void *)i8_groups_kernel<TYPE>, dim3(i8_grid(j.rows, i8_ld(j.cols) / 8, 256)), dim3(256), params, 0, s);
+}
+
+template <int TYPE>
+hipError_t back_type(const I8BackJob &job, hipStream_t s) {
+    I8BackJob j = job;
+    void *params[] = {&j};
+    return hipLaunchKernel((const void *)i8_back_kernel<TYPE>, dim3(i8_grid(j.rows, (j.cols + 7) / 8, 256)), dim3(256), params, 0, s);
+}
+
+}  // namespace
+
+int64_t i8_part_bytes(int rows, int cols) { return rows > 0 ? parts_of(rows) * i8_ld(cols) * 4 : 0; }
+
+#define I8_BY_TYPE(type, call)                          \
+    switch (type) {                                     \
+    case SGEMM_TYPE_F32: return call(SGEMM_TYPE_F32);   \
+    case SGEMM_TYPE_BF16: return call(SGEMM_TYPE_BF16); \
+    case SGEMM_TYPE_F16: return call(SGEMM_TYPE_F16);   \
+    default: return hipErrorInvalidValue;               \
+    }
+
+hipError_t launch_i8_rows_two(const I8RowsJob &j, const I8RowsJob &k, hipStream_t s) {
+#define CALL(T) rows_type<T>(j, k, s)
+    I8_BY_TYPE(j.type, CALL)
+#undef CALL
+}
+
+hipError_t launch_i8_rows(const I8RowsJob &j, hipStream_t s) {
+    I8RowsJob none = j;
+    none.rows = 0;
+    return launch_i8_rows_two(j, none, s);
+}
+
+hipError_t launch_i8_cols(const I8ColsJob &j, hipStream_t s) {
+#define CALL(T) cols_type<T>(j, s)
+    I8_BY_TYPE(j.type, CALL)
+#undef CALL
+}
+
+hipError_t launch_i8_groups(const I8GroupsJob &j, hipStream_t s) {
+#define CALL(T) groups_type<T>(j, s)
+    I8_BY_TYPE(j.type, CALL)
+#undef CALL
+}
+
+hipError_t launch_i8_back(const I8BackJob &j, hipStream_t s) {
+#define CALL(T) back_type<T>(j, s)
+    I8_BY_TYPE(j.type, CALL)
+#undef CALL
+}
+
+}  // namespace sgemm

@@ -1,0 +1,89 @@
+// The gated activation H = silu(G) * U of GU = [G, U], with an 8-bit checkpoint
+// of G and U in groups of 128 columns, and its gradient from that checkpoint:
+//
+//     p = 1 / (1 + exp(-g))     h = g p u
+//     dg = dh u p (1 + g (1 - p))     du = dh g p
+//
+// with the checkpoint's g and u in the gradient.  In fp32, rounded once.
+//
+// Bound by HBM: a lane takes eight columns of G and the same of U, so that
+// every value is read and written once.
+#include "i8.h"
+
+namespace sgemm {
+namespace {
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void i8_swiglu_forward_kernel(I8SwigluJob j) {
+    typedef typename MxType<TYPE>::T E;
+    const int chunks = (int)(i8_ld(j.inner) / 8);
+    const I8Place at = i8_place(chunks, 256);
+    const bool real = at.row < j.rows;
+    const E *x = (const E *)j.x + (real ? at.row : 0) * j.ldx;
+    float g[8], u[8], h[8];
+    mx_load_edge8<TYPE>(x, at.c, real ? j.inner : 0, g);
+    mx_load_edge8<TYPE>(x + j.inner, at.c, real ? j.inner : 0, u);
+    const float sg = i8_scale(i8_max16(i8_max8(g)), kI8Levels), su = i8_scale(i8_max16(i8_max8(u)), kI8Levels);
+    if (!real) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = g[i] / (1.0f + expf(-g[i])) * u[i];
+    const int64_t q = at.row * chunks * 8 + at.c;
+    *(uint2 *)(j.gq + q) = i8_nearest8(g, sg, 1.0f / sg);
+    *(uint2 *)(j.uq + q) = i8_nearest8(u, su, 1.0f / su);
+    if ((threadIdx.x & 15) == 0) j.gs[q / 128] = sg, j.us[q / 128] = su;
+    i8_store8<TYPE>((E *)j.y + at.row * j.ldy, at.c, j.inner, h);
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void i8_swiglu_backward_kernel(I8SwigluJob j) {
+    typedef typename MxType<TYPE>::T E;
+    const int chunks = (j.inner + 7) / 8;
+    const I8Place at = i8_place(chunks, 256);
+    if (at.row >= j.rows) return;
+    const int64_t q = at.row * i8_ld(j.inner) + at.c;
+    float g[8], u[8], d[8], dg[8], du[8];
+    mx_load_edge8<TYPE>((const E *)j.x + at.row * j.ldx, at.c, j.inner, d);
+    i8_values8(*(const uint2 *)(j.gq + q), j.gs[q / 128], g);
+    i8_values8(*(const uint2 *)(j.uq + q), j.us[q / 128], u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // 1 - p as it is: for large g it is exp(-g) p, of which the difference would lose the last bits.
+        const float e = expf(-g[i]), p = 1.0f / (1.0f + e), rest = g[i] > 0.0f ? e * p : 1.0f - p;
+        dg[i] = d[i] * u[i] * p * (1.0f + g[i] * rest);
+        du[i] = d[i] * (g[i] * p);
+    }
+    E *y = (E *)j.y + at.row * j.ldy;
+    i8_store8<TYPE>(y, at.c, j.inner, dg);
+    i8_store8<TYPE>(y + j.inner, at.c, j.inner, du);
+}
+
+const void *forward_kernel(int type) {
+    switch (type) {
+    case SGEMM_TYPE_F32: return (const void *)i8_swiglu_forward_kernel<SGEMM_TYPE_F32>;
+    case SGEMM_TYPE_BF16: return (const void *)i8_swiglu_forward_kernel<SGEMM_TYPE_BF16>;
+    default: return (const void *)i8_swiglu_forward_kernel<SGEMM_TYPE_F16>;
+    }
+}
+const void *backward_kernel(int type) {
+    switch (type) {
+    case SGEMM_TYPE_F32: return (const void *)i8_swiglu_backward_kernel<SGEMM_TYPE_F32>;
+    case SGEMM_TYPE_BF16: return (const void *)i8_swiglu_backward_kernel<SGEMM_TYPE_BF16>;
+    default: return (const void *)i8_swiglu_backward_kernel<SGEMM_TYPE_F16>;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_i8_swiglu_forward(const I8SwigluJob &job, hipStream_t s) {
+    I8SwigluJob j = job;
+    void *params[] = {&j};
+    return hipLaunchKernel(forward_kernel(j.type), dim3(i8_grid(j.rows, i8_ld(j.inner) / 8, 256)), dim3(256), params, 0, s);
+}
+
+hipError_t launch_i8_swiglu_backward(const I8SwigluJob &job, hipStream_t s) {
+    I8SwigluJob j = job;
+    void *params[] = {&j};
+    return hipLaunchKernel(backward_kernel(j.type), dim3(i8_grid(j.rows, (j.inner + 7) / 8, 256)), dim3(256), params, 0, s);
+}
+
+}  // namespace sgemm

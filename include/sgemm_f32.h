@@ -505,6 +505,126 @@ int sgemm_f32_mx4_moe(int tokens, int hidden, int inner, int experts, int top, i
 int sgemm_f32_mx4_moe_scratch(int tokens, int hidden, int inner, int experts, int top,
                               int type, long long *bytes);
 
+/*
+ * 8-bit integer matrices.
+ *
+ * A matrix of `rows` x `cols` values is two device arrays:
+ *   values  rows x kp signed bytes, kp = cols rounded up to 128; zeros beyond
+ *           cols
+ *   scales  floats: one for each row (group = 0), or one for each 128 columns
+ *           of a row, rows x kp / 128 (group = SGEMM_I8_GROUP)
+ * and stands for value * scale.  values must be 16-byte aligned, scales
+ * 4-byte aligned.  The products rely on the zeros beyond cols
+ * (sgemm_f32_i8_quantize writes them) and on values in [-127, 127].  rows and
+ * cols are at most SGEMM_I8_MAX_DIM, and rows x kp at most SGEMM_I8_MAX_VALUES.
+ *
+ * Rounding: for the largest magnitude m of a row or group, the scale is
+ * s = max(m / 127 rounded to a float, 2^-126), and x is held as the whole
+ * number nearest to x / s (the exact quotient), of two equally near the even
+ * one.  A row or group that holds a NaN or an infinity has the scale NaN and
+ * values 0: whatever it enters becomes NaN.
+ *
+ * The products' sums are exact: 32-bit integers, which is why a sum is at
+ * most SGEMM_I8_MAX_SUM long.  A sum becomes a float, is multiplied by the
+ * smaller of its two scales, then by the larger, then by alpha, and is rounded
+ * to C's type.
+ *
+ * What the 4-bit calls have in common above holds here too: types, leading
+ * dimensions, alignment, checks, status codes, and nothing allocated,
+ * synchronised or kept.
+ */
+#define SGEMM_I8_MAX_DIM  (1 << 22)
+#define SGEMM_I8_MAX_VALUES (1LL << 34)
+#define SGEMM_I8_MAX_SUM  (1 << 17)
+#define SGEMM_I8_GROUP    128
+
+/* Bytes of the two arrays of a rows x cols matrix (either may be NULL). */
+int sgemm_f32_i8_bytes(int rows, int cols, int group, long long *values_bytes, long long *scales_bytes);
+
+/*
+ * Quantises the rows x cols matrix X, with a scale for each row, or for each
+ * 128 columns of a row (group = SGEMM_I8_GROUP).  trans = 1: X is stored cols x
+ * rows (ldx >= rows), and group must be 0; this takes scratch memory, at least
+ * the bytes that sgemm_f32_i8_quantize_scratch gives, 256-byte aligned,
+ * overlapping nothing (trans = 0: none, NULL).
+ */
+int sgemm_f32_i8_quantize(int trans, int rows, int cols, int group, int type, const void *X, int ldx,
+                          void *values, void *scales, void *scratch, long long scratch_bytes,
+                          hipStream_t stream);
+int sgemm_f32_i8_quantize_scratch(int trans, int rows, int cols, long long *bytes);
+
+/* Y (rows x cols) = value * scale, as a float and then rounded to Y's type. */
+int sgemm_f32_i8_dequantize(int rows, int cols, int group, const void *values, const void *scales,
+                            int type, void *Y, int ldy, hipStream_t stream);
+
+/*
+ * C = alpha * A * B^T + beta * C for A (M x K) and B (N x K) with a scale for
+ * each row (tokens and channels).  As in sgemm_f32_gemm, beta == 0 means C is
+ * not read, and alpha == 0 or K == 0 that A and B are not (nor checked).
+ * K <= SGEMM_I8_MAX_SUM.
+ */
+int sgemm_f32_i8_gemm(int M, int N, int K, float alpha, const void *a, const void *a_scales,
+                      const void *b, const void *b_scales, float beta,
+                      int type, void *C, int ldc, hipStream_t stream);
+
+/*
+ * Y = q(X) * W^T for float rows X (M x K), quantised by row on the way, and
+ * 8-bit weights W (N x K) with a scale for each row; Y (M x N) in X's type.
+ * The same values as sgemm_f32_i8_quantize and sgemm_f32_i8_gemm give.  K <=
+ * SGEMM_I8_MAX_SUM.  scratch: device memory of at least the bytes that
+ * sgemm_f32_i8_linear_scratch gives (for few tokens none), 256-byte aligned,
+ * overlapping nothing; its contents do not matter before or after.
+ */
+int sgemm_f32_i8_linear(int M, int N, int K, int type, const void *X, int ldx,
+                        const void *w, const void *w_scales, void *Y, int ldy,
+                        void *scratch, long long scratch_bytes, hipStream_t stream);
+int sgemm_f32_i8_linear_scratch(int M, int N, int K, int type, long long *bytes);
+
+/*
+ * A training step of the layer Y = X W^T, X (M x K), W (N x K), whose
+ * checkpoint is 8-bit.  Forward leaves X and W quantised by row (xq, wq) and
+ * gives Y = xq wq^T in X's type; it is sgemm_f32_i8_quantize of each and
+ * sgemm_f32_i8_gemm in one call.  Backward needs nothing else of the forward
+ * pass.  With x_m and w_n the scales of xq and wq, and xq[m, k], wq[n, k] their
+ * whole numbers:
+ *     dX[m, k] = sum over n of (dY[m, n] * w_n) * wq[n, k]
+ *     dW[n, k] = sum over m of (dY[m, n] * x_m) * xq[m, k]   (+ beta * dW)
+ * the gradients with the rounding taken as the identity.  dY times a scale is
+ * rounded to a float, and then to whole numbers: for dX with a scale for each
+ * token m, as above (8 bits); for dW with a scale for each channel n, s =
+ * max(largest / 32639 rounded to a float, 2^-126) (16 bits).  The sums are exact, those
+ * of dW in two parts that are added as floats.  dX comes in dY's type, dW in
+ * fp32.  M, N and K are at most SGEMM_I8_MAX_SUM each.  scratch: at least the
+ * bytes that sgemm_f32_i8_train_scratch gives, 256-byte aligned, overlapping
+ * nothing.
+ */
+int sgemm_f32_i8_train_forward(int M, int N, int K, int type, const void *X, int ldx,
+                               int type_w, const void *W, int ldw, void *Y, int ldy,
+                               void *xq, void *x_scales, void *wq, void *w_scales, hipStream_t stream);
+int sgemm_f32_i8_train_backward(int M, int N, int K, int type, const void *dY, int lddy,
+                                const void *xq, const void *x_scales, const void *wq, const void *w_scales,
+                                void *dX, int lddx, float beta, void *dW, int lddw,
+                                void *scratch, long long scratch_bytes, hipStream_t stream);
+int sgemm_f32_i8_train_scratch(int M, int N, int K, long long *bytes);
+
+/*
+ * The gated activation H = silu(G) * U, silu(g) = g / (1 + exp(-g)), of the
+ * rows x 2 inner matrix GU = [G, U], with an 8-bit checkpoint: forward gives H
+ * (rows x inner, GU's type) and leaves G and U, each quantised as
+ * sgemm_f32_i8_quantize does with group = SGEMM_I8_GROUP.  Backward gives the
+ * gradient of GU (rows x 2 inner, dH's type) with g and u the checkpoint's
+ * values and p = 1 / (1 + exp(-g)):
+ *     dG = dH * u * p * (1 + g * (1 - p))        dU = dH * g * p
+ * All in fp32, rounded once.
+ */
+int sgemm_f32_i8_swiglu_forward(int rows, int inner, int type, const void *GU, int ldgu, void *H, int ldh,
+                                void *g_values, void *g_scales, void *u_values, void *u_scales,
+                                hipStream_t stream);
+int sgemm_f32_i8_swiglu_backward(int rows, int inner, int type, const void *dH, int lddh,
+                                 const void *g_values, const void *g_scales,
+                                 const void *u_values, const void *u_scales,
+                                 void *dGU, int lddgu, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
