@@ -247,51 +247,66 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
         freed = stage;
         stage = next;
     }
-    // Loads still in flight write this workgroup's LDS: let them land.
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    // Loads still in flight write this workgroup's LDS: let them land.  Then the
+    // scales take its place: a lane that fetched the scale of each of its rows
+    // from memory would wait for every one of them.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    constexpr int ROWS = TL::BM / PIECES;
+    float *scales = (float *)lds;
+    for (int i = tid; i < ROWS; i += TL::NT) scales[i] = g.sa && m0 / PIECES + i < g.M ? g.sa[m0 / PIECES + i] : 1.0f;
+    __syncthreads();
 
     // Lane l holds columns FN (l % 32) + 0 .. FN-1 of its wave's tile (down:
     // l % 32 + 32 k), rows 8 (r / 4) + 4 (l / 32) + r % 4 of each fragment.
     constexpr int APART = DOWN ? 32 : 1;   // columns between a lane's
     const int col = n0 + wn * TL::WTN + (DOWN ? 1 : TL::FN) * fr;
-    const bool wide = !DOWN && col + TL::FN <= g.N;
     float sb[TL::FN];
 #pragma unroll
     for (int k = 0; k < TL::FN; ++k) sb[k] = g.sb && col + APART * k < g.N ? g.sb[col + APART * k] : 1.0f;
+    const auto write = [&](auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
+        const bool wide = !DOWN && (!MASKED || col + TL::FN <= g.N);
 #pragma unroll
-    for (int i = 0; i < TL::FM; i += PIECES)
+        for (int i = 0; i < TL::FM; i += PIECES)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = (m0 + wm * TL::WTM + 32 * i) / PIECES + 8 * (r / 4) + 4 * h + r % 4;
-            if (row >= g.M) continue;
-            const float sa = g.sa ? g.sa[row] : 1.0f;
-            float v[TL::FN];
+            for (int r4 = 0; r4 < 4; ++r4) {
+                const int first = (wm * TL::WTM + 32 * i) / PIECES + 8 * r4 + 4 * h;
+                const f32v4 sa = *(const f32v4 *)(scales + first);
 #pragma unroll
-            for (int k = 0; k < TL::FN; ++k) {
-                float sum = (float)acc[i][k][r];
-                if constexpr (PIECES == 2) sum = fmaf(256.0f, sum, (float)acc[i + 1][k][r]);
-                v[k] = g.alpha * scaled(sum, sa, sb[k]);
-            }
-            T *p = (T *)g.c + row * g.ldc + col;
-            if (wide) {
-                Vec<TL::FN, T> out;
-                if (g.beta != 0.0f) {
-                    const Vec<TL::FN, T> old = *(const Vec<TL::FN, T> *)p;
+                for (int r1 = 0; r1 < 4; ++r1) {
+                    const int row = m0 / PIECES + first + r1, r = 4 * r4 + r1;
+                    if (MASKED && row >= g.M) continue;
+                    float v[TL::FN];
 #pragma unroll
-                    for (int k = 0; k < TL::FN; ++k) v[k] += g.beta * MxType<TYPE>::load(&old.v[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < TL::FN; ++k) out.v[k] = MxType<TYPE>::from(v[k]);
-                store<TL::BM >= 256>((Vec<TL::FN, T> *)p, out);
-            } else {
-#pragma unroll
-                for (int k = 0; k < TL::FN; ++k)
-                    if (col + APART * k < g.N) {
-                        if (g.beta != 0.0f) v[k] += g.beta * MxType<TYPE>::load(p + APART * k);
-                        p[APART * k] = MxType<TYPE>::from(v[k]);
+                    for (int k = 0; k < TL::FN; ++k) {
+                        float sum = (float)acc[i][k][r];
+                        if constexpr (PIECES == 2) sum = fmaf(256.0f, sum, (float)acc[i + 1][k][r]);
+                        v[k] = g.alpha * scaled(sum, sa[r1], sb[k]);
                     }
+                    T *p = (T *)g.c + row * g.ldc + col;
+                    if (wide) {
+                        Vec<TL::FN, T> out;
+                        if (g.beta != 0.0f) {
+                            const Vec<TL::FN, T> old = *(const Vec<TL::FN, T> *)p;
+#pragma unroll
+                            for (int k = 0; k < TL::FN; ++k) v[k] += g.beta * MxType<TYPE>::load(&old.v[k]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < TL::FN; ++k) out.v[k] = MxType<TYPE>::from(v[k]);
+                        store<TL::BM >= 256>((Vec<TL::FN, T> *)p, out);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < TL::FN; ++k)
+                            if (!MASKED || col + APART * k < g.N) {
+                                if (g.beta != 0.0f) v[k] += g.beta * MxType<TYPE>::load(p + APART * k);
+                                p[APART * k] = MxType<TYPE>::from(v[k]);
+                            }
+                    }
+                }
             }
-        }
+    };
+    if (m0 / PIECES + ROWS <= g.M && n0 + TL::BN <= g.N) write(std::false_type{});
+    else write(std::true_type{});
 }
 
 template <class TL, int TYPE, bool DOWN, int PIECES>
@@ -299,9 +314,11 @@ __global__ __launch_bounds__(TL::NT, 1) void i8_gemm_kernel(Args g) {
     compute_tile<TL, TYPE, DOWN, PIECES>(g, blockIdx.x);
 }
 
-typedef Tile<256, 256, 2, 4, 2> T256;
-typedef Tile<128, 128, 2, 4, 2> T128;
-typedef Tile<64, 64, 1, 4, 2> T64;
+typedef Tile<256, 256, 2, 4, 2> T256;       // 8 waves of 128 x 64, 128 KiB
+typedef Tile<128, 128, 2, 4, 2> T128;       // 8 waves of 64 x 32, 64 KiB: two workgroups on a CU
+typedef Tile<128, 128, 2, 4, 4> T128Deep;   // the same, 128 KiB
+typedef Tile<64, 64, 2, 2, 4> T64;          // 4 waves of 32 x 32, 64 KiB
+typedef Tile<64, 64, 1, 2, 4> T64Pairs;     // 2 waves of 64 x 32: fragments in pairs
 
 template <class TL>
 Args arguments(const I8GemmJob &j) {
@@ -318,9 +335,35 @@ hipError_t launch_tile(const I8GemmJob &j, hipStream_t s) {
                            TL::S * TL::STAGE, s);
 }
 
+enum Kind { k256, k128, k128Deep, k64 };
+
+Kind kind_of(const I8GemmJob &j, int num_cus) {
+    const int64_t rows = j.pieces == 2 ? i8_piece_rows(j.M) : j.M;
+    const auto tiles = [&](int b) { return ((rows + b - 1) / b) * (((int64_t)j.N + b - 1) / b); };
+    // The largest tile that gives every CU one and whose rounds leave at most
+    // a fifth of the CUs' time unused (272 tiles of 256 x 256, 4352 x 4096 x
+    // 4096: 98.5 us, 96.6 in tiles of 128 x 128, two to a CU; 448 in two rounds,
+    // 7000 x 4096 x 4096: 119 against 137).
+    const int64_t rounds = (tiles(256) + num_cus - 1) / num_cus;
+    if (tiles(256) >= num_cus && 4 * rounds * num_cus <= 5 * tiles(256)) return k256;
+    // One tile of 128 x 128 for a CU at most: a deep ring hides the memory's
+    // latency (2048 x 2048 x 4096: 23.7 us against 26.6); more, and a second
+    // workgroup hides it (1111 x 4097 x 2050, 297 tiles: 21.4 against 31.0).
+    // With less than half a tile for a CU, smaller ones spread further (200 x
+    // 8192 x 4096, 128 tiles: 17.5 us against 21.4; 1000 x 1000 x 8192, 64: 20.4
+    // against 33.1; but 1024 x 4096 x 4096, 256: 27.8 against 23.7).
+    if (tiles(128) > num_cus) return k128;
+    return 2 * tiles(128) > num_cus ? k128Deep : k64;
+}
+
 template <int TYPE, bool DOWN, int PIECES>
 hipError_t launch_form(const I8GemmJob &j, int num_cus, hipStream_t s) {
-    return launch_tile<T128, TYPE, DOWN, PIECES>(j, s);
+    switch (kind_of(j, num_cus)) {
+    case k256: return launch_tile<T256, TYPE, DOWN, PIECES>(j, s);
+    case k128: return launch_tile<T128, TYPE, DOWN, PIECES>(j, s);
+    case k128Deep: return launch_tile<T128Deep, TYPE, DOWN, PIECES>(j, s);
+    default: return launch_tile<std::conditional_t<PIECES == 2, T64Pairs, T64>, TYPE, DOWN, PIECES>(j, s);
+    }
 }
 
 }  // namespace
