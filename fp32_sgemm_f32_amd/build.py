@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libsgemm_f32.so")
 
 SOURCES = ["sgemm_f32.hip", "plan.cpp", "gemm_mfma.hip", "gemm_mfma_dl.hip", "gemm_generic.hip", "gemm_valu.hip", "pack.hip", "sk_fixup.hip", "skinny.hip", "rowdot.hip",
            "mx4_api.hip", "mx4_quant.hip", "mx4_gemm.hip", "mx4_linear.hip", "mx4_moe.hip",
-           "i8_api.hip", "i8_quant.hip", "i8_gemm.hip", "i8_swiglu.hip"]
+           "i8_api.hip", "i8_quant.hip", "i8_gemm.hip", "i8_thin.hip", "i8_swiglu.hip"]
 ARCH = "gfx950"
 
 COMMON = [

@@ -26,17 +26,22 @@ __device__ __forceinline__ float i8_scale(uint32_t m, float levels) {
     return fmaxf(__fdiv_rn(__uint_as_float(m), levels), 0x1p-126f);
 }
 
-// The whole number nearest to v / s, exactly (of two the even one), with inv =
-// 1 / s.  v * inv is within 2^-22 of the quotient, relatively, so its nearest
-// whole number q is right, or one off where the quotient lies next to a border;
-// v - q s, exact in a fused product (its bits lie between the last of s or v and
-// s / 2), says on which side.  NaN scales give 0.
-__device__ __forceinline__ int i8_nearest(float v, float s, float inv) {
-    const float q = rintf(v * inv), r = fmaf(-q, s, v);
-    int n = (int)q;
-    const float twice = 2.0f * fabsf(r);
+// The whole number n nearest to v / s (of two the even one), as the bits of 1.5
+// 2^23 + n: its low bytes are n's.  With inv = 1 / s, v * inv lies within 2^-23 of
+// the quotient, relatively, so n is right but where the quotient lies next to a
+// border; v - n s, exact in a fused product (its bits lie between the last of s
+// or v and s / 2), reaches s / 2 there, and only there is n looked at again.
+constexpr float kI8Bias = 12582912.0f;
+__device__ __forceinline__ uint32_t i8_bits(float v, float s, float inv, float &rest) {
+    const float b = fmaf(v, inv, kI8Bias);
+    rest = fabsf(fmaf(-(b - kI8Bias), s, v));
+    return __float_as_uint(b);
+}
+__device__ __forceinline__ uint32_t i8_bits_at_border(float v, float s, float inv) {
+    const float b = fmaf(v, inv, kI8Bias), r = fmaf(-(b - kI8Bias), s, v), twice = 2.0f * fabsf(r);
+    uint32_t n = __float_as_uint(b);
     if (twice > s || (twice == s && (n & 1))) n += r > 0.0f ? 1 : -1;
-    return s == s ? n : 0;
+    return n;
 }
 
 // The largest of the 16 lanes of a row of lanes, in all of them.
@@ -54,17 +59,83 @@ __device__ __forceinline__ uint32_t i8_max8(const float (&v)[8]) {
     return m;
 }
 
-// Eight values as whole numbers, bytes in order.
+// Eight values as whole numbers, bytes in order; zeros under a NaN scale.
 __device__ __forceinline__ uint2 i8_nearest8(const float (&v)[8], float s, float inv) {
-    uint32_t w[2] = {0, 0};
+    uint32_t n[8];
+    float most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i / 4] |= ((uint32_t)i8_nearest(v[i], s, inv) & 255u) << (8 * (i % 4));
-    return uint2{w[0], w[1]};
+    for (int i = 0; i < 8; ++i) {
+        float rest;
+        n[i] = i8_bits(v[i], s, inv, rest);
+        most = fmaxf(most, rest);
+    }
+    if (__builtin_expect(2.0f * most >= s, 0)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = i8_bits_at_border(v[i], s, inv);
+    }
+    uint2 w;
+    w.x = __builtin_amdgcn_perm(__builtin_amdgcn_perm(n[3], n[2], 0x0c0c0400), __builtin_amdgcn_perm(n[1], n[0], 0x0c0c0400), 0x05040100);
+    w.y = __builtin_amdgcn_perm(__builtin_amdgcn_perm(n[7], n[6], 0x0c0c0400), __builtin_amdgcn_perm(n[5], n[4], 0x0c0c0400), 0x05040100);
+    return s == s ? w : uint2{0, 0};
 }
 // And back.
 __device__ __forceinline__ void i8_values8(uint2 q, float s, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = (float)(int8_t)((i < 4 ? q.x : q.y) >> (8 * (i % 4))) * s;
+}
+
+// Eight adjacent values of a row as they come from memory.
+template <int TYPE>
+struct I8Raw {
+    typedef typename MxType<TYPE>::T E;
+    u32v4_any w[TYPE == SGEMM_TYPE_F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const E *p) {
+        w[0] = ((const u32v4_any *)p)[0];
+        if constexpr (TYPE == SGEMM_TYPE_F32) w[1] = ((const u32v4_any *)p)[1];
+    }
+    // The first n < 8 of them, zeros behind.
+    __device__ __forceinline__ void load(const E *p, int n) {
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? (TYPE == SGEMM_TYPE_F32 ? ((const uint32_t *)p)[i] : (uint32_t)((const uint16_t *)p)[i]) : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if constexpr (TYPE == SGEMM_TYPE_F32) w[i / 4][i % 4] = v[i];
+            else w[0][i / 2] = i % 2 ? w[0][i / 2] | v[i] << 16 : v[i];
+    }
+    __device__ __forceinline__ void clear() {
+        w[0] = u32v4_any{0, 0, 0, 0};
+        if constexpr (TYPE == SGEMM_TYPE_F32) w[1] = w[0];
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if constexpr (TYPE == SGEMM_TYPE_F32) {
+                v[i] = __uint_as_float(w[i / 4][i % 4]);
+            } else {
+                const uint16_t h = (uint16_t)(w[0][i / 2] >> (16 * (i % 2)));
+                v[i] = MxType<TYPE>::load(&h);
+            }
+    }
+};
+
+// N eights of a row, from columns c, c + step, ... on; zeros at and after
+// `cols`.  All loads are in flight before any is waited for.
+template <int TYPE, int N>
+__device__ __forceinline__ void i8_load_row(const typename MxType<TYPE>::T *row, int c, int step, int cols, I8Raw<TYPE> (&r)[N]) {
+    const int whole = cols & ~7;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        r[i].clear();
+        if (c + i * step < whole) r[i].load(row + c + i * step);
+    }
+    if (whole < cols) {   // one lane's
+        I8Raw<TYPE> last;
+        last.load(row + whole, cols - whole);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c + i * step == whole) r[i] = last;
+    }
 }
 
 // Eight adjacent values of a row from column c on, those before `cols`.
@@ -177,6 +248,13 @@ hipError_t launch_i8_cols(const I8ColsJob &j, hipStream_t s);
 hipError_t launch_i8_groups(const I8GroupsJob &j, hipStream_t s);
 hipError_t launch_i8_back(const I8BackJob &j, hipStream_t s);
 hipError_t launch_i8_gemm(const I8GemmJob &j, int num_cus, hipStream_t s);
+// The same for at most kI8ThinRows rows of A or B (not down, one piece): weights
+// streamed past tokens.  floats: A is quantised on the way (type j.type, leading
+// dimension ldx).
+constexpr int kI8ThinRows = 8;
+bool i8_thin_takes(int M, int N, int K);
+bool i8_thin_takes_floats(int M, int N, int K);
+hipError_t launch_i8_thin(const I8GemmJob &j, const void *floats, int64_t ldx, int num_cus, hipStream_t s);
 hipError_t launch_i8_swiglu_forward(const I8SwigluJob &j, hipStream_t s);
 hipError_t launch_i8_swiglu_backward(const I8SwigluJob &j, hipStream_t s);
 

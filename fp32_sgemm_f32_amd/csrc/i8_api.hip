@@ -92,14 +92,16 @@ SGEMM_API int sgemm_f32_i8_gemm(int M, int N, int K, float alpha, const void *a,
                                 k > 0 ? (const float *)sb : nullptr, M, N, k, type, 0, 1, alpha, beta, C, ldc}, cus, stream));
 }
 
-// Scratch memory of a product with float rows: their 8-bit form.
-static int64_t linear_scratch(int M, int K) { return K > 0 ? up256(values_bytes(M, K)) + up256((int64_t)M * 4) : 0; }
+// Scratch memory of a product with float rows: their 8-bit form, where a kernel of its own makes it.
+static int64_t linear_scratch(int M, int N, int K) {
+    return K > 0 && !i8_thin_takes_floats(M, N, K) ? up256(values_bytes(M, K)) + up256((int64_t)M * 4) : 0;
+}
 
 SGEMM_API int sgemm_f32_i8_linear_scratch(int M, int N, int K, int type, long long *bytes) {
     if (!size_ok(M, K) || !size_ok(N, K) || K > SGEMM_I8_MAX_SUM) return SGEMM_ERR_SHAPE;
     if (!known_type(type)) return SGEMM_ERR_CONFIG;
     if (!bytes) return SGEMM_ERR_NULL;
-    *bytes = linear_scratch(M, K);
+    *bytes = linear_scratch(M, N, K);
     return SGEMM_OK;
 }
 
@@ -109,7 +111,7 @@ SGEMM_API int sgemm_f32_i8_linear(int M, int N, int K, int type, const void *X, 
     if (!known_type(type)) return SGEMM_ERR_CONFIG;
     if (M == 0 || N == 0) return SGEMM_OK;
     if (ldx < K || ldy < N) return SGEMM_ERR_LD;
-    const int64_t need = linear_scratch(M, K);
+    const int64_t need = linear_scratch(M, N, K);
     if (scratch && scratch_bytes < need) return SGEMM_ERR_SCRATCH;
     const Span spans[] = {floats(X, M, K, ldx, type, false), values(w, N, K, false), scales(sw, N, K, 0, false),
                           floats(Y, M, N, ldy, type, true), Span{scratch, need, 256, true}};
@@ -117,6 +119,9 @@ SGEMM_API int sgemm_f32_i8_linear(int M, int N, int K, int type, const void *X, 
     int status = check_spans(spans, &dev);
     if (status == SGEMM_OK) status = compute_units(dev, &cus);
     if (status != SGEMM_OK) return status;
+    if (K > 0 && need == 0)
+        return done(launch_i8_thin({nullptr, nullptr, (const int8_t *)w, (const float *)sw, M, N, K, type, 0, 1, 1.0f, 0.0f, Y, ldy}, X, ldx,
+                                   cus, stream));
     int8_t *q = (int8_t *)scratch;
     float *s = K > 0 ? (float *)(q + up256(values_bytes(M, K))) : nullptr;
     const hipError_t e = K > 0 ? launch_i8_rows({X, ldx, M, K, type, nullptr, q, s}, stream) : hipSuccess;

@@ -51,16 +51,17 @@ struct Args {
     float alpha, beta;
 };
 
-template <int BM_, int BN_, int WM_, int WN_, int S_>
+template <int BM_, int BN_, int WM_, int WN_, int S_, int KS_ = 1>
 struct Tile {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
-    static constexpr int NW = WM * WN, NT = 64 * NW;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, KS = KS_;
+    static constexpr int NW = WM * WN, NT = 64 * NW * KS;                            // waves of a set, threads of all
+
     static constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
     static constexpr int STEPS = kChunk / 32;
-    static constexpr int A_BYTES = BM * kChunk, B_BYTES = BN * kChunk, STAGE = A_BYTES + B_BYTES;
+    static constexpr int A_BYTES = BM * kChunk, B_BYTES = BN * kChunk, STAGE = A_BYTES + B_BYTES, RING = S * STAGE;
     static constexpr int A_PW = A_BYTES / 1024 / NW, B_PW = B_BYTES / 1024 / NW, L = A_PW + B_PW;   // loads of a wave per chunk
     static_assert(A_PW * NW * 1024 == A_BYTES && B_PW * NW * 1024 == B_BYTES, "a chunk's loads split evenly over the waves");
-    static_assert(S * STAGE <= 160 * 1024 && (S - 2) * L < 64 && S >= 2, "LDS and vmcnt budget");
+    static_assert(KS * RING <= 160 * 1024 && (KS - 1) * BM * BN <= KS * RING / 4 && (S - 2) * L < 64 && S >= 2, "LDS and vmcnt budget");
 
     __device__ __forceinline__ static int swz(int r) { return (r ^ (r >> 3)) & 7; }
     // Column of the tile that B's LDS row r holds.
@@ -82,7 +83,7 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
     typedef typename MxType<TYPE>::T T;
     extern __shared__ __attribute__((aligned(1024))) int8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int all = __builtin_amdgcn_readfirstlane(tid >> 6), set = all / TL::NW, wave = all % TL::NW;
     const int wm = wave / TL::WN, wn = wave % TL::WN;
 
     // Workgroup -> tile: each XCD (workgroups w, w + 8, ...) takes a
@@ -123,11 +124,14 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
             vb[i] = (uint32_t)(TL::b_col(r) * rowb) + 16 * ((lane % 8) ^ TL::swz(r));
         }
     }
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)lds;
+    const int8_t *ring = lds + set * TL::RING;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)lds + set * TL::RING;
 
     // Loads i = 0 .. L-1 of a chunk, A's first; `next_chunk` moves the
     // resources on by one chunk.  From the last chunk on they are empty.
-    int lc = 0;   // the chunk that the resources stand at
+    int lc = set;   // the chunk that the resources stand at
+    advance(ra, (int64_t)set * kChunk);
+    advance(rb, set * (DOWN ? kChunk * downb : kChunk));
     auto limits = [&] {
         const bool in = lc < chunks;
         ra[2] = in ? (int)(am * rowb - lc * kChunk) : 0;
@@ -142,9 +146,9 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
         else if constexpr (i < TL::L) dma16(rb, vb[i - TL::A_PW], base + TL::A_BYTES + (wave * TL::B_PW + i - TL::A_PW) * 1024);
     };
     auto next_chunk = [&] {
-        ++lc;
-        advance(ra, kChunk);
-        advance(rb, DOWN ? kChunk * downb : kChunk);
+        lc += TL::KS;
+        advance(ra, TL::KS * kChunk);
+        advance(rb, TL::KS * (DOWN ? kChunk * downb : kChunk));
         limits();
     };
     auto load_chunk = [&](int stage) {
@@ -169,7 +173,7 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
         i32v4 a[TL::FM], b[TL::FN];
     };
     auto read_ops = [&](Ops &o, int stage, int j) {
-        const int8_t *st = lds + stage * TL::STAGE;
+        const int8_t *st = ring + stage * TL::STAGE;
 #pragma unroll
         for (int i = 0; i < TL::FM; ++i) {
             const int r = wm * TL::WTM + 32 * i + fr;
@@ -212,7 +216,7 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
     Ops o[2];
     read_ops(o[0], 0, 0);
     int stage = 0, freed = TL::S - 1;
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; c < chunks; c += TL::KS) {
         const int next = stage + 1 == TL::S ? 0 : stage + 1;
         each<0, TL::STEPS - 1>([&](auto jc) {
             constexpr int j = decltype(jc)::value;
@@ -248,9 +252,27 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
         stage = next;
     }
     // Loads still in flight write this workgroup's LDS: let them land.  Then the
-    // scales take its place: a lane that fetched the scale of each of its rows
-    // from memory would wait for every one of them.
+    // other sets' sums take their place, and then the scales: a lane that
+    // fetched the scale of each of its rows from memory would wait for every
+    // one of them.
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if constexpr (TL::KS > 1) {
+        constexpr int OF_WAVE = TL::FM * TL::FN * 16 * 64;
+        int *sums = (int *)lds + lane;
+        if (set > 0) {
+#pragma unroll
+            for (int i = 0; i < TL::FM * TL::FN * 16; ++i)
+                sums[((set - 1) * TL::NW + wave) * OF_WAVE + i * 64] = acc[i / 16 / TL::FN][i / 16 % TL::FN][i % 16];
+        }
+        __syncthreads();
+        if (set == 0) {
+            for (int k = 0; k < TL::KS - 1; ++k)
+#pragma unroll
+                for (int i = 0; i < TL::FM * TL::FN * 16; ++i)
+                    acc[i / 16 / TL::FN][i / 16 % TL::FN][i % 16] += sums[(k * TL::NW + wave) * OF_WAVE + i * 64];
+        }
+        __syncthreads();
+    }
     constexpr int ROWS = TL::BM / PIECES;
     float *scales = (float *)lds;
     for (int i = tid; i < ROWS; i += TL::NT) scales[i] = g.sa && m0 / PIECES + i < g.M ? g.sa[m0 / PIECES + i] : 1.0f;
@@ -305,6 +327,7 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
                 }
             }
     };
+    if (set > 0) return;
     if (m0 / PIECES + ROWS <= g.M && n0 + TL::BN <= g.N) write(std::false_type{});
     else write(std::true_type{});
 }
@@ -318,7 +341,11 @@ typedef Tile<256, 256, 2, 4, 2> T256;       // 8 waves of 128 x 64, 128 KiB
 typedef Tile<128, 128, 2, 4, 2> T128;       // 8 waves of 64 x 32, 64 KiB: two workgroups on a CU
 typedef Tile<128, 128, 2, 4, 4> T128Deep;   // the same, 128 KiB
 typedef Tile<64, 64, 2, 2, 4> T64;          // 4 waves of 32 x 32, 64 KiB
-typedef Tile<64, 64, 1, 2, 4> T64Pairs;     // 2 waves of 64 x 32: fragments in pairs
+typedef Tile<64, 32, 2, 1, 4, 2> T64x32;    // 2 x 2 waves of 32 x 32, 96 KiB
+typedef Tile<32, 32, 1, 1, 4, 2> T32;       // 2 waves of 32 x 32, 64 KiB
+// With fragments in pairs.
+typedef Tile<64, 64, 1, 2, 4> T64Pairs;        // 2 waves of 64 x 32
+typedef Tile<64, 32, 1, 1, 4, 2> T64x32Pairs;  // 2 waves of 64 x 32
 
 template <class TL>
 Args arguments(const I8GemmJob &j) {
@@ -332,28 +359,35 @@ hipError_t launch_tile(const I8GemmJob &j, hipStream_t s) {
     Args g = arguments<TL>(j);
     void *params[] = {&g};
     return hipLaunchKernel((const void *)i8_gemm_kernel<TL, TYPE, DOWN, PIECES>, dim3((unsigned)(g.tiles_m * g.tiles_n)), dim3(TL::NT), params,
-                           TL::S * TL::STAGE, s);
+                           TL::KS * TL::RING, s);
 }
 
-enum Kind { k256, k128, k128Deep, k64 };
+enum Kind { k256, k128, k128Deep, k64, k64x32, k32 };
 
 Kind kind_of(const I8GemmJob &j, int num_cus) {
     const int64_t rows = j.pieces == 2 ? i8_piece_rows(j.M) : j.M;
-    const auto tiles = [&](int b) { return ((rows + b - 1) / b) * (((int64_t)j.N + b - 1) / b); };
+    const auto tiles = [&](int m, int n) { return ((rows + m - 1) / m) * (((int64_t)j.N + n - 1) / n); };
     // The largest tile that gives every CU one and whose rounds leave at most
     // a fifth of the CUs' time unused (272 tiles of 256 x 256, 4352 x 4096 x
     // 4096: 98.5 us, 96.6 in tiles of 128 x 128, two to a CU; 448 in two rounds,
     // 7000 x 4096 x 4096: 119 against 137).
-    const int64_t rounds = (tiles(256) + num_cus - 1) / num_cus;
-    if (tiles(256) >= num_cus && 4 * rounds * num_cus <= 5 * tiles(256)) return k256;
+    const int64_t rounds = (tiles(256, 256) + num_cus - 1) / num_cus;
+    if (tiles(256, 256) >= num_cus && 4 * rounds * num_cus <= 5 * tiles(256, 256)) return k256;
     // One tile of 128 x 128 for a CU at most: a deep ring hides the memory's
     // latency (2048 x 2048 x 4096: 23.7 us against 26.6); more, and a second
     // workgroup hides it (1111 x 4097 x 2050, 297 tiles: 21.4 against 31.0).
     // With less than half a tile for a CU, smaller ones spread further (200 x
     // 8192 x 4096, 128 tiles: 17.5 us against 21.4; 1000 x 1000 x 8192, 64: 20.4
     // against 33.1; but 1024 x 4096 x 4096, 256: 27.8 against 23.7).
-    if (tiles(128) > num_cus) return k128;
-    return 2 * tiles(128) > num_cus ? k128Deep : k64;
+    // At most 32 rows or columns of C: 32 x 4096 x 4096 8.6 us, in tiles of 64 x
+    // 64 14.2, 32 x 28672 x 8192 51 and 54.
+    if (j.pieces == 1 && (rows <= 32 || j.N <= 32)) return k32;
+    if (tiles(128, 128) > num_cus) return k128;
+    if (2 * tiles(128, 128) > num_cus) return k128Deep;
+    // Up to one tile of 64 x 32 for a CU: two sets of waves, each with a ring of
+    // its own, take every other chunk of K (128 x 4096 x 4096: 10.4 us against 12.8;
+    // 400 x 1000 x 8192: 12.8 against 18.4; 200 x 300 x 700: 6.2 against 6.5).
+    return tiles(64, 32) <= num_cus ? k64x32 : k64;
 }
 
 template <int TYPE, bool DOWN, int PIECES>
@@ -362,13 +396,18 @@ hipError_t launch_form(const I8GemmJob &j, int num_cus, hipStream_t s) {
     case k256: return launch_tile<T256, TYPE, DOWN, PIECES>(j, s);
     case k128: return launch_tile<T128, TYPE, DOWN, PIECES>(j, s);
     case k128Deep: return launch_tile<T128Deep, TYPE, DOWN, PIECES>(j, s);
-    default: return launch_tile<std::conditional_t<PIECES == 2, T64Pairs, T64>, TYPE, DOWN, PIECES>(j, s);
+    case k64: return launch_tile<std::conditional_t<PIECES == 2, T64Pairs, T64>, TYPE, DOWN, PIECES>(j, s);
+    case k64x32: return launch_tile<std::conditional_t<PIECES == 2, T64x32Pairs, T64x32>, TYPE, DOWN, PIECES>(j, s);
+    default:
+        if constexpr (PIECES == 1) return launch_tile<T32, TYPE, DOWN, PIECES>(j, s);
+        return hipErrorInvalidValue;
     }
 }
 
 }  // namespace
 
 hipError_t launch_i8_gemm(const I8GemmJob &j, int num_cus, hipStream_t s) {
+    if (!j.down && j.K > 0 && i8_thin_takes(j.M, j.N, j.K)) return launch_i8_thin(j, nullptr, 0, num_cus, s);
     if (j.pieces == 2) return launch_form<SGEMM_TYPE_F32, true, 2>(j, num_cus, s);
     switch (j.type) {
     case SGEMM_TYPE_F32: return j.down ? launch_form<SGEMM_TYPE_F32, true, 1>(j, num_cus, s) : launch_form<SGEMM_TYPE_F32, false, 1>(j, num_cus, s);

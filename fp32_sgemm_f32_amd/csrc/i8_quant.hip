@@ -31,25 +31,34 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void i8_rows_kernel(
     if (row >= j.rows) return;
     const E *x = (const E *)j.x + row * j.ldx;
     const int ld = (int)i8_ld(j.cols);
-    const auto load = [&](int c, float (&v)[8]) {
-        mx_load_edge8<TYPE>(x, c, j.cols, v);
+    // Values kKeep T eights from c on, and their largest magnitude.
+    const auto load = [&](int c, float (&v)[kKeep][8], uint32_t m) {
+        I8Raw<TYPE> raw[kKeep];
+        i8_load_row<TYPE>(x, c, 8 * T, j.cols, raw);
         if (j.fold) {
-            float w[8];
-            mx_load_edge8<SGEMM_TYPE_F32>(j.fold, c, j.cols, w);
+            I8Raw<SGEMM_TYPE_F32> fold[kKeep];
+            i8_load_row<SGEMM_TYPE_F32>(j.fold, c, 8 * T, j.cols, fold);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= w[i];
+            for (int i = 0; i < kKeep; ++i) {
+                float w[8];
+                raw[i].get(v[i]);
+                fold[i].get(w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[i][k] *= w[k];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) raw[i].get(v[i]);
         }
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) m = i8_max(m, i8_max8(v[i]));
+        return m;
     };
     float v[kKeep][8];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i) load(8 * (t + T * i), v[i]);
-#pragma unroll
-    for (int i = 0; i < kKeep; ++i) m = i8_max(m, i8_max8(v[i]));
-    for (int c = 8 * (t + T * kKeep); c < j.cols; c += 8 * T) {
-        float w[8];
-        load(c, w);
-        m = i8_max(m, i8_max8(w));
+    uint32_t m = load(8 * t, v, 0);
+    for (int c = 8 * (t + T * kKeep); c < j.cols; c += 8 * T * kKeep) {
+        float w[kKeep][8];
+        m = load(c, w, m);
     }
     m = i8_max16(m);
     m = i8_max(m, __shfl_xor(m, 16, 64));
@@ -63,15 +72,13 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void i8_rows_kernel(
     }
     const float s = i8_scale(m, kI8Levels), inv = 1.0f / s;
     int8_t *q = j.q + row * ld;
+    for (int c0 = 8 * t; c0 < ld; c0 += 8 * T * kKeep) {
+        if (c0 > 8 * t) load(c0, v, 0);
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i) {
-        const int c = 8 * (t + T * i);
-        if (c < ld) *(uint2 *)(q + c) = i8_nearest8(v[i], s, inv);
-    }
-    for (int c = 8 * (t + T * kKeep); c < ld; c += 8 * T) {
-        float w[8];
-        load(c, w);
-        *(uint2 *)(q + c) = i8_nearest8(w, s, inv);
+        for (int i = 0; i < kKeep; ++i) {
+            const int c = c0 + 8 * T * i;
+            if (c < ld) *(uint2 *)(q + c) = i8_nearest8(v[i], s, inv);
+        }
     }
     if (t == 0) j.s[row] = s;
 }
@@ -96,7 +103,9 @@ __global__ __launch_bounds__(256) void i8_part_kernel(I8ColsJob j) {
 #pragma unroll 4
     for (int row = begin + r; row < end; row += 16) {
         float v[8];
-        mx_load_edge8<TYPE>((const E *)j.x + row * j.ldx, c0 + c, j.cols, v);
+        const E *x = (const E *)j.x + row * j.ldx;
+        if (c0 + 128 <= j.cols) mx_load8<TYPE>(x + c0 + c, v);
+        else mx_load_edge8<TYPE>(x, c0 + c, j.cols, v);
         const float f = j.fold ? j.fold[row] : 1.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) m[i] = i8_max(m[i], i8_magnitude(v[i] * f));
@@ -140,26 +149,51 @@ __global__ __launch_bounds__(256) void i8_cols_kernel(I8ColsJob j) {
     for (int it = 0; it < 2; ++it) {
         const int four = (tid >> 4) + 16 * it;   // four rows, one word of a column
         float v[4][8];
+        if (c0 + 128 <= j.cols && r0 + 128 <= j.rows) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int row = r0 + 4 * four + k;
-            const bool real = row < j.rows;
-            mx_load_edge8<TYPE>((const E *)j.x + (real ? row : 0) * j.ldx, c0 + c, real ? j.cols : 0, v[k]);
-            const float f = j.fold && real ? j.fold[row] : 1.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] *= f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t high = 0, low = 0;
+            for (int k = 0; k < 4; ++k) mx_load8<TYPE>((const E *)j.x + (r0 + 4 * four + k) * j.ldx + c0 + c, v[k]);
+        } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int n = i8_nearest(v[k][i], scale[c + i], inverse[c + i]);
-                if constexpr (PIECES == 2) high |= ((uint32_t)((n + 128) >> 8) & 255u) << (8 * k);
-                low |= ((uint32_t)n & 255u) << (8 * k);
+                const int row = r0 + 4 * four + k;
+                const bool real = row < j.rows;
+                mx_load_edge8<TYPE>((const E *)j.x + (real ? row : 0) * j.ldx, c0 + c, real ? j.cols : 0, v[k]);
             }
-            if constexpr (PIECES == 2) tile[0][c + i][four] = high;
-            tile[PIECES - 1][c + i][four] = low;
+        }
+        if (j.fold)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int row = r0 + 4 * four + k;
+                const float f = row < j.rows ? j.fold[row] : 1.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] *= f;
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float s = scale[c + i], inv = inverse[c + i];
+            uint32_t n[4];
+            float most = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float rest;
+                n[k] = i8_bits(v[k][i], s, inv, rest);
+                most = fmaxf(most, rest);
+            }
+            if (__builtin_expect(2.0f * most >= s, 0)) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) n[k] = i8_bits_at_border(v[k][i], s, inv);
+            }
+            if constexpr (PIECES == 2) {
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[k] = n[k] + 128;   // its second byte
+                const uint32_t high = __builtin_amdgcn_perm(__builtin_amdgcn_perm(h[3], h[2], 0x0c0c0501),
+                                                            __builtin_amdgcn_perm(h[1], h[0], 0x0c0c0501), 0x05040100);
+                tile[0][c + i][four] = s == s ? high : 0;
+            }
+            const uint32_t low = __builtin_amdgcn_perm(__builtin_amdgcn_perm(n[3], n[2], 0x0c0c0400),
+                                                       __builtin_amdgcn_perm(n[1], n[0], 0x0c0c0400), 0x05040100);
+            tile[PIECES - 1][c + i][four] = s == s ? low : 0;
         }
     }
     __syncthreads();
