@@ -174,27 +174,38 @@ inline unsigned i8_grid(int64_t rows, int64_t chunks, int threads) { return (uns
 
 // ---- host: one job per launcher ----
 
-// Rows of a float matrix, by row (q, s).  fold: each column times fold[column]
-// first, rounded.
+// Rows of a float matrix, by row (q, s).
 struct I8RowsJob {
     const void *x;
     int64_t ldx;
     int rows, cols, type;
-    const float *fold;
     int8_t *q;
     float *s;
 };
-// Columns of a rows x cols float matrix: q (pieces = 1: cols rows; 2: see
-// i8_quant.hip) of `rows` bytes, padded.  fold: each row times fold[row] first.
-// part: scratch memory, i8_part_bytes(rows, cols).
+// Columns of a rows x cols float matrix, as rows of `rows` bytes, padded.  fold:
+// each row times fold[row] first.  part: scratch memory, i8_part_bytes(rows, cols).
 struct I8ColsJob {
     const void *x;
     int64_t ldx;
-    int rows, cols, type, pieces;
+    int rows, cols, type;
     const float *fold;
     uint32_t *part;
     int8_t *q;
     float *s;
+};
+// A gradient both ways: times by_col, by row (q, s), and times by_row, by column
+// in 16 bits (qt, st; two rows for a column, see i8_quant.hip).  part: scratch
+// memory, i8_both_part_bytes(rows, cols).
+struct I8BothJob {
+    const void *x;
+    int64_t ldx;
+    int rows, cols, type;
+    const float *by_col, *by_row;
+    uint32_t *part;
+    int8_t *q;
+    float *s;
+    int8_t *qt;
+    float *st;
 };
 // By 128 columns of a row, and both formats back.
 struct I8GroupsJob {
@@ -240,11 +251,13 @@ struct I8SwigluJob {
 // Rows of the matrix that holds 16-bit numbers of n columns in two pieces.
 inline __host__ __device__ int64_t i8_piece_rows(int64_t n) { return (n + 31) / 32 * 64; }
 int64_t i8_part_bytes(int rows, int cols);
+int64_t i8_both_part_bytes(int rows, int cols);
 
 hipError_t launch_i8_rows(const I8RowsJob &j, hipStream_t s);
 // Two matrices of one type, in one launch.
 hipError_t launch_i8_rows_two(const I8RowsJob &j, const I8RowsJob &k, hipStream_t s);
 hipError_t launch_i8_cols(const I8ColsJob &j, hipStream_t s);
+hipError_t launch_i8_both(const I8BothJob &j, hipStream_t s);
 hipError_t launch_i8_groups(const I8GroupsJob &j, hipStream_t s);
 hipError_t launch_i8_back(const I8BackJob &j, hipStream_t s);
 hipError_t launch_i8_gemm(const I8GemmJob &j, int num_cus, hipStream_t s);

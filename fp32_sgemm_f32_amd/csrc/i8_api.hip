@@ -56,9 +56,9 @@ SGEMM_API int sgemm_f32_i8_quantize(int trans, int rows, int cols, int group, in
     int dev = 0;
     const int status = check_spans(spans, &dev);
     if (status != SGEMM_OK) return status;
-    if (trans) return done(launch_i8_cols({X, ldx, cols, rows, type, 1, nullptr, (uint32_t *)scratch, (int8_t *)q, (float *)s}, stream));
+    if (trans) return done(launch_i8_cols({X, ldx, cols, rows, type, nullptr, (uint32_t *)scratch, (int8_t *)q, (float *)s}, stream));
     if (group) return done(launch_i8_groups({X, ldx, rows, cols, type, (int8_t *)q, (float *)s}, stream));
-    return done(launch_i8_rows({X, ldx, rows, cols, type, nullptr, (int8_t *)q, (float *)s}, stream));
+    return done(launch_i8_rows({X, ldx, rows, cols, type, (int8_t *)q, (float *)s}, stream));
 }
 
 SGEMM_API int sgemm_f32_i8_dequantize(int rows, int cols, int group, const void *q, const void *s, int type, void *Y, int ldy,
@@ -124,7 +124,7 @@ SGEMM_API int sgemm_f32_i8_linear(int M, int N, int K, int type, const void *X, 
                                    cus, stream));
     int8_t *q = (int8_t *)scratch;
     float *s = K > 0 ? (float *)(q + up256(values_bytes(M, K))) : nullptr;
-    const hipError_t e = K > 0 ? launch_i8_rows({X, ldx, M, K, type, nullptr, q, s}, stream) : hipSuccess;
+    const hipError_t e = K > 0 ? launch_i8_rows({X, ldx, M, K, type, q, s}, stream) : hipSuccess;
     if (e != hipSuccess) return done(e);
     return done(launch_i8_gemm({q, s, (const int8_t *)w, K > 0 ? (const float *)sw : nullptr, M, N, K, type, 0, 1, K > 0 ? 1.0f : 0.0f,
                                 0.0f, Y, ldy}, cus, stream));
@@ -148,7 +148,7 @@ SGEMM_API int sgemm_f32_i8_train_forward(int M, int N, int K, int type, const vo
     int status = check_spans(spans, &dev);
     if (status == SGEMM_OK) status = compute_units(dev, &cus);
     if (status != SGEMM_OK) return status;
-    const I8RowsJob jx{X, ldx, M, K, type, nullptr, (int8_t *)xq, (float *)sx}, jw{W, ldw, N, K, type_w, nullptr, (int8_t *)wq, (float *)sw};
+    const I8RowsJob jx{X, ldx, M, K, type, (int8_t *)xq, (float *)sx}, jw{W, ldw, N, K, type_w, (int8_t *)wq, (float *)sw};
     hipError_t e = hipSuccess;
     if (x && w && type == type_w) {
         e = launch_i8_rows_two(jx, jw, stream);
@@ -176,7 +176,7 @@ Back back_layout(int M, int N) {
     b.sd = take((int64_t)M * 4);
     b.t = take(i8_piece_rows(N) * i8_ld(M));
     b.st = take((int64_t)N * 4);
-    b.part = take(i8_part_bytes(M, N));
+    b.part = take(i8_both_part_bytes(M, N));
     b.bytes = M > 0 && N > 0 ? at : 0;
     return b;
 }
@@ -209,10 +209,8 @@ SGEMM_API int sgemm_f32_i8_train_backward(int M, int N, int K, int type, const v
     int8_t *dq = (int8_t *)(p + at.d), *tq = (int8_t *)(p + at.t);
     float *sd = (float *)(p + at.sd), *st = (float *)(p + at.st);
     hipError_t e = hipSuccess;
-    if (d) {
-        e = launch_i8_rows({dY, ldd, M, N, type, (const float *)sw, dq, sd}, stream);
-        if (e == hipSuccess) e = launch_i8_cols({dY, ldd, M, N, type, 2, (const float *)sx, (uint32_t *)(p + at.part), tq, st}, stream);
-    }
+    if (d)
+        e = launch_i8_both({dY, ldd, M, N, type, (const float *)sw, (const float *)sx, (uint32_t *)(p + at.part), dq, sd, tq, st}, stream);
     if (x && e == hipSuccess)
         e = launch_i8_gemm({dq, N > 0 ? sd : nullptr, (const int8_t *)wq, nullptr, M, K, N, type, 1, 1, N > 0 ? 1.0f : 0.0f, 0.0f, dX, lddx},
                            cus, stream);

@@ -35,21 +35,8 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void i8_rows_kernel(
     const auto load = [&](int c, float (&v)[kKeep][8], uint32_t m) {
         I8Raw<TYPE> raw[kKeep];
         i8_load_row<TYPE>(x, c, 8 * T, j.cols, raw);
-        if (j.fold) {
-            I8Raw<SGEMM_TYPE_F32> fold[kKeep];
-            i8_load_row<SGEMM_TYPE_F32>(j.fold, c, 8 * T, j.cols, fold);
 #pragma unroll
-            for (int i = 0; i < kKeep; ++i) {
-                float w[8];
-                raw[i].get(v[i]);
-                fold[i].get(w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[i][k] *= w[k];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kKeep; ++i) raw[i].get(v[i]);
-        }
+        for (int i = 0; i < kKeep; ++i) raw[i].get(v[i]);
 #pragma unroll
         for (int i = 0; i < kKeep; ++i) m = i8_max(m, i8_max8(v[i]));
         return m;
@@ -106,9 +93,8 @@ __global__ __launch_bounds__(256) void i8_part_kernel(I8ColsJob j) {
         const E *x = (const E *)j.x + row * j.ldx;
         if (c0 + 128 <= j.cols) mx_load8<TYPE>(x + c0 + c, v);
         else mx_load_edge8<TYPE>(x, c0 + c, j.cols, v);
-        const float f = j.fold ? j.fold[row] : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[i] = i8_max(m[i], i8_magnitude(v[i] * f));
+        for (int i = 0; i < 8; ++i) m[i] = i8_max(m[i], i8_magnitude(v[i]));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) most[r][c + i] = m[i];
@@ -121,16 +107,22 @@ __global__ __launch_bounds__(256) void i8_part_kernel(I8ColsJob j) {
     }
 }
 
-// 128 columns x 128 rows, written as rows.
-template <int TYPE, int PIECES>
-__global__ __launch_bounds__(256) void i8_cols_kernel(I8ColsJob j) {
+// 128 columns x ROWS rows, written as rows.  fold: each row times fold[row]
+// first.
+template <int TYPE, int PIECES, int ROWS>
+__global__ __launch_bounds__(256) void i8_cols_kernel(I8ColsJob j, int parts) {
     typedef typename MxType<TYPE>::T E;
-    __shared__ uint32_t tile[PIECES][128][33];   // 128 bytes of a column; one word more, so that columns start on other banks
+    // The bytes of a column, in quads of four words: quad q at q ^ (column / 8),
+    // so that the 16 columns that a row of lanes writes at a time lie in
+    // different banks.
+    constexpr int WORDS = ROWS / 4, QUADS = ROWS / 16;
+    __shared__ __attribute__((aligned(16))) uint32_t tile[PIECES][128][WORDS];
+    const auto word = [](int column, int at) { return (((at >> 2) ^ (column >> 3)) & (QUADS - 1)) * 4 + (at & 3); };
     __shared__ uint32_t most[128];
     __shared__ float scale[128], inverse[128];
-    const int tid = threadIdx.x, c0 = blockIdx.x * 128, r0 = blockIdx.y * 128, ld = (int)i8_ld(j.rows);
+    const int tid = threadIdx.x, c0 = blockIdx.x * 128, ld = (int)i8_ld(j.rows);
     {
-        const int c = tid & 127, parts = parts_of(j.rows);
+        const int c = tid & 127;
         uint32_t m = 0;
 #pragma unroll 8
         for (int p = tid >> 7; p < parts; p += 2) m = i8_max(m, j.part[p * i8_ld(j.cols) + c0 + c]);
@@ -145,63 +137,170 @@ __global__ __launch_bounds__(256) void i8_cols_kernel(I8ColsJob j) {
         __syncthreads();
     }
     const int c = 8 * (tid & 15);
+    const int r0 = blockIdx.y * ROWS;
+    {
 #pragma unroll
-    for (int it = 0; it < 2; ++it) {
-        const int four = (tid >> 4) + 16 * it;   // four rows, one word of a column
-        float v[4][8];
-        if (c0 + 128 <= j.cols && r0 + 128 <= j.rows) {
+        for (int it = 0; it < ROWS / 64; ++it) {
+            const int four = (tid >> 4) + 16 * it;   // four rows, one word of a column
+            float v[4][8];
+            if (c0 + 128 <= j.cols && r0 + ROWS <= j.rows) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx_load8<TYPE>((const E *)j.x + (r0 + 4 * four + k) * j.ldx + c0 + c, v[k]);
-        } else {
+                for (int k = 0; k < 4; ++k) mx_load8<TYPE>((const E *)j.x + (r0 + 4 * four + k) * j.ldx + c0 + c, v[k]);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int row = r0 + 4 * four + k;
-                const bool real = row < j.rows;
-                mx_load_edge8<TYPE>((const E *)j.x + (real ? row : 0) * j.ldx, c0 + c, real ? j.cols : 0, v[k]);
+                for (int k = 0; k < 4; ++k) {
+                    const int row = r0 + 4 * four + k;
+                    const bool real = row < j.rows;
+                    mx_load_edge8<TYPE>((const E *)j.x + (real ? row : 0) * j.ldx, c0 + c, real ? j.cols : 0, v[k]);
+                }
+            }
+            if (j.fold)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int row = r0 + 4 * four + k;
+                    const float f = row < j.rows ? j.fold[row] : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k][i] *= f;
+                }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float s = scale[c + i], inv = inverse[c + i];
+                uint32_t q[4];
+                float rests = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float rest;
+                    q[k] = i8_bits(v[k][i], s, inv, rest);
+                    rests = fmaxf(rests, rest);
+                }
+                if (__builtin_expect(2.0f * rests >= s, 0)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) q[k] = i8_bits_at_border(v[k][i], s, inv);
+                }
+                if constexpr (PIECES == 2) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[k] = q[k] + 128;   // its second byte
+                    const uint32_t high = __builtin_amdgcn_perm(__builtin_amdgcn_perm(h[3], h[2], 0x0c0c0501),
+                                                                __builtin_amdgcn_perm(h[1], h[0], 0x0c0c0501), 0x05040100);
+                    tile[0][c + i][word(c + i, four)] = s == s ? high : 0;
+                }
+                const uint32_t low = __builtin_amdgcn_perm(__builtin_amdgcn_perm(q[3], q[2], 0x0c0c0400),
+                                                           __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400), 0x05040100);
+                tile[PIECES - 1][c + i][word(c + i, four)] = s == s ? low : 0;
             }
         }
-        if (j.fold)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int row = r0 + 4 * four + k;
-                const float f = row < j.rows ? j.fold[row] : 1.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[k][i] *= f;
-            }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float s = scale[c + i], inv = inverse[c + i];
-            uint32_t n[4];
-            float most = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float rest;
-                n[k] = i8_bits(v[k][i], s, inv, rest);
-                most = fmaxf(most, rest);
-            }
-            if (__builtin_expect(2.0f * most >= s, 0)) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) n[k] = i8_bits_at_border(v[k][i], s, inv);
-            }
-            if constexpr (PIECES == 2) {
-                uint32_t h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = n[k] + 128;   // its second byte
-                const uint32_t high = __builtin_amdgcn_perm(__builtin_amdgcn_perm(h[3], h[2], 0x0c0c0501),
-                                                            __builtin_amdgcn_perm(h[1], h[0], 0x0c0c0501), 0x05040100);
-                tile[0][c + i][four] = s == s ? high : 0;
-            }
-            const uint32_t low = __builtin_amdgcn_perm(__builtin_amdgcn_perm(n[3], n[2], 0x0c0c0400),
-                                                       __builtin_amdgcn_perm(n[1], n[0], 0x0c0c0400), 0x05040100);
-            tile[PIECES - 1][c + i][four] = s == s ? low : 0;
+        __syncthreads();
+        for (int i = tid / QUADS; i < PIECES * 128; i += 256 / QUADS) {
+            const int piece = i >> 7, n = i & 127, column = c0 + n, quad = tid % QUADS;
+            if (column >= j.cols) continue;
+            const int64_t row = PIECES == 2 ? (int64_t)(column >> 5) * 64 + piece * 32 + (column & 31) : column;
+            *(uint4 *)(j.q + row * ld + r0 + 16 * quad) = *(const uint4 *)&tile[piece][n][word(n, 4 * quad)];
         }
     }
-    __syncthreads();
-    for (int i = tid >> 5; i < PIECES * 128; i += 8) {
-        const int piece = i >> 7, n = c0 + (i & 127);
-        if (n >= j.cols) continue;
-        const int64_t row = PIECES == 2 ? (int64_t)(n >> 5) * 64 + piece * 32 + (n & 31) : n;
-        *(uint32_t *)(j.q + row * ld + r0 + 4 * (tid & 31)) = tile[piece][i & 127][tid & 31];
+}
+
+// The largest of `per` parts each.
+__global__ __launch_bounds__(256) void i8_join_kernel(const uint32_t *part, uint32_t *out, int parts, int per, int ld) {
+    const int c = blockIdx.x * 256 + threadIdx.x, first = blockIdx.y * per, end = first + per < parts ? first + per : parts;
+    if (c >= ld) return;
+    uint32_t m = 0;
+#pragma unroll 8
+    for (int p = first; p < end; ++p) m = i8_max(m, part[(int64_t)p * ld + c]);
+    out[(int64_t)blockIdx.y * ld + c] = m;
+}
+
+// ---- a gradient, both ways ----
+//
+// One pass over dY (where its rows fit): each value times its column's scale,
+// by row in 8 bits; and the columns' largest magnitudes of each value times its
+// row's scale, over the rows of a workgroup, for i8_cols_kernel.
+
+// A workgroup of 512 takes kBothRows rows at a time, each lane eight columns of
+// them (or, KEEP = false, of several runs of 4096 columns, read twice).
+constexpr int kBothRows = 8;
+
+template <int TYPE, bool KEEP>
+__global__ __launch_bounds__(512) void i8_both_kernel(I8BothJob j, int groups) {
+    typedef typename MxType<TYPE>::T E;
+    constexpr int R = kBothRows;
+    __shared__ uint32_t most[8][R];
+    __shared__ float scale[R], inverse[R];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int ld = (int)i8_ld(j.cols), runs = KEEP ? 1 : (ld + 4095) / 4096;
+    for (int group = blockIdx.x; group < groups; group += gridDim.x) {
+        const int r0 = group * R;
+        I8Raw<TYPE> raw[R];
+        float w[8];
+        const auto load = [&](int run) {
+            const int c = 4096 * run + 8 * tid;
+            mx_load_edge8<SGEMM_TYPE_F32>(j.by_col, c, j.cols, w);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                I8Raw<TYPE> one[1];
+                i8_load_row<TYPE>((const E *)j.x + (r0 + r < j.rows ? r0 + r : 0) * j.ldx, c, 0, r0 + r < j.rows ? j.cols : 0, one);
+                raw[r] = one[0];
+            }
+        };
+        uint32_t rm[R] = {};
+        for (int run = 0; run < runs; ++run) {
+            load(run);
+            uint32_t cm[8] = {};
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float v[8];
+                raw[r].get(v);
+                const float f = r0 + r < j.rows ? j.by_row[r0 + r] : 1.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    rm[r] = i8_max(rm[r], i8_magnitude(v[i] * w[i]));
+                    cm[i] = i8_max(cm[i], i8_magnitude(v[i] * f));
+                }
+            }
+            const int c = 4096 * run + 8 * tid;
+            if (c < ld) {
+                uint4 *p = (uint4 *)(j.part + (int64_t)blockIdx.x * ld + c);
+                if (group != (int)blockIdx.x) {   // this thread's own, of the rows before
+                    const uint4 a = p[0], b = p[1];
+                    cm[0] = i8_max(cm[0], a.x), cm[1] = i8_max(cm[1], a.y), cm[2] = i8_max(cm[2], a.z), cm[3] = i8_max(cm[3], a.w);
+                    cm[4] = i8_max(cm[4], b.x), cm[5] = i8_max(cm[5], b.y), cm[6] = i8_max(cm[6], b.z), cm[7] = i8_max(cm[7], b.w);
+                }
+                p[0] = uint4{cm[0], cm[1], cm[2], cm[3]};
+                p[1] = uint4{cm[4], cm[5], cm[6], cm[7]};
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint32_t m = i8_max16(rm[r]);
+            m = i8_max(m, __shfl_xor(m, 16, 64));
+            m = i8_max(m, __shfl_xor(m, 32, 64));
+            if (lane == 0) most[wave][r] = m;
+        }
+        __syncthreads();
+        if (tid < R) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = i8_max(m, most[i][tid]);
+            const float s = i8_scale(m, kI8Levels);
+            scale[tid] = s;
+            inverse[tid] = 1.0f / s;
+            if (r0 + tid < j.rows) j.s[r0 + tid] = s;
+        }
+        __syncthreads();
+        for (int run = 0; run < runs; ++run) {
+            if (!KEEP) load(run);
+            const int c = 4096 * run + 8 * tid;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (c < ld && r0 + r < j.rows) {
+                    float v[8];
+                    raw[r].get(v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] *= w[i];
+                    *(uint2 *)(j.q + (int64_t)(r0 + r) * ld + c) = i8_nearest8(v, scale[r], inverse[r]);
+                }
+        }
+        // (the next group writes `most` again only after its loads, and `scale` behind a barrier)
     }
 }
 
@@ -252,15 +351,51 @@ hipError_t rows_type(const I8RowsJob &j, const I8RowsJob &k, hipStream_t s) {
     return rows<TYPE, 16>(j, k, s);
 }
 
+// Tiles of 64 rows, or 128 where there are many.
+template <int TYPE, int PIECES>
+hipError_t cols_tiles(I8ColsJob j, int parts, hipStream_t s) {
+    const int across = (int)(i8_ld(j.cols) / 128), down = (int)(i8_ld(j.rows) / 128);
+    const bool many = (int64_t)across * down >= 512;
+    void *params[] = {&j, &parts};
+    return hipLaunchKernel(many ? (const void *)i8_cols_kernel<TYPE, PIECES, 128> : (const void *)i8_cols_kernel<TYPE, PIECES, 64>,
+                           dim3((unsigned)across, (unsigned)(many ? down : 2 * down)), dim3(256), params, 0, s);
+}
+
 template <int TYPE>
 hipError_t cols_type(const I8ColsJob &job, hipStream_t s) {
     I8ColsJob j = job;
     void *params[] = {&j};
-    const unsigned across = (unsigned)(i8_ld(j.cols) / 128), down = (unsigned)(i8_ld(j.rows) / 128);
-    const hipError_t e = hipLaunchKernel((const void *)i8_part_kernel<TYPE>, dim3(across, (unsigned)parts_of(j.rows)), dim3(256), params, 0, s);
+    const hipError_t e = hipLaunchKernel((const void *)i8_part_kernel<TYPE>, dim3((unsigned)(i8_ld(j.cols) / 128), (unsigned)parts_of(j.rows)),
+                                         dim3(256), params, 0, s);
+    return e == hipSuccess ? cols_tiles<TYPE, 1>(j, parts_of(j.rows), s) : e;
+}
+
+// Two workgroups of i8_both_kernel on a CU, each with largest magnitudes of its
+// own; where they are many they are joined to kJoined first: every workgroup
+// of i8_cols_kernel reads them all.
+constexpr int kMostBoth = 512, kJoined = 16;
+int both_parts(int rows) {
+    const int groups = (rows + kBothRows - 1) / kBothRows;
+    return groups < kMostBoth ? groups : kMostBoth;
+}
+
+template <int TYPE>
+hipError_t both_type(I8BothJob j, hipStream_t s) {
+    int groups = (j.rows + kBothRows - 1) / kBothRows, parts = both_parts(j.rows), ld = (int)i8_ld(j.cols);
+    void *params[] = {&j, &groups};
+    hipError_t e = hipLaunchKernel(j.cols <= 4096 ? (const void *)i8_both_kernel<TYPE, true> : (const void *)i8_both_kernel<TYPE, false>,
+                                   dim3((unsigned)parts), dim3(512), params, 0, s);
     if (e != hipSuccess) return e;
-    return hipLaunchKernel(j.pieces == 2 ? (const void *)i8_cols_kernel<TYPE, 2> : (const void *)i8_cols_kernel<TYPE, 1>, dim3(across, down),
-                           dim3(256), params, 0, s);
+    uint32_t *part = j.part;
+    if (parts > 4 * kJoined) {
+        int per = (parts + kJoined - 1) / kJoined;
+        part += (int64_t)parts * ld;
+        void *join[] = {&j.part, &part, &parts, &per, &ld};
+        e = hipLaunchKernel((const void *)i8_join_kernel, dim3((unsigned)((ld + 255) / 256), (unsigned)((parts + per - 1) / per)), dim3(256), join, 0, s);
+        if (e != hipSuccess) return e;
+        parts = (parts + per - 1) / per;
+    }
+    return cols_tiles<TYPE, 2>({j.x, j.ldx, j.rows, j.cols, TYPE, j.by_row, part, j.qt, j.st}, parts, s);
 }
 
 template <int TYPE>
@@ -280,6 +415,7 @@ hipError_t back_type(const I8BackJob &job, hipStream_t s) {
 }  // namespace
 
 int64_t i8_part_bytes(int rows, int cols) { return rows > 0 ? parts_of(rows) * i8_ld(cols) * 4 : 0; }
+int64_t i8_both_part_bytes(int rows, int cols) { return (int64_t)(both_parts(rows) + kJoined) * i8_ld(cols) * 4; }
 
 #define I8_BY_TYPE(type, call)                          \
     switch (type) {                                     \
@@ -303,6 +439,12 @@ hipError_t launch_i8_rows(const I8RowsJob &j, hipStream_t s) {
 
 hipError_t launch_i8_cols(const I8ColsJob &j, hipStream_t s) {
 #define CALL(T) cols_type<T>(j, s)
+    I8_BY_TYPE(j.type, CALL)
+#undef CALL
+}
+
+hipError_t launch_i8_both(const I8BothJob &j, hipStream_t s) {
+#define CALL(T) both_type<T>(j, s)
     I8_BY_TYPE(j.type, CALL)
 #undef CALL
 }
