@@ -261,6 +261,8 @@ hipError_t launch_i8_both(const I8BothJob &j, hipStream_t s);
 hipError_t launch_i8_groups(const I8GroupsJob &j, hipStream_t s);
 hipError_t launch_i8_back(const I8BackJob &j, hipStream_t s);
 hipError_t launch_i8_gemm(const I8GemmJob &j, int num_cus, hipStream_t s);
+// Two products, down, the second with pieces = 2 (and a result in fp32).
+hipError_t launch_i8_gemm_two(const I8GemmJob &j, const I8GemmJob &k, int num_cus, hipStream_t s);
 // The same for at most kI8ThinRows rows of A or B (not down, one piece): weights
 // streamed past tokens.  floats: A is quantised on the way (type j.type, leading
 // dimension ldx).

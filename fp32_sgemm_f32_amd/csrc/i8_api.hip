@@ -211,12 +211,12 @@ SGEMM_API int sgemm_f32_i8_train_backward(int M, int N, int K, int type, const v
     hipError_t e = hipSuccess;
     if (d)
         e = launch_i8_both({dY, ldd, M, N, type, (const float *)sw, (const float *)sx, (uint32_t *)(p + at.part), dq, sd, tq, st}, stream);
-    if (x && e == hipSuccess)
-        e = launch_i8_gemm({dq, N > 0 ? sd : nullptr, (const int8_t *)wq, nullptr, M, K, N, type, 1, 1, N > 0 ? 1.0f : 0.0f, 0.0f, dX, lddx},
-                           cus, stream);
-    if (w && e == hipSuccess)
-        e = launch_i8_gemm({tq, M > 0 ? st : nullptr, (const int8_t *)xq, nullptr, N, K, M, SGEMM_TYPE_F32, 1, 2, M > 0 ? 1.0f : 0.0f, beta,
-                            dW, lddw}, cus, stream);
+    const I8GemmJob gx{dq, N > 0 ? sd : nullptr, (const int8_t *)wq, nullptr, M, K, N, type, 1, 1, N > 0 ? 1.0f : 0.0f, 0.0f, dX, lddx};
+    const I8GemmJob gw{tq, M > 0 ? st : nullptr, (const int8_t *)xq, nullptr, N, K, M, SGEMM_TYPE_F32, 1, 2, M > 0 ? 1.0f : 0.0f, beta, dW, lddw};
+    if (e == hipSuccess) e = x && w ? launch_i8_gemm_two(gx, gw, cus, stream)
+                             : x    ? launch_i8_gemm(gx, cus, stream)
+                             : w    ? launch_i8_gemm(gw, cus, stream)
+                                    : hipSuccess;
     return done(e);
 }
 

@@ -285,56 +285,74 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
     float sb[TL::FN];
 #pragma unroll
     for (int k = 0; k < TL::FN; ++k) sb[k] = g.sb && col + APART * k < g.N ? g.sb[col + APART * k] : 1.0f;
-    const auto write = [&](auto masked) {
-        constexpr bool MASKED = decltype(masked)::value;
-        const bool wide = !DOWN && (!MASKED || col + TL::FN <= g.N);
+    // What is masked: nothing, rows, or rows and columns (then stores are one value wide).
+    const auto write = [&](auto mask_c, auto beta_c) {
+        constexpr int MASK = decltype(mask_c)::value;
+        constexpr bool BETA = decltype(beta_c)::value, WIDE = !DOWN && MASK < 2;
+        typedef Vec<TL::FN, T> V;
 #pragma unroll
         for (int i = 0; i < TL::FM; i += PIECES)
 #pragma unroll
             for (int r4 = 0; r4 < 4; ++r4) {
-                const int first = (wm * TL::WTM + 32 * i) / PIECES + 8 * r4 + 4 * h;
+                const int first = (wm * TL::WTM + 32 * i) / PIECES + 8 * r4 + 4 * h, row = m0 / PIECES + first;
                 const f32v4 sa = *(const f32v4 *)(scales + first);
+                T *const p = (T *)g.c + row * g.ldc + col;
+                V old[4] = {};
+                if constexpr (BETA) {
 #pragma unroll
-                for (int r1 = 0; r1 < 4; ++r1) {
-                    const int row = m0 / PIECES + first + r1, r = 4 * r4 + r1;
-                    if (MASKED && row >= g.M) continue;
-                    float v[TL::FN];
+                    for (int r = 0; r < 4; ++r) {
+                        if (MASK > 0 && row + r >= g.M) continue;
+                        if constexpr (WIDE) old[r] = *(const V *)(p + r * g.ldc);
+                        else
+#pragma unroll
+                            for (int k = 0; k < TL::FN; ++k)
+                                if (MASK < 2 || col + APART * k < g.N) old[r].v[k] = p[r * g.ldc + APART * k];
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    V out;
 #pragma unroll
                     for (int k = 0; k < TL::FN; ++k) {
-                        float sum = (float)acc[i][k][r];
-                        if constexpr (PIECES == 2) sum = fmaf(256.0f, sum, (float)acc[i + 1][k][r]);
-                        v[k] = g.alpha * scaled(sum, sa[r1], sb[k]);
+                        float sum = (float)acc[i][k][4 * r4 + r];
+                        if constexpr (PIECES == 2) sum = fmaf(256.0f, sum, (float)acc[i + 1][k][4 * r4 + r]);
+                        float v = g.alpha * scaled(sum, sa[r], sb[k]);
+                        if constexpr (BETA) v += g.beta * MxType<TYPE>::load(&old[r].v[k]);
+                        out.v[k] = MxType<TYPE>::from(v);
                     }
-                    T *p = (T *)g.c + row * g.ldc + col;
-                    if (wide) {
-                        Vec<TL::FN, T> out;
-                        if (g.beta != 0.0f) {
-                            const Vec<TL::FN, T> old = *(const Vec<TL::FN, T> *)p;
-#pragma unroll
-                            for (int k = 0; k < TL::FN; ++k) v[k] += g.beta * MxType<TYPE>::load(&old.v[k]);
-                        }
-#pragma unroll
-                        for (int k = 0; k < TL::FN; ++k) out.v[k] = MxType<TYPE>::from(v[k]);
-                        store<TL::BM >= 256>((Vec<TL::FN, T> *)p, out);
-                    } else {
+                    if (MASK > 0 && row + r >= g.M) continue;
+                    if constexpr (WIDE) *(V *)(p + r * g.ldc) = out;
+                    else
 #pragma unroll
                         for (int k = 0; k < TL::FN; ++k)
-                            if (!MASKED || col + APART * k < g.N) {
-                                if (g.beta != 0.0f) v[k] += g.beta * MxType<TYPE>::load(p + APART * k);
-                                p[APART * k] = MxType<TYPE>::from(v[k]);
-                            }
-                    }
+                            if (MASK < 2 || col + APART * k < g.N) p[r * g.ldc + APART * k] = out.v[k];
                 }
             }
     };
     if (set > 0) return;
-    if (m0 / PIECES + ROWS <= g.M && n0 + TL::BN <= g.N) write(std::false_type{});
-    else write(std::true_type{});
+    const auto masked = [&](auto beta_c) {
+        if (n0 + TL::BN > g.N) write(std::integral_constant<int, 2>{}, beta_c);
+        else if (m0 / PIECES + ROWS > g.M) write(std::integral_constant<int, 1>{}, beta_c);
+        else write(std::integral_constant<int, 0>{}, beta_c);
+    };
+    if (g.beta != 0.0f) masked(std::true_type{});
+    else masked(std::false_type{});
 }
 
 template <class TL, int TYPE, bool DOWN, int PIECES>
 __global__ __launch_bounds__(TL::NT, 1) void i8_gemm_kernel(Args g) {
     compute_tile<TL, TYPE, DOWN, PIECES>(g, blockIdx.x);
+}
+
+// Two products, down, the second of pairs with a result in fp32, in one launch:
+// the first `head` workgroups compute g, or k if k_first, the others the other.
+template <class TL, class PAIRS, int TYPE>
+__global__ __launch_bounds__(TL::NT, 1) void i8_gemm_two_kernel(Args g, Args k, int head, bool k_first) {
+    static_assert(TL::NT == PAIRS::NT, "one size of workgroups");
+    const bool early = (int)blockIdx.x < head;
+    const int block = early ? blockIdx.x : blockIdx.x - head;
+    if (early == k_first) compute_tile<PAIRS, SGEMM_TYPE_F32, true, 2>(k, block);
+    else compute_tile<TL, TYPE, true, 1>(g, block);
 }
 
 typedef Tile<256, 256, 2, 4, 2> T256;       // 8 waves of 128 x 64, 128 KiB
@@ -343,9 +361,7 @@ typedef Tile<128, 128, 2, 4, 4> T128Deep;   // the same, 128 KiB
 typedef Tile<64, 64, 2, 2, 4> T64;          // 4 waves of 32 x 32, 64 KiB
 typedef Tile<64, 32, 2, 1, 4, 2> T64x32;    // 2 x 2 waves of 32 x 32, 96 KiB
 typedef Tile<32, 32, 1, 1, 4, 2> T32;       // 2 waves of 32 x 32, 64 KiB
-// With fragments in pairs.
-typedef Tile<64, 64, 1, 2, 4> T64Pairs;        // 2 waves of 64 x 32
-typedef Tile<64, 32, 1, 1, 4, 2> T64x32Pairs;  // 2 waves of 64 x 32
+typedef Tile<128, 64, 2, 2, 3> T64Pairs;    // for fragments in pairs: 4 waves of 64 x 32, 72 KiB
 
 template <class TL>
 Args arguments(const I8GemmJob &j) {
@@ -362,7 +378,7 @@ hipError_t launch_tile(const I8GemmJob &j, hipStream_t s) {
                            TL::KS * TL::RING, s);
 }
 
-enum Kind { k256, k128, k128Deep, k64, k64x32, k32 };
+enum Kind { k256, k128, k128Deep, k64, k64x32, k32 };   // pairs: no k64x32, no k32
 
 Kind kind_of(const I8GemmJob &j, int num_cus) {
     const int64_t rows = j.pieces == 2 ? i8_piece_rows(j.M) : j.M;
@@ -384,6 +400,7 @@ Kind kind_of(const I8GemmJob &j, int num_cus) {
     if (j.pieces == 1 && (rows <= 32 || j.N <= 32)) return k32;
     if (tiles(128, 128) > num_cus) return k128;
     if (2 * tiles(128, 128) > num_cus) return k128Deep;
+    if (j.pieces == 2) return k64;
     // Up to one tile of 64 x 32 for a CU: two sets of waves, each with a ring of
     // its own, take every other chunk of K (128 x 4096 x 4096: 10.4 us against 12.8;
     // 400 x 1000 x 8192: 12.8 against 18.4; 200 x 300 x 700: 6.2 against 6.5).
@@ -392,16 +409,44 @@ Kind kind_of(const I8GemmJob &j, int num_cus) {
 
 template <int TYPE, bool DOWN, int PIECES>
 hipError_t launch_form(const I8GemmJob &j, int num_cus, hipStream_t s) {
-    switch (kind_of(j, num_cus)) {
+    const Kind kind = kind_of(j, num_cus);
+    switch (kind) {
     case k256: return launch_tile<T256, TYPE, DOWN, PIECES>(j, s);
     case k128: return launch_tile<T128, TYPE, DOWN, PIECES>(j, s);
     case k128Deep: return launch_tile<T128Deep, TYPE, DOWN, PIECES>(j, s);
     case k64: return launch_tile<std::conditional_t<PIECES == 2, T64Pairs, T64>, TYPE, DOWN, PIECES>(j, s);
-    case k64x32: return launch_tile<std::conditional_t<PIECES == 2, T64x32Pairs, T64x32>, TYPE, DOWN, PIECES>(j, s);
-    default:
-        if constexpr (PIECES == 1) return launch_tile<T32, TYPE, DOWN, PIECES>(j, s);
-        return hipErrorInvalidValue;
+    default: break;
     }
+    if constexpr (PIECES == 1) {
+        if (kind == k64x32) return launch_tile<T64x32, TYPE, DOWN, PIECES>(j, s);
+        return launch_tile<T32, TYPE, DOWN, PIECES>(j, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+template <class TL, class PAIRS, int TYPE>
+hipError_t launch_two(const I8GemmJob &first, const I8GemmJob &second, hipStream_t s) {
+    Args g = arguments<TL>(first), k = arguments<PAIRS>(second);
+    bool k_first = k.K > g.K;   // the longer tiles begin
+    const int tiles_g = g.tiles_m * g.tiles_n, tiles_k = k.tiles_m * k.tiles_n;
+    int head = k_first ? tiles_k : tiles_g;
+    void *params[] = {&g, &k, &head, &k_first};
+    constexpr int bytes = TL::KS * TL::RING > PAIRS::KS * PAIRS::RING ? TL::KS * TL::RING : PAIRS::KS * PAIRS::RING;
+    return hipLaunchKernel((const void *)i8_gemm_two_kernel<TL, PAIRS, TYPE>, dim3((unsigned)(tiles_g + tiles_k)), dim3(TL::NT), params, bytes, s);
+}
+
+// The products of a backward pass share a launch where they take like tiles: no
+// CU idles between the end of one and the beginning of the other.
+template <int TYPE>
+hipError_t launch_pair(const I8GemmJob &j, const I8GemmJob &k, int num_cus, hipStream_t s) {
+    const Kind a = kind_of(j, num_cus), b = kind_of(k, num_cus);
+    if (a == k256 && b == k256) return launch_two<T256, T256, TYPE>(j, k, s);
+    if (a == k128 && b == k128) return launch_two<T128, T128, TYPE>(j, k, s);
+    const auto tiles = [](int64_t m, int64_t n, int bm, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
+    if (a >= k128Deep && b >= k128Deep && tiles(j.M, j.N, 64, 64) + tiles(i8_piece_rows(k.M), k.N, 128, 64) <= 3 * num_cus)
+        return launch_two<T64, T64Pairs, TYPE>(j, k, s);
+    const hipError_t e = launch_form<TYPE, true, 1>(j, num_cus, s);
+    return e == hipSuccess ? launch_form<SGEMM_TYPE_F32, true, 2>(k, num_cus, s) : e;
 }
 
 }  // namespace
@@ -413,6 +458,15 @@ hipError_t launch_i8_gemm(const I8GemmJob &j, int num_cus, hipStream_t s) {
     case SGEMM_TYPE_F32: return j.down ? launch_form<SGEMM_TYPE_F32, true, 1>(j, num_cus, s) : launch_form<SGEMM_TYPE_F32, false, 1>(j, num_cus, s);
     case SGEMM_TYPE_BF16: return j.down ? launch_form<SGEMM_TYPE_BF16, true, 1>(j, num_cus, s) : launch_form<SGEMM_TYPE_BF16, false, 1>(j, num_cus, s);
     case SGEMM_TYPE_F16: return j.down ? launch_form<SGEMM_TYPE_F16, true, 1>(j, num_cus, s) : launch_form<SGEMM_TYPE_F16, false, 1>(j, num_cus, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_i8_gemm_two(const I8GemmJob &j, const I8GemmJob &k, int num_cus, hipStream_t s) {
+    switch (j.type) {
+    case SGEMM_TYPE_F32: return launch_pair<SGEMM_TYPE_F32>(j, k, num_cus, s);
+    case SGEMM_TYPE_BF16: return launch_pair<SGEMM_TYPE_BF16>(j, k, num_cus, s);
+    case SGEMM_TYPE_F16: return launch_pair<SGEMM_TYPE_F16>(j, k, num_cus, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -75,6 +75,14 @@ def _size(rows, cols):
         raise ValueError(f"a {rows} x {cols} matrix holds more than {MAX_VALUES} values")
 
 
+@functools.lru_cache(maxsize=4096)
+def _layout(rows, cols, group):
+    """(bytes of the values, of both arrays); refuses what no matrix can be."""
+    _size(rows, cols)
+    ld = _ld(cols)
+    return rows * ld, rows * ld + 4 * rows * (ld // 128 if group else 1)
+
+
 class I8:
     """A rows x cols matrix of signed bytes with a float scale for each row, or for each 128 columns of a row.
 
@@ -108,19 +116,12 @@ class I8:
         q._values, q._scales, q._base, q._at, q.shape, q.group = None, None, base, at, (rows, cols), group
         return q
 
-    @staticmethod
-    def _bytes(rows, cols, group=None):
-        """Bytes of both arrays (the values' are a multiple of 128)."""
-        ld = _ld(cols)
-        return rows * ld + 4 * rows * (ld // 128 if group else 1)
-
     def _view(self):
         rows, cols = self.shape
-        n, shape = rows * _ld(cols), _scales(rows, cols, self.group)
-        m = 4 * rows * (shape[1] if self.group else 1)
+        n, end = _layout(rows, cols, self.group)
         torch = mx4._h().torch
         self._values = self._base[self._at:self._at + n].view(torch.int8).view(rows, _ld(cols))
-        self._scales = self._base[self._at + n:self._at + n + m].view(torch.float32).view(shape)
+        self._scales = self._base[self._at + n:self._at + end].view(torch.float32).view(_scales(rows, cols, self.group))
 
     @property
     def values(self):
@@ -142,7 +143,7 @@ class I8:
         if self._base is None:
             return self._values.data_ptr(), self._scales.data_ptr()
         p = self._base.data_ptr() + self._at
-        return p, p + self.shape[0] * _ld(self.shape[1])
+        return p, p + _layout(*self.shape, self.group)[0]
 
     def record_stream(self, stream):
         for t in (self._values, self._scales) if self._base is None else (self._base,):
@@ -167,16 +168,13 @@ def _held(q, name, device=None, group=None):
 
 
 def _new(run, rows, cols, group=None):
-    _size(rows, cols)
-    return I8._of(run.bytes(I8._bytes(rows, cols, group)), 0, rows, cols, group)
+    return I8._of(run.bytes(_layout(rows, cols, group)[1]), 0, rows, cols, group)
 
 
 def _two(run, shape, other, group=None):
     """Two new matrices in one allocation."""
-    _size(*shape)
-    _size(*other)
-    at = (I8._bytes(*shape, group) + 255) // 256 * 256
-    base = run.bytes(at + I8._bytes(*other, group))
+    at = (_layout(*shape, group)[1] + 255) // 256 * 256
+    base = run.bytes(at + _layout(*other, group)[1])
     return I8._of(base, 0, *shape, group), I8._of(base, at, *other, group)
 
 
@@ -211,11 +209,11 @@ def i8_quantize(X, group=None, stream=None):
     trans = group is None and mx4._column_major(X)
     ty, ld = mx4._floats(X.t() if trans else X, "X")
     rows, cols = X.shape
-    _size(rows, cols)
+    _layout(rows, cols, group)
     run = mx4._Run(X.device, stream)
     need = 0
     if trans:
-        _size(cols, rows)
+        _layout(cols, rows, None)
         need = _scratch("quantize_scratch", 1, rows, cols)
     scratch = run.bytes(need) if need else None
     q = _new(run, rows, cols, group)
@@ -269,7 +267,7 @@ def i8_linear(X, W, out=None, stream=None):
     if K != K2:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
     _sum(K)
-    _size(M, K)
+    _layout(M, K, None)
     need = _scratch("linear_scratch", M, N, K, ty)
     run = mx4._Run(device, stream)
     out, _, ldy = mx4._out(run, out, (M, N), X.dtype)
@@ -279,6 +277,7 @@ def i8_linear(X, W, out=None, stream=None):
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def _train_sizes(M, N, K):
     for n in (M, N, K):
         _sum(n)
