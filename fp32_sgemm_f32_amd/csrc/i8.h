@@ -172,6 +172,13 @@ __device__ __forceinline__ I8Place i8_place(int chunks, int threads) {
 }
 inline unsigned i8_grid(int64_t rows, int64_t chunks, int threads) { return (unsigned)((rows * chunks + threads - 1) / threads); }
 
+// A sum times its row's and its column's scale: the smaller first, which
+// neither overflows nor underflows where the result does not.
+__device__ __forceinline__ float i8_scaled(float sum, float x, float y) {
+    const bool less = x < y;   // (where one is NaN, it comes second)
+    return sum * (less ? x : y) * (less ? y : x);
+}
+
 // ---- host: one job per launcher ----
 
 // Rows of a float matrix, by row (q, s).

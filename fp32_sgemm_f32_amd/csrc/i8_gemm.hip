@@ -55,7 +55,6 @@ template <int BM_, int BN_, int WM_, int WN_, int S_, int KS_ = 1>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, KS = KS_;
     static constexpr int NW = WM * WN, NT = 64 * NW * KS;                            // waves of a set, threads of all
-
     static constexpr int WTM = BM / WM, WTN = BN / WN, FM = WTM / 32, FN = WTN / 32;
     static constexpr int STEPS = kChunk / 32;
     static constexpr int A_BYTES = BM * kChunk, B_BYTES = BN * kChunk, STAGE = A_BYTES + B_BYTES, RING = S * STAGE;
@@ -69,13 +68,6 @@ struct Tile {
     // Rows of BN bytes: 256 / BN of them to all banks.
     __device__ __forceinline__ static int swz_down(int k) { return 2 * ((k / (256 / BN)) & (BN / 32 - 1)); }
 };
-
-// A sum times its row's and its column's scale: the smaller first, which
-// neither overflows nor underflows where the result does not.
-__device__ __forceinline__ float scaled(float sum, float x, float y) {
-    const bool less = x < y;   // (where one is NaN, it comes second)
-    return sum * (less ? x : y) * (less ? y : x);
-}
 
 // The tile of workgroup `block` of the product g.
 template <class TL, int TYPE, bool DOWN, int PIECES>
@@ -132,11 +124,12 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
     int lc = set;   // the chunk that the resources stand at
     advance(ra, (int64_t)set * kChunk);
     advance(rb, set * (DOWN ? kChunk * downb : kChunk));
+    int left_a = (int)(am * rowb) - set * kChunk, left_b = (int)(bn * rowb) - set * kChunk;
+    const int whole = (int)(kChunk * downb), tail = (int)((g.K - (chunks - 1) * kChunk) * downb);   // down: bytes of a chunk, of the last
     auto limits = [&] {
-        const bool in = lc < chunks;
-        ra[2] = in ? (int)(am * rowb - lc * kChunk) : 0;
-        if constexpr (DOWN) rb[2] = in ? (int)((g.K - lc * kChunk < kChunk ? g.K - lc * kChunk : kChunk) * downb) : 0;
-        else rb[2] = in ? (int)(bn * rowb - lc * kChunk) : 0;
+        ra[2] = lc < chunks ? left_a : 0;
+        if constexpr (DOWN) rb[2] = lc < chunks - 1 ? whole : lc < chunks ? tail : 0;
+        else rb[2] = lc < chunks ? left_b : 0;
     };
     limits();
     auto load_one = [&](auto ic, int stage) {
@@ -147,6 +140,8 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
     };
     auto next_chunk = [&] {
         lc += TL::KS;
+        left_a -= TL::KS * kChunk;
+        left_b -= TL::KS * kChunk;
         advance(ra, TL::KS * kChunk);
         advance(rb, TL::KS * (DOWN ? kChunk * downb : kChunk));
         limits();
@@ -316,7 +311,7 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
                     for (int k = 0; k < TL::FN; ++k) {
                         float sum = (float)acc[i][k][4 * r4 + r];
                         if constexpr (PIECES == 2) sum = fmaf(256.0f, sum, (float)acc[i + 1][k][4 * r4 + r]);
-                        float v = g.alpha * scaled(sum, sa[r], sb[k]);
+                        float v = g.alpha * i8_scaled(sum, sa[r], sb[k]);
                         if constexpr (BETA) v += g.beta * MxType<TYPE>::load(&old[r].v[k]);
                         out.v[k] = MxType<TYPE>::from(v);
                     }

@@ -14,8 +14,6 @@
 namespace sgemm {
 namespace {
 
-typedef int i32v4 __attribute__((ext_vector_type(4)));
-
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 template <int TYPE>
 constexpr int kKept = TYPE == SGEMM_TYPE_F32 ? 2 : 4;   // eights of a token that a lane keeps while it looks for the largest
@@ -36,11 +34,6 @@ struct Args {
     void *c;
     int64_t by_row, by_token;   // elements from one row of weights (token) to the next in the result
 };
-
-__device__ __forceinline__ float scaled(float sum, float x, float y) {
-    const bool less = x < y;   // (where one is NaN, it comes second)
-    return sum * (less ? x : y) * (less ? y : x);
-}
 
 template <int TYPE>
 __device__ __forceinline__ void put(const Args &g, int64_t at, float v) {
@@ -175,7 +168,7 @@ __global__ __launch_bounds__(kThreads, 4) void i8_thin_kernel(Args g) {
         int sum = 0;
         for (int k = 0; k < g.wk; ++k) sum += p[k * (G * 128)] + p[k * (G * 128) + 8];
         const float sx = FLOATS >= 0 ? scale[t] : g.sx ? g.sx[t] : 1.0f, sw = g.sw ? g.sw[row] : 1.0f;
-        const float v = g.alpha * scaled((float)sum, sx, sw);
+        const float v = g.alpha * i8_scaled((float)sum, sx, sw);
         const int64_t to = row * g.by_row + t * g.by_token;
         if (g.type == SGEMM_TYPE_F32) put<SGEMM_TYPE_F32>(g, to, v);
         else if (g.type == SGEMM_TYPE_BF16) put<SGEMM_TYPE_BF16>(g, to, v);
