@@ -351,12 +351,16 @@ __global__ __launch_bounds__(TL::NT, 1) void i8_gemm_two_kernel(Args g, Args k, 
 }
 
 typedef Tile<256, 256, 2, 4, 2> T256;       // 8 waves of 128 x 64, 128 KiB
-typedef Tile<128, 128, 2, 4, 2> T128;       // 8 waves of 64 x 32, 64 KiB: two workgroups on a CU
-typedef Tile<128, 128, 2, 4, 4> T128Deep;   // the same, 128 KiB
+typedef Tile<256, 128, 4, 4, 3> T256x128;   // 16 waves of 64 x 32, 144 KiB
+typedef Tile<128, 128, 4, 2, 2> T128;       // 8 waves of 32 x 64, 64 KiB: two workgroups on a CU
+typedef Tile<128, 128, 4, 2, 4> T128Deep;   // the same, 128 KiB
 typedef Tile<64, 64, 2, 2, 4> T64;          // 4 waves of 32 x 32, 64 KiB
 typedef Tile<64, 32, 2, 1, 4, 2> T64x32;    // 2 x 2 waves of 32 x 32, 96 KiB
 typedef Tile<32, 32, 1, 1, 4, 2> T32;       // 2 waves of 32 x 32, 64 KiB
-typedef Tile<128, 64, 2, 2, 3> T64Pairs;    // for fragments in pairs: 4 waves of 64 x 32, 72 KiB
+// For fragments in pairs: waves of 64 x 32.
+typedef Tile<128, 128, 2, 4, 2> T128Pairs;
+typedef Tile<128, 128, 2, 4, 4> T128DeepPairs;
+typedef Tile<128, 64, 2, 2, 3> T64Pairs;    // 72 KiB
 
 template <class TL>
 Args arguments(const I8GemmJob &j) {
@@ -373,50 +377,58 @@ hipError_t launch_tile(const I8GemmJob &j, hipStream_t s) {
                            TL::KS * TL::RING, s);
 }
 
-enum Kind { k256, k128, k128Deep, k64, k64x32, k32 };   // pairs: no k64x32, no k32
+enum Kind { k256, k256x128, k128, k128Deep, k64, k64x32, k32 };   // pairs: k256, k128, k128Deep, k64
 
+// (Times: 1 GiB of different weights in turn, bf16 results, in us.)
 Kind kind_of(const I8GemmJob &j, int num_cus) {
-    const int64_t rows = j.pieces == 2 ? i8_piece_rows(j.M) : j.M;
+    const bool pairs = j.pieces == 2;
+    const int64_t rows = pairs ? i8_piece_rows(j.M) : j.M;
     const auto tiles = [&](int m, int n) { return ((rows + m - 1) / m) * (((int64_t)j.N + n - 1) / n); };
     // The largest tile that gives every CU one and whose rounds leave at most
     // a fifth of the CUs' time unused (272 tiles of 256 x 256, 4352 x 4096 x
-    // 4096: 98.5 us, 96.6 in tiles of 128 x 128, two to a CU; 448 in two rounds,
-    // 7000 x 4096 x 4096: 119 against 137).
+    // 4096: 95.1, 90.5 in tiles of 128 x 128, two to a CU; 8192 x 4096 x 4096: 116
+    // against 156).
     const int64_t rounds = (tiles(256, 256) + num_cus - 1) / num_cus;
     if (tiles(256, 256) >= num_cus && 4 * rounds * num_cus <= 5 * tiles(256, 256)) return k256;
-    // One tile of 128 x 128 for a CU at most: a deep ring hides the memory's
-    // latency (2048 x 2048 x 4096: 23.7 us against 26.6); more, and a second
-    // workgroup hides it (1111 x 4097 x 2050, 297 tiles: 21.4 against 31.0).
-    // With less than half a tile for a CU, smaller ones spread further (200 x
-    // 8192 x 4096, 128 tiles: 17.5 us against 21.4; 1000 x 1000 x 8192, 64: 20.4
-    // against 33.1; but 1024 x 4096 x 4096, 256: 27.8 against 23.7).
-    // At most 32 rows or columns of C: 32 x 4096 x 4096 8.6 us, in tiles of 64 x
-    // 64 14.2, 32 x 28672 x 8192 51 and 54.
-    if (j.pieces == 1 && (rows <= 32 || j.N <= 32)) return k32;
-    if (tiles(128, 128) > num_cus) return k128;
+    // At most 32 rows or columns of C: 32 x 4096 x 4096 8.6, in tiles of 64 x 64
+    // 14.2, 32 x 28672 x 8192 51 and 54.
+    if (!pairs && (rows <= 32 || j.N <= 32)) return k32;
+    // More tiles of 128 x 128 than CUs: two workgroups on a CU hide the memory's
+    // latency, or, where tiles of 256 x 128 go round once, sixteen waves (1111 x
+    // 4097 x 2050: 19.0, 20.8 in tiles of 128 x 128, 24.1 with the deep ring;
+    // 2500 x 2500 x 1000: 14.9, 15.7, 19.0).
+    if (tiles(128, 128) > num_cus) return !pairs && tiles(256, 128) <= num_cus ? k256x128 : k128;
+    // One for a CU at most: a deep ring hides it (2048 x 2048 x 2048: 12.5 against
+    // 17.7; 1024 x 4096 x 4096 22.7 against 32.4).  With less than half a tile for a
+    // CU, smaller ones spread further (200 x 8192 x 4096, 128 tiles: 18.6 against
+    // 24.3; 1000 x 1000 x 8192, 64: 21.8 against 38.6).
     if (2 * tiles(128, 128) > num_cus) return k128Deep;
-    if (j.pieces == 2) return k64;
     // Up to one tile of 64 x 32 for a CU: two sets of waves, each with a ring of
-    // its own, take every other chunk of K (128 x 4096 x 4096: 10.4 us against 12.8;
+    // its own, take every other chunk of K (128 x 4096 x 4096: 10.4 against 12.8;
     // 400 x 1000 x 8192: 12.8 against 18.4; 200 x 300 x 700: 6.2 against 6.5).
-    return tiles(64, 32) <= num_cus ? k64x32 : k64;
+    return !pairs && tiles(64, 32) <= num_cus ? k64x32 : k64;
 }
 
-template <int TYPE, bool DOWN, int PIECES>
+template <int TYPE, bool DOWN>
 hipError_t launch_form(const I8GemmJob &j, int num_cus, hipStream_t s) {
-    const Kind kind = kind_of(j, num_cus);
-    switch (kind) {
-    case k256: return launch_tile<T256, TYPE, DOWN, PIECES>(j, s);
-    case k128: return launch_tile<T128, TYPE, DOWN, PIECES>(j, s);
-    case k128Deep: return launch_tile<T128Deep, TYPE, DOWN, PIECES>(j, s);
-    case k64: return launch_tile<std::conditional_t<PIECES == 2, T64Pairs, T64>, TYPE, DOWN, PIECES>(j, s);
-    default: break;
+    switch (kind_of(j, num_cus)) {
+    case k256: return launch_tile<T256, TYPE, DOWN, 1>(j, s);
+    case k256x128: return launch_tile<T256x128, TYPE, DOWN, 1>(j, s);
+    case k128: return launch_tile<T128, TYPE, DOWN, 1>(j, s);
+    case k128Deep: return launch_tile<T128Deep, TYPE, DOWN, 1>(j, s);
+    case k64: return launch_tile<T64, TYPE, DOWN, 1>(j, s);
+    case k64x32: return launch_tile<T64x32, TYPE, DOWN, 1>(j, s);
+    default: return launch_tile<T32, TYPE, DOWN, 1>(j, s);
     }
-    if constexpr (PIECES == 1) {
-        if (kind == k64x32) return launch_tile<T64x32, TYPE, DOWN, PIECES>(j, s);
-        return launch_tile<T32, TYPE, DOWN, PIECES>(j, s);
+}
+
+hipError_t launch_pairs(const I8GemmJob &j, int num_cus, hipStream_t s) {
+    switch (kind_of(j, num_cus)) {
+    case k256: return launch_tile<T256, SGEMM_TYPE_F32, true, 2>(j, s);
+    case k128: return launch_tile<T128Pairs, SGEMM_TYPE_F32, true, 2>(j, s);
+    case k128Deep: return launch_tile<T128DeepPairs, SGEMM_TYPE_F32, true, 2>(j, s);
+    default: return launch_tile<T64Pairs, SGEMM_TYPE_F32, true, 2>(j, s);
     }
-    return hipErrorInvalidValue;
 }
 
 template <class TL, class PAIRS, int TYPE>
@@ -436,23 +448,23 @@ template <int TYPE>
 hipError_t launch_pair(const I8GemmJob &j, const I8GemmJob &k, int num_cus, hipStream_t s) {
     const Kind a = kind_of(j, num_cus), b = kind_of(k, num_cus);
     if (a == k256 && b == k256) return launch_two<T256, T256, TYPE>(j, k, s);
-    if (a == k128 && b == k128) return launch_two<T128, T128, TYPE>(j, k, s);
+    if ((a == k128 || a == k256x128) && b == k128) return launch_two<T128, T128Pairs, TYPE>(j, k, s);
     const auto tiles = [](int64_t m, int64_t n, int bm, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
     if (a >= k128Deep && b >= k128Deep && tiles(j.M, j.N, 64, 64) + tiles(i8_piece_rows(k.M), k.N, 128, 64) <= 3 * num_cus)
         return launch_two<T64, T64Pairs, TYPE>(j, k, s);
-    const hipError_t e = launch_form<TYPE, true, 1>(j, num_cus, s);
-    return e == hipSuccess ? launch_form<SGEMM_TYPE_F32, true, 2>(k, num_cus, s) : e;
+    const hipError_t e = launch_form<TYPE, true>(j, num_cus, s);
+    return e == hipSuccess ? launch_pairs(k, num_cus, s) : e;
 }
 
 }  // namespace
 
 hipError_t launch_i8_gemm(const I8GemmJob &j, int num_cus, hipStream_t s) {
     if (!j.down && j.K > 0 && i8_thin_takes(j.M, j.N, j.K)) return launch_i8_thin(j, nullptr, 0, num_cus, s);
-    if (j.pieces == 2) return launch_form<SGEMM_TYPE_F32, true, 2>(j, num_cus, s);
+    if (j.pieces == 2) return launch_pairs(j, num_cus, s);
     switch (j.type) {
-    case SGEMM_TYPE_F32: return j.down ? launch_form<SGEMM_TYPE_F32, true, 1>(j, num_cus, s) : launch_form<SGEMM_TYPE_F32, false, 1>(j, num_cus, s);
-    case SGEMM_TYPE_BF16: return j.down ? launch_form<SGEMM_TYPE_BF16, true, 1>(j, num_cus, s) : launch_form<SGEMM_TYPE_BF16, false, 1>(j, num_cus, s);
-    case SGEMM_TYPE_F16: return j.down ? launch_form<SGEMM_TYPE_F16, true, 1>(j, num_cus, s) : launch_form<SGEMM_TYPE_F16, false, 1>(j, num_cus, s);
+    case SGEMM_TYPE_F32: return j.down ? launch_form<SGEMM_TYPE_F32, true>(j, num_cus, s) : launch_form<SGEMM_TYPE_F32, false>(j, num_cus, s);
+    case SGEMM_TYPE_BF16: return j.down ? launch_form<SGEMM_TYPE_BF16, true>(j, num_cus, s) : launch_form<SGEMM_TYPE_BF16, false>(j, num_cus, s);
+    case SGEMM_TYPE_F16: return j.down ? launch_form<SGEMM_TYPE_F16, true>(j, num_cus, s) : launch_form<SGEMM_TYPE_F16, false>(j, num_cus, s);
     default: return hipErrorInvalidValue;
     }
 }
