@@ -23,6 +23,15 @@
 // pieces = 2 (down): A's fragments come in pairs, the high and the low bytes of
 // 16-bit whole numbers; a pair's sums are joined as 256 high + low.
 //
+// Small tiles slice K: KS sets of waves, each with a ring of its own, take every
+// KS-th chunk, and the first adds up the sums.
+//
+// Bound, where tiles are large, by the power the chip may draw: 16384^3 runs in
+// 3510 to 3800 us on different chips (2.3 to 2.5 POPS; the library's product of the
+// same type 2.1), on zeros 8% faster, and a tile's loop at 2.6 POPS, on zeros at
+// 4.3.  Where they are small, by the loads: 60 to 85 GB/s reach a CU, of the 117
+// that such loads reach alone.  LDS conflicts: none (counters).
+//
 // Ring: before the last step of chunk c, whose operands are in registers by
 // then, the waves meet once (loads of chunk c + 1 landed, LDS reads of chunk c
 // done), read the first operands of chunk c + 1, and load chunk c + S into the
@@ -443,7 +452,9 @@ hipError_t launch_two(const I8GemmJob &first, const I8GemmJob &second, hipStream
 }
 
 // The products of a backward pass share a launch where they take like tiles: no
-// CU idles between the end of one and the beginning of the other.
+// CU idles between the end of one and the beginning of the other (333 x 1000 x
+// 1536: 11.4 us, apart 8.3 and 6.3 with what lies between two launches; 8192 x 4096
+// x 4096: 378 against 244 and 139).
 template <int TYPE>
 hipError_t launch_pair(const I8GemmJob &j, const I8GemmJob &k, int num_cus, hipStream_t s) {
     const Kind a = kind_of(j, num_cus), b = kind_of(k, num_cus);

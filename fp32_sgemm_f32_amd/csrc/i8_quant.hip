@@ -11,7 +11,12 @@
 // apart in a matrix of twice the rows (rows 64 b + i hold h, 64 b + 32 + i l of
 // column 32 b + i), which is how a fragment of a matrix instruction takes them.
 //
-// Bound by HBM.
+// Bound by HBM (a copy runs at 5.1 TB/s): 8191 x 16388 floats in groups 129 us (5.2
+// TB/s), back 113 to 129 (5.2 to 6.0); rows of 12288 x 4096 bf16 29 us (5.2); a
+// gradient of 8192 x 4096 bf16 28 us by row with the columns' largest magnitudes
+// (3.9), 4 to join those, 27 by column (4.9).  Rounding once cost twenty
+// instructions a value and was half of a row's time; now it takes five, and
+// looks again only next to a border (i8_bits).
 #include "i8.h"
 
 namespace sgemm {
@@ -19,7 +24,10 @@ namespace {
 
 constexpr int kKeep = 4;   // eights of a row that a lane keeps in registers between the two passes
 
-// WAVES waves take a row; four rows a workgroup where that is one.
+// WAVES waves take a row, few enough that their lanes keep it between the two
+// passes (longer ones are read again); four rows a workgroup where that is one.
+// All loads of a lane are out before it waits for any: with a test for the
+// row's end around each of them 4.3 us for 16 x 4096, now 3.0.
 template <int TYPE, int WAVES>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void i8_rows_kernel(I8RowsJob j0, I8RowsJob j1, int64_t blocks0) {
     constexpr int T = 64 * WAVES, ROWS = WAVES == 1 ? 4 : 1;
@@ -216,6 +224,8 @@ __global__ __launch_bounds__(256) void i8_join_kernel(const uint32_t *part, uint
 // by row in 8 bits; and the columns' largest magnitudes of each value times its
 // row's scale, over the rows of a workgroup, for i8_cols_kernel.
 
+// Eight rows, so that two workgroups fit on a CU and one reads while the other
+// writes (8192 x 4096 bf16: 28 us; sixteen rows and one workgroup 39).
 // A workgroup of 512 takes kBothRows rows at a time, each lane eight columns of
 // them (or, KEEP = false, of several runs of 4096 columns, read twice).
 constexpr int kBothRows = 8;
@@ -371,8 +381,9 @@ hipError_t cols_type(const I8ColsJob &job, hipStream_t s) {
 }
 
 // Two workgroups of i8_both_kernel on a CU, each with largest magnitudes of its
-// own; where they are many they are joined to kJoined first: every workgroup
-// of i8_cols_kernel reads them all.
+// own; where they are many they are joined to kJoined first, in a kernel of 4
+// us: every workgroup of i8_cols_kernel reads them all (8192 x 4096: 27 us so,
+// 42 with 256 of them and four tiles to a workgroup).
 constexpr int kMostBoth = 512, kJoined = 16;
 int both_parts(int rows) {
     const int groups = (rows + kBothRows - 1) / kBothRows;

@@ -9,6 +9,10 @@
 // the second takes half c of token t: entries with p = c are parts of the result
 // (of row r and token t), the others are dropped.  Half of the matrix work is
 // wasted, which is idle otherwise.
+//
+// In a graph, different weights in turn, one token: 4096 x 4096 5.9 us (16.8 MB: 3.3
+// at 5.1 TB/s), from bf16 7.4; 16384 x 4096 14.4 (67 MB: 13.1); 5001 x 16384 21.4 (82
+// MB: 16.0).  Eight: 6.5, 9.5, 15.4, 23.4.
 #include "i8.h"
 
 namespace sgemm {
