@@ -27,9 +27,8 @@
 // KS-th chunk, and the first adds up the sums.
 //
 // Bound, where tiles are large, by the power the chip may draw: 16384^3 runs in
-// 3510 to 3800 us on different chips (2.3 to 2.5 POPS; the library's product of the
-// same type 2.1), on zeros 8% faster, and a tile's loop at 2.6 POPS, on zeros at
-// 4.3.  Where they are small, by the loads: 60 to 85 GB/s reach a CU, of the 117
+// 3470 to 3700 us on different chips (2.4 to 2.5 POPS; the library's product of the
+// same type, 8192^3, at 2.1), and a tile's loop at 2.8 POPS, on zeros at 4.3.  Where they are small, by the loads: 60 to 85 GB/s reach a CU, of the 117
 // that such loads reach alone.  LDS conflicts: none (counters).
 //
 // Ring: before the last step of chunk c, whose operands are in registers by
@@ -88,16 +87,22 @@ __device__ __forceinline__ void compute_tile(const Args &g, int block) {
     const int wm = wave / TL::WN, wn = wave % TL::WN;
 
     // Workgroup -> tile: each XCD (workgroups w, w + 8, ...) takes a
-    // contiguous run of tiles, which go down columns of 8-row groups.
+    // contiguous run of tiles, which go down columns of 8-row groups.  Large
+    // grids are first cut into two by four parts, one for each XCD, where that
+    // goes evenly: what the chip works on at a time is then as many rows as
+    // columns, half of what it reads otherwise (16384^3: 3480 us against 3615; 16384
+    // x 16384 x 4096 920 against 966; 8192^3 the same).
     int tm, tn;
     {
-        const int tiles = g.tiles_m * g.tiles_n, per = tiles >> 3, rest = tiles & 7;
         const int x = block & 7, y = block >> 3;
-        const int t = x * per + (x < rest ? x : rest) + y;
-        const int group = 8 * g.tiles_n, gi = t / group, first = gi * 8;
-        const int rows = g.tiles_m - first < 8 ? g.tiles_m - first : 8;
-        tm = first + (t - gi * group) % rows;
-        tn = (t - gi * group) / rows;
+        const bool parts = g.tiles_m >= 32 && g.tiles_n >= 32 && g.tiles_m % 2 == 0 && g.tiles_n % 4 == 0;
+        const int pm = parts ? g.tiles_m / 2 : g.tiles_m, pn = parts ? g.tiles_n / 4 : g.tiles_n;
+        const int tiles = pm * pn, per = tiles >> 3, rest = tiles & 7;
+        const int t = parts ? y : x * per + (x < rest ? x : rest) + y;
+        const int group = 8 * pn, gi = t / group, first = gi * 8;
+        const int rows = pm - first < 8 ? pm - first : 8;
+        tm = first + (t - gi * group) % rows + (parts ? (x & 1) * pm : 0);
+        tn = (t - gi * group) / rows + (parts ? (x >> 1) * pn : 0);
     }
     const int m0 = tm * TL::BM, n0 = tn * TL::BN;
     const int chunks = (g.K + kChunk - 1) / kChunk;
@@ -400,7 +405,8 @@ Kind kind_of(const I8GemmJob &j, int num_cus) {
     const int64_t rounds = (tiles(256, 256) + num_cus - 1) / num_cus;
     if (tiles(256, 256) >= num_cus && 4 * rounds * num_cus <= 5 * tiles(256, 256)) return k256;
     // At most 32 rows or columns of C: 32 x 4096 x 4096 8.6, in tiles of 64 x 64
-    // 14.2, 32 x 28672 x 8192 51 and 54.
+    // 14.2; 32 x 5001 x 16384 24.8 and 41; 32 x 16384 x 16384 54 and 61, but 32 x
+    // 28672 x 8192 51 and 49.
     if (!pairs && (rows <= 32 || j.N <= 32)) return k32;
     // More tiles of 128 x 128 than CUs: two workgroups on a CU hide the memory's
     // latency, or, where tiles of 256 x 128 go round once, sixteen waves (1111 x

@@ -26,8 +26,7 @@ constexpr int kKeep = 4;   // eights of a row that a lane keeps in registers bet
 
 // WAVES waves take a row, few enough that their lanes keep it between the two
 // passes (longer ones are read again); four rows a workgroup where that is one.
-// All loads of a lane are out before it waits for any: with a test for the
-// row's end around each of them 4.3 us for 16 x 4096, now 3.0.
+// All loads of a lane are out before it waits for any.
 template <int TYPE, int WAVES>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void i8_rows_kernel(I8RowsJob j0, I8RowsJob j1, int64_t blocks0) {
     constexpr int T = 64 * WAVES, ROWS = WAVES == 1 ? 4 : 1;

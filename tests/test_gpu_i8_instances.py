@@ -39,7 +39,8 @@ def want(a, b):
 
 
 # tiles of 256 x 256; 256 x 128; 128 x 128 (two workgroups on a CU, or a deep ring); 64 x 64; 64 x 32 and 32 x 32 (two sets of waves)
-PRODUCTS = [(4096, 4096, 256), (4100, 4090, 130), (4352, 7600, 129), (2100, 2500, 130), (2176, 2560, 384), (2048, 4096, 256), (3000, 3010, 333), (1920, 6272, 130), (2048, 1100, 200), (2100, 1024, 640),
+# ... and grids of tiles that are cut into a part for each XCD
+PRODUCTS = [(4096, 4096, 256), (8192, 8190, 300), (8700, 8900, 130), (4100, 4090, 130), (4352, 7600, 129), (2100, 2500, 130), (2176, 2560, 384), (2048, 4096, 256), (3000, 3010, 333), (1920, 6272, 130), (2048, 1100, 200), (2100, 1024, 640),
             (700, 1300, 333), (704, 1344, 256), (200, 300, 700), (64, 32, 128), (65, 33, 1290), (20, 300, 129), (9, 5000, 1000), (300, 20, 520),
             (32, 64, 256), (5000, 31, 140)]
 
