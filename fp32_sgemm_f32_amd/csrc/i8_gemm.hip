@@ -375,6 +375,9 @@ typedef Tile<32, 32, 1, 1, 4, 2> T32;       // 2 waves of 32 x 32, 64 KiB
 typedef Tile<128, 128, 2, 4, 2> T128Pairs;
 typedef Tile<128, 128, 2, 4, 4> T128DeepPairs;
 typedef Tile<128, 64, 2, 2, 3> T64Pairs;    // 72 KiB
+// Both in 48 KiB: three workgroups on a CU.
+typedef Tile<64, 64, 2, 2, 3> T64Third;
+typedef Tile<128, 64, 2, 2, 2> T64PairsThird;
 
 template <class TL>
 Args arguments(const I8GemmJob &j) {
@@ -458,17 +461,23 @@ hipError_t launch_two(const I8GemmJob &first, const I8GemmJob &second, hipStream
 }
 
 // The products of a backward pass share a launch where they take like tiles: no
-// CU idles between the end of one and the beginning of the other (333 x 1000 x
-// 1536: 11.4 us, apart 8.3 and 6.3 with what lies between two launches; 8192 x 4096
-// x 4096: 378 against 244 and 139).
+// CU idles between the end of one and the beginning of the other (8192 x 4096 x
+// 4096: 378 us against 244 and 139).
 template <int TYPE>
 hipError_t launch_pair(const I8GemmJob &j, const I8GemmJob &k, int num_cus, hipStream_t s) {
     const Kind a = kind_of(j, num_cus), b = kind_of(k, num_cus);
     if (a == k256 && b == k256) return launch_two<T256, T256, TYPE>(j, k, s);
     if ((a == k128 || a == k256x128) && b == k128) return launch_two<T128, T128Pairs, TYPE>(j, k, s);
+    // Small tiles for both.  Up to two workgroups on a CU take the deeper rings
+    // (the whole backward pass of 1024 x 1024 x 1024, 512 tiles: 23.5 us against
+    // 24.2); more fit three to a CU (333 x 1000 x 1536, 528 tiles: 21.7 against 22.9;
+    // 200 x 600 x 3000, 658: 20.0 against 21.8).  Up to some 1300 tiles that is also
+    // faster than two launches (2000 x 500 x 2000, 1280: 37.5 against 41.2; 600 x
+    // 900 x 3000, 1175, the same; 1000 x 800 x 4000, 1827: 43.3 against 42.2).
     const auto tiles = [](int64_t m, int64_t n, int bm, int bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
-    if (a >= k128Deep && b >= k128Deep && tiles(j.M, j.N, 64, 64) + tiles(i8_piece_rows(k.M), k.N, 128, 64) <= 3 * num_cus)
-        return launch_two<T64, T64Pairs, TYPE>(j, k, s);
+    const int64_t small = tiles(j.M, j.N, 64, 64) + tiles(i8_piece_rows(k.M), k.N, 128, 64);
+    if (a >= k128Deep && b >= k128Deep && small <= 5 * num_cus)
+        return small <= 2 * num_cus ? launch_two<T64, T64Pairs, TYPE>(j, k, s) : launch_two<T64Third, T64PairsThird, TYPE>(j, k, s);
     const hipError_t e = launch_form<TYPE, true>(j, num_cus, s);
     return e == hipSuccess ? launch_pairs(k, num_cus, s) : e;
 }

@@ -93,10 +93,11 @@ def test_linear_where_its_choice_changes(dev, m, n, k):
     assert torch.equal(sg.i8_linear(x, w), want(sg.i8_quantize(x), w).bfloat16())
 
 
-# The backward products: both in tiles of 256 x 256, of 128 x 128, in small ones, and apart in each size
+# The backward products: both in tiles of 256 x 256, of 128 x 128, in small ones (two or three workgroups on a CU), and
+# apart in each size
 TRAINS = [(4096, 2048, 4096), (4200, 2100, 4100), (2100, 1100, 2500), (4096, 300, 4096), (100, 2048, 4096), (100, 1100, 2500), (300, 2048, 4096),
           (20, 2048, 4096), (600, 2048, 4096), (1500, 2048, 4096), (700, 513, 900), (333, 1000, 1536), (4096, 100, 4096), (1000, 1000, 3000),
-          (20, 30, 40), (2100, 700, 5000), (9, 4097, 130), (4097, 9, 130), (2500, 4100, 33)]
+          (20, 30, 40), (2100, 700, 5000), (9, 4097, 130), (4097, 9, 130), (2500, 4100, 33), (2000, 500, 2000), (200, 600, 3000), (1024, 1024, 1024), (1000, 800, 4000)]
 
 
 @pytest.mark.parametrize("m, n, k", TRAINS)
