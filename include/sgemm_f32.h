@@ -615,7 +615,8 @@ int sgemm_f32_i8_train_scratch(int M, int N, int K, long long *bytes);
  * gradient of GU (rows x 2 inner, dH's type) with g and u the checkpoint's
  * values and p = 1 / (1 + exp(-g)):
  *     dG = dH * u * p * (1 + g * (1 - p))        dU = dH * g * p
- * All in fp32, rounded once.
+ * In fp32, rounded once; g below -87, where p leaves fp32's normal numbers, in 64
+ * bits: what u and dH make large again is not lost.
  */
 int sgemm_f32_i8_swiglu_forward(int rows, int inner, int type, const void *GU, int ldgu, void *H, int ldh,
                                 void *g_values, void *g_scales, void *u_values, void *u_scales,
