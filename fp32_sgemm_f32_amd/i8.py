@@ -12,6 +12,7 @@ import functools
 from . import mx4
 
 GROUP = 128
+FLOOR = 2.0 ** -126     # the least scale
 MAX_DIM = 1 << 22
 MAX_VALUES = 1 << 34
 MAX_SUM = 1 << 17
@@ -168,14 +169,24 @@ def _held(q, name, device=None, group=None):
 
 
 def _new(run, rows, cols, group=None):
-    return I8._of(run.bytes(_layout(rows, cols, group)[1]), 0, rows, cols, group)
+    q = I8._of(run.bytes(_layout(rows, cols, group)[1]), 0, rows, cols, group)
+    return q if cols else _without_columns(run, q)
 
 
 def _two(run, shape, other, group=None):
-    """Two new matrices in one allocation."""
+    """Two new matrices in one allocation, with equally many columns."""
     at = (_layout(*shape, group)[1] + 255) // 256 * 256
     base = run.bytes(at + _layout(*other, group)[1])
-    return I8._of(base, 0, *shape, group), I8._of(base, at, *other, group)
+    q, p = I8._of(base, 0, *shape, group), I8._of(base, at, *other, group)
+    return (q, p) if shape[1] else (_without_columns(run, q), _without_columns(run, p))
+
+
+def _without_columns(run, q):
+    """q with its scales, those of a largest magnitude of 0: the library neither reads nor writes any there."""
+    if q.group is None:
+        with run.h.torch.cuda.stream(run.other):     # (of None: the current one)
+            q.scales.fill_(FLOOR)
+    return q
 
 
 @functools.lru_cache(maxsize=1024)

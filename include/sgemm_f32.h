@@ -512,7 +512,8 @@ int sgemm_f32_mx4_moe_scratch(int tokens, int hidden, int inner, int experts, in
  *   values  rows x kp signed bytes, kp = cols rounded up to 128; zeros beyond
  *           cols
  *   scales  floats: one for each row (group = 0), or one for each 128 columns
- *           of a row, rows x kp / 128 (group = SGEMM_I8_GROUP)
+ *           of a row, rows x kp / 128 (group = SGEMM_I8_GROUP); without columns
+ *           none: no call reads or writes them then
  * and stands for value * scale.  values must be 16-byte aligned, scales
  * 4-byte aligned.  The products rely on the zeros beyond cols
  * (sgemm_f32_i8_quantize writes them) and on values in [-127, 127].  rows and

@@ -1,5 +1,5 @@
 """Edges of the 8-bit integer operators on the GPU against the 64-bit reference: gates whose exponential leaves fp32's
-range while the result does not."""
+range while the result does not, and matrices without columns."""
 import numpy as np
 import pytest
 import torch
@@ -81,3 +81,44 @@ def test_swiglu_far_gates_of_16_bits(dev, dtype):
     lim = 7 * U * np.abs(want) + np.abs(G * V) * 2.0 ** -275 + 2.0 ** -149
     lim = lim + np.maximum((np.abs(want) + lim) * (f.eps / 2), f.smallest_normal * f.eps / 2)
     assert (np.abs(host(h) - want) <= lim).all()
+
+
+def test_scales_of_matrices_without_columns(dev):
+    """The largest magnitude of nothing is 0, so the scale is the least one: not what the memory held before."""
+    floor = 2.0 ** -126
+
+    def check(q, rows):
+        assert q.values.shape == (rows, 0) and q.scales.shape == (rows,) and q.group is None
+        assert torch.equal(q.scales, torch.full((rows,), floor, device=dev))
+
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        for rows in (1, 5, 100):
+            x, w = torch.ones(rows, 0, device=dev), torch.ones(7, 0, device=dev, dtype=torch.bfloat16)
+            with torch.cuda.stream(stream or torch.cuda.current_stream()):      # memory that held something else
+                dirty = [torch.full((128,), float("nan"), device=dev) for _ in range(8)]
+                del dirty
+            torch.cuda.synchronize()
+            q = sg.i8_quantize(x, stream=stream)
+            _, saved = sg.i8_train_forward(x, w, stream=stream)
+            _, given = sg.i8_train_forward(x, sg.i8_quantize(w, stream=stream), stream=stream)
+            torch.cuda.synchronize()
+            check(q, rows), check(saved[0], rows), check(saved[1], 7), check(given[0], rows), check(given[1], 7)
+            assert sg.i8_quantize(x, group=128).scales.shape == (rows, 0)
+            back = sg.I8(q.values, q.scales, rows, 0)
+            assert torch.equal(sg.i8_gemm(back, given[1]), torch.zeros(rows, 7, device=dev))
+
+
+def test_scales_without_columns_in_a_graph(dev):
+    x = torch.ones(5, 0, device=dev)
+    sg.i8_quantize(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q = sg.i8_quantize(x)
+    scales = q.scales
+    for _ in range(3):
+        scales.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert scales.eq(2.0 ** -126).all()
