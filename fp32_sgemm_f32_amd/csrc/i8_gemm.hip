@@ -28,8 +28,15 @@
 //
 // Bound, where tiles are large, by the power the chip may draw: 16384^3 runs in
 // 3470 to 3700 us on different chips (2.4 to 2.5 POPS; the library's product of the
-// same type, 8192^3, at 2.1), and a tile's loop at 2.8 POPS, on zeros at 4.3.  Where they are small, by the loads: 60 to 85 GB/s reach a CU, of the 117
-// that such loads reach alone.  LDS conflicts: none (counters).
+// same type, 8192^3, at 2.1), at 1.6 GHz with the matrix pipes busy in 76% of the
+// cycles; on zeros, which draw less, in 2850 to 2900 (3.1), at 2.4 GHz and 61%.  The
+// waves wait (for memory, at barriers) in 32% of their cycles, on zeros in 44%.
+// Where tiles are small, by the loads: 60 to 85 GB/s reach a CU, of the 117 that
+// such loads reach alone.  LDS conflicts: none (counters).
+//
+// K is not shared between workgroups: a small result of a long sum has few of
+// them, and each goes through all of K (64 x 64 x 16384 18.6 us, 64 x 64 x 65536
+// 61.4; a backward pass of 65536 x 64 x 64 273).
 //
 // Ring: before the last step of chunk c, whose operands are in registers by
 // then, the waves meet once (loads of chunk c + 1 landed, LDS reads of chunk c

@@ -14,9 +14,11 @@
 // Bound by HBM (a copy runs at 5.1 TB/s): 8191 x 16388 floats in groups 129 us (5.2
 // TB/s), back 113 to 129 (5.2 to 6.0); rows of 12288 x 4096 bf16 29 us (5.2); a
 // gradient of 8192 x 4096 bf16 28 us by row with the columns' largest magnitudes
-// (3.9), 4 to join those, 27 by column (4.9).  Rounding once cost twenty
-// instructions a value and was half of a row's time; now it takes five, and
-// looks again only next to a border (i8_bits).
+// (3.9), 4 to join those, 27 by column (4.9); any bf16 matrix of that size by
+// column 12 for the largest magnitudes (5.5) and 21 to write it (4.8), 16384 x 16384
+// 128 (4.2) and 175 (4.6).  Rounding once cost twenty instructions a value and was
+// half of a row's time; now it takes five, and looks again only next to a border
+// (i8_bits).
 #include "i8.h"
 
 namespace sgemm {
@@ -119,9 +121,11 @@ __global__ __launch_bounds__(256) void i8_part_kernel(I8ColsJob j) {
 template <int TYPE, int PIECES, int ROWS>
 __global__ __launch_bounds__(256) void i8_cols_kernel(I8ColsJob j, int parts) {
     typedef typename MxType<TYPE>::T E;
-    // The bytes of a column, in quads of four words: quad q at q ^ (column / 8),
-    // so that the 16 columns that a row of lanes writes at a time lie in
-    // different banks.
+    // The bytes of a column, in quads of four words: quad q at q ^ (column / 8).
+    // The 16 columns that a wave writes at a time, whose rows begin at the same
+    // bank, so take QUADS different quads: two to a bank with 128 rows, four with
+    // 64.  (Conflicts are 61 to 66% of the cycles in which LDS is busy, those a
+    // quarter to a third of the kernel's.)
     constexpr int WORDS = ROWS / 4, QUADS = ROWS / 16;
     __shared__ __attribute__((aligned(16))) uint32_t tile[PIECES][128][WORDS];
     const auto word = [](int column, int at) { return (((at >> 2) ^ (column >> 3)) & (QUADS - 1)) * 4 + (at & 3); };

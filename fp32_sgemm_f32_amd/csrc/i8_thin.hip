@@ -147,7 +147,10 @@ __global__ __launch_bounds__(kThreads, 4) void i8_thin_kernel(Args g) {
             if (next < g.blocks) load(b[u], next);
         }
     }
-    // Sums of the waves that share rows, and of the two halves of a block.
+    // Sums of the waves that share rows, and of the two halves of a block.  (A
+    // lane reads one row's, and those of neighbouring rows lie 16 or 64 words apart:
+    // with one token and 4096 columns 48 of a workgroup's 112 conflict cycles.  LDS
+    // is busy in 4% of the kernel's cycles, conflicts in 19% of those.)
     __syncthreads();
     int *red = (int *)lds;    // [set][kw][G][row parity][lane]
     {
