@@ -523,7 +523,8 @@ int sgemm_f32_mx4_moe_scratch(int tokens, int hidden, int inner, int experts, in
  * s = max(m / 127 rounded to a float, 2^-126), and x is held as the whole
  * number nearest to x / s (the exact quotient), of two equally near the even
  * one.  A row or group that holds a NaN or an infinity has the scale NaN and
- * values 0: whatever it enters becomes NaN.
+ * values 0: whatever it enters becomes NaN.  (127 s can round to more than m:
+ * where m is the largest float, and there alone, value * scale is infinite.)
  *
  * The products' sums are exact: 32-bit integers, which is why a sum is at
  * most SGEMM_I8_MAX_SUM long.  A sum becomes a float, is multiplied by the
