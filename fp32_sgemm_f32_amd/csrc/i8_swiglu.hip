@@ -8,8 +8,8 @@
 // rounded once.
 //
 // Bound by HBM: a lane takes eight columns of G and the same of U, so that
-// every value is read and written once (8192 x 14336 bf16: 0.95 GB each way in 191
-// us, 5.0 TB/s, and 191).
+// every value is read and written once (8192 x 14336 bf16: 0.95 GB each way in 192
+// us, 4.9 TB/s, and 194).
 #include "i8.h"
 
 namespace sgemm {
@@ -20,7 +20,8 @@ namespace {
 // gates, 1 + exp(g) = 1, are taken in 64 bits from the square of exp(g / 2).
 // What a lane knows of its gates' magnitudes says whether to look for them, which
 // it does behind its stores, writing again: hardly any does, and before the stores
-// the others take 3% longer (8192 x 14336 bf16; so 232 and 204 us, with and without).
+// the others take 3% longer (8192 x 14336 and 4096 x 4096 bf16; so no longer than
+// without).
 constexpr float kFarGate = -87.0f;
 __device__ __forceinline__ double i8_far_gate(float g) {
     const double e = expf(0.5f * g);
