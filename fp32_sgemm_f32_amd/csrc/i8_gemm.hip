@@ -27,7 +27,7 @@
 // KS-th chunk, and the first adds up the sums.
 //
 // Bound, where tiles are large, by the power the chip may draw: 16384^3 runs in
-// 3470 to 3700 us on different chips (2.4 to 2.5 POPS; the library's product of the
+// 3420 to 3700 us on different chips (2.4 to 2.6 POPS; the library's product of the
 // same type, 8192^3, at 2.1), at 1.6 GHz with the matrix pipes busy in 76% of the
 // cycles; on zeros, which draw less, in 2850 to 2900 (3.1), at 2.4 GHz and 61%.  The
 // waves wait (for memory, at barriers) in 32% of their cycles, on zeros in 44%.

@@ -122,3 +122,38 @@ def test_scales_without_columns_in_a_graph(dev):
         graph.replay()
         torch.cuda.synchronize()
         assert scales.eq(2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("inner", [1, 13, 130])
+def test_swiglu_far_gates_of_ragged_strided_rows(dev, dtype, inner):
+    """Far gates beside near ones, at the end of rows that lie apart: nothing between the rows is written."""
+    rows, rng = 5, np.random.default_rng(41)
+    g = np.where(rng.random((rows, inner)) < 0.5, -95.0 - 8 * rng.random((rows, inner)), rng.standard_normal((rows, inner)))
+    g[:, -1] = -100.0
+    x = torch.from_numpy(np.concatenate((g, np.full_like(g, 2.0 ** 100)), 1)).to(dtype).to(dev)
+    d = torch.from_numpy(rng.standard_normal((rows, inner)) * 2.0 ** -20).to(dtype).to(dev)
+
+    def apart(cols):
+        return torch.full((rows, cols + 3), float("nan"), dtype=dtype, device=dev)[:, 1:1 + cols]
+
+    h, out = apart(inner), apart(2 * inner)
+    _, saved = sg.i8_swiglu_forward(x, out=h)
+    sg.i8_swiglu_backward(d, saved, out=out)
+    for t in (h, out):
+        assert int(t._base.isnan().sum()) == 3 * rows
+    f = torch.finfo(dtype)
+
+    def near(got, want, bound):
+        lim = bound + np.maximum((np.abs(want) + bound) * (f.eps / 2), f.smallest_normal * f.eps / 2)
+        assert (np.abs(host(got) - want) <= lim).all()
+
+    G, V, D = host(x)[:, :inner], host(x)[:, inner:], host(d)
+    want = ref.gated(G, V)
+    near(h, want, 7 * U * np.abs(want) + 2.0 ** -149)
+    G, V = (ref.values(host(q.values), host(q.scales), inner).astype(np.float64) for q in saved)
+    dg, du = ref.gated_backward(D, G, V)
+    p = ref.sigmoid(G)
+    near(out[:, :inner], dg, 14 * U * np.abs(D * V * p) * (1.0 + np.abs(G) * ref.sigmoid(-G)) + 2.0 ** -148)
+    near(out[:, inner:], du, 8 * U * np.abs(du) + 2.0 ** -148)
+    assert (np.abs(dg[:, -1]) > 2.0 ** -126).all() and (np.abs(want[:, -1]) > 2.0 ** -126).all()
